@@ -12,6 +12,8 @@
  * and two routes onto them: (2n-2):2n lifted into overlapping 2:4 windows
  * ("SlideSparse", abstract) and a Reverse Cuthill-McKee permutation before
  * BCSR ("SMaT", abstract).  SDDMM samples a dense product at a CSR pattern.
+ * One-hot matrices (tokens by expert, tokens by vocabulary row) are stored by
+ * their sorted rows (spmm_route_t) and multiplied by the one-hot operators.
  *
  * Conventions shared by every entry point
  *   - All matrix pointers are DEVICE pointers owned by the caller.  The library
@@ -72,7 +74,8 @@ typedef enum {
  * E5M2: exponent bias 15, IEEE-style infinities and NaN), the FP8 that the
  * pages pair with 2:4 sparse tensor cores ("Spense", abstract, on the "sparse
  * FP4 GEMM" search page: B200 with FP8 precision). */
-typedef enum { SPMM_BF16 = 0, SPMM_F16 = 1, SPMM_I8 = 2, SPMM_E4M3 = 3, SPMM_E5M2 = 4 } spmm_dtype;
+/* SPMM_F32: rows of the one-hot operators only (spmm_dispatch and below). */
+typedef enum { SPMM_BF16 = 0, SPMM_F16 = 1, SPMM_I8 = 2, SPMM_E4M3 = 3, SPMM_E5M2 = 4, SPMM_F32 = 5 } spmm_dtype;
 
 /* Bits of the sticky device error word. */
 #define SPMM_DEVERR_TIMEOUT 1 /* a bounded pipeline wait gave up                        */
@@ -191,6 +194,23 @@ typedef struct {
     uint8_t *meta;
 } spmm_tvw_t;
 
+/* One-hot rows, stored by their sorted order.  ids[T][k] are integers (experts
+ * of a token, or its vocabulary row with k = 1); flat index f = t k + j, R = T k.
+ * A choice with an id in [0, n_keys) is kept, any other is dropped.
+ *   order[R]            flat indices sorted stably by id, dropped ones last
+ *   pos[R]              place of flat index f in order; -1 if dropped
+ *   offsets[n_keys + 1] first place of each key; offsets[n_keys] = kept choices
+ * It stands for the R x T matrix P with P[p][order[p] / k] = 1 for p <
+ * offsets[n_keys] and zero rows after. */
+typedef struct {
+    int64_t T;
+    int32_t k;
+    int64_t n_keys;
+    int32_t *order;   /* [T k]        */
+    int32_t *pos;     /* [T k]        */
+    int32_t *offsets; /* [n_keys + 1] */
+} spmm_route_t;
+
 /* ---------------------------------------------------------------- utilities */
 
 SPMM_API const char *spmm_status_string(spmm_status s);
@@ -215,6 +235,9 @@ SPMM_API spmm_status spmm_selftest_timeout(uint64_t timeout_ns, spmm_stream_t st
 #define SPMM_KERNEL_PRUNE 5   /* dense -> 2:4 magnitude pruning                    */
 #define SPMM_KERNEL_PERMUTE 6 /* row gather / scatter (permuted BCSR product)      */
 #define SPMM_KERNEL_SDDMM 7   /* sampled dense-dense product                       */
+#define SPMM_KERNEL_ROUTE 8   /* sort of tokens by key (route builder)             */
+#define SPMM_KERNEL_ROWS 9    /* rows moved or summed through a route or by id     */
+#define SPMM_KERNEL_EXPERTS 10 /* the experts' products                            */
 /* Turns tracing on (clearing earlier records) or off. */
 SPMM_API spmm_status spmm_trace_enable(int32_t on);
 /* Synchronises the traced events and reports launches and total milliseconds
@@ -459,6 +482,79 @@ SPMM_API spmm_status spmm_bcsr_permuted_workspace_size(const spmm_bcsr_t *A, int
 SPMM_API spmm_status spmm_bcsr_permuted(const spmm_bcsr_t *A, const int32_t *perm, const void *B, int64_t ldb,
                                         float *C, int64_t ldc, int64_t N, void *workspace, size_t workspace_bytes,
                                         spmm_stream_t stream);
+
+/* ---------------------------------------------------------------- one-hot operators
+ * Products with one-hot sparse matrices, the sparse operands of a mixture of
+ * experts and of an embedding table.  Rows are bf16, fp16 or fp32 (the experts'
+ * products: bf16 or fp16), row-major with a pitch in elements of at least the row
+ * length; sums are fp32 and rounded once (to nearest even).  Row pointers need
+ * only their element's alignment except where stated; rows whose base, pitch and
+ * length are multiples of 16 bytes move in 16-byte pieces.  Every call is
+ * asynchronous on `stream` and gives the same bits on every run.  A shape with
+ * nothing to write returns SPMM_OK without launching.  A dimension of 2^31 or
+ * more, or T k >= 2^31, -> SPMM_ERR_UNSUPPORTED (row offsets are 64-bit). */
+
+/* Workspace bytes spmm_build_route needs (0 when n_keys < 512). */
+SPMM_API spmm_status spmm_build_route_workspace_size(int64_t T, int32_t k, int64_t n_keys, size_t *bytes);
+/* Sorts ids[T][k] (device, id_bytes 4 or 8 per signed id, row pitch ldi) into
+ * R->order, R->pos and R->offsets (device arrays of the caller; R->T, R->k and
+ * R->n_keys are inputs).  Negative ids are dropped choices; an id >= n_keys is
+ * dropped as well and sets SPMM_DEVERR_INDEX.  Equal ids keep their flat order. */
+SPMM_API spmm_status spmm_build_route(const void *ids, int32_t id_bytes, int64_t ldi, const spmm_route_t *R,
+                                      void *workspace, size_t workspace_bytes, spmm_stream_t stream);
+
+/* xs = P x: xs[p] = x[order[p] / k] for the kept places, zero rows after them.
+ * x is T x H, xs is T k x H. */
+SPMM_API spmm_status spmm_dispatch(const spmm_route_t *R, const void *x, int64_t ldx, void *xs, int64_t ldxs,
+                                   int64_t H, int32_t dtype, spmm_stream_t stream);
+/* y = P^T diag(w) ys: y[t] = sum_j w[t][j] ys[pos[t][j]] over the kept choices of
+ * token t (a token without any gets zeros), j ascending.  w is T x k fp32,
+ * contiguous; null means weights of 1, which is the gradient of spmm_dispatch
+ * (dx from dxs). */
+SPMM_API spmm_status spmm_combine(const spmm_route_t *R, const void *ys, int64_t ldys, const float *w, void *y,
+                                  int64_t ldy, int64_t H, int32_t dtype, spmm_stream_t stream);
+/* Gradients of spmm_combine: dys[pos[t][j]] = w[t][j] dy[t] (zero rows past the
+ * kept places) and dw[t][j] = <dy[t], ys[pos[t][j]]> (0 for a dropped choice). */
+SPMM_API spmm_status spmm_combine_grad(const spmm_route_t *R, const void *dy, int64_t lddy, const void *ys,
+                                       int64_t ldys, const float *w, void *dys, int64_t lddys, float *dw, int64_t H,
+                                       int32_t dtype, spmm_stream_t stream);
+
+/* out[t] = scale * table[ids[t]] for T contiguous ids (id_bytes 4 or 8); a
+ * negative id (padding) gives a zero row, an id >= V as well and sets
+ * SPMM_DEVERR_INDEX.  table is V x H, out is T x H of the same type. */
+SPMM_API spmm_status spmm_embed(const void *table, int64_t V, int64_t H, int64_t ldt, int32_t dtype, const void *ids,
+                                int32_t id_bytes, int64_t T, float scale, void *out, int64_t ldo,
+                                spmm_stream_t stream);
+/* Workspace bytes spmm_embed_grad needs. */
+SPMM_API spmm_status spmm_embed_grad_workspace_size(const spmm_route_t *R, int64_t H, size_t *bytes);
+/* Gradient of spmm_embed for the table: dtable[v] = scale * sum of dy[t] over the
+ * tokens with id v, for the route R of the ids (R->k == 1, R->n_keys = V).
+ * accumulate = 0 writes every row (zeros for a row without tokens); accumulate =
+ * 1 adds to the rows that have tokens and leaves the others alone.  dtable is
+ * V x H of dy's type or fp32 (out_dtype). */
+SPMM_API spmm_status spmm_embed_grad(const spmm_route_t *R, const void *dy, int64_t lddy, int64_t H, int32_t dtype,
+                                     float scale, int32_t accumulate, void *dtable, int64_t ldt, int32_t out_dtype,
+                                     void *workspace, size_t workspace_bytes, spmm_stream_t stream);
+
+/* The experts' products on rows sorted by expert (R->n_keys experts, places
+ * offsets[e] .. offsets[e + 1] - 1 belong to expert e).  W[e] is N x K, row pitch
+ * ldw, expert pitch lde elements.  bf16 or fp16.  K, N and every pitch multiples
+ * of 8 and every pointer 16-byte aligned (TMA), else SPMM_ERR_SHAPE; at most
+ * 65535 experts.
+ *   spmm_experts     ys[p]  = W[e] xs[p]            ys  T k x N, xs T k x K
+ *   spmm_experts_dx  dxs[p] = W[e]^T dys[p]
+ *   spmm_experts_dw  dW[e]  = sum_p dys[p] xs[p]^T  (zeros for an unused expert)
+ * Rows past the kept places are written as zeros and, as inputs, never read into
+ * a result. */
+SPMM_API spmm_status spmm_experts(const spmm_route_t *R, const void *xs, int64_t ldx, const void *W, int64_t ldw,
+                                  int64_t lde, int64_t N, int64_t K, int32_t dtype, void *ys, int64_t ldy,
+                                  spmm_stream_t stream);
+SPMM_API spmm_status spmm_experts_dx(const spmm_route_t *R, const void *dys, int64_t ldy, const void *W, int64_t ldw,
+                                     int64_t lde, int64_t N, int64_t K, int32_t dtype, void *dxs, int64_t ldx,
+                                     spmm_stream_t stream);
+SPMM_API spmm_status spmm_experts_dw(const spmm_route_t *R, const void *dys, int64_t ldy, const void *xs, int64_t ldx,
+                                     int64_t N, int64_t K, int32_t dtype, void *dW, int64_t ldw, int64_t lde,
+                                     spmm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,11 +13,15 @@ Format containers hold device tensors:
   TVW(M, K, tile_rows, dtype, n_tiles, Kp, tile_ptr, cols, vals, meta)
   CSR(M, K, nnz, dtype, row_ptr, col, val)
   WCSR(...)  (see include/spmm_gb300.h for the field meanings)
+  Route(T, k, n_keys, order, pos, offsets)   (one-hot rows sorted by key)
 
 Beyond C = A B for those formats: spmm_slide ((2n-2):2n as overlapping 2:4
 windows), spmm_bcsr_permuted (BCSR after a Reverse Cuthill-McKee order from
 rcm_order), spmm_sddmm (A B sampled at a CSR pattern) and the pruning
-builders spmm_prune_24 / spmm_prune_tvw.
+builders spmm_prune_24 / spmm_prune_tvw.  One-hot operators (tokens by expert or
+by vocabulary row): spmm_build_route, spmm_dispatch, spmm_combine and their
+gradients, spmm_embed and spmm_embed_grad, and the experts' products
+spmm_experts / spmm_experts_dx / spmm_experts_dw between them.
 """
 from __future__ import annotations
 
@@ -36,6 +40,9 @@ __all__ = ["BCSR", "Mat24", "Slide", "TVW", "CSR", "WCSR", "SpmmError", "spmm_bc
            "spmm_build_wcsr_fill", "build_wcsr", "spmm_wcsr", "spmm_wcsr_workspace_size",
            "spmm_build_slide", "spmm_slide", "spmm_slide_workspace_size",
            "spmm_sddmm", "rcm_order", "spmm_permute_sym", "spmm_permute_rows", "spmm_bcsr_permuted", "spmm_bcsr_permuted_workspace_size",
+           "Route", "spmm_build_route", "spmm_build_route_workspace_size", "spmm_dispatch", "spmm_dispatch_grad",
+           "spmm_combine", "spmm_combine_grad", "spmm_embed", "spmm_embed_grad", "spmm_embed_grad_workspace_size",
+           "spmm_experts", "spmm_experts_dx", "spmm_experts_dw", "spmm_experts_grad",
            "last_device_error", "selftest_timeout", "library_path", "trace_enable", "trace_read"]
 
 _DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.int8: _lib.SPMM_I8,
@@ -513,3 +520,267 @@ def spmm_wcsr(A: WCSR, B: torch.Tensor, C_: Optional[torch.Tensor] = None,
     _lib.call("spmm_wcsr", C.byref(a), _ptr(B), B.stride(0), _ptr(out), out.stride(0), N, _ptr(workspace),
               workspace.numel(), _stream(stream))
     return out
+
+
+# ------------------------------------------------------------------ one-hot operators
+_ROW_DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.float32: _lib.SPMM_F32}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+@dataclass
+class Route:
+    """T x k ids sorted by value: order (flat indices, dropped ones last), pos
+    (place of each flat index, -1 if dropped) and offsets (first place per key).
+    All int32 on the device; pos has the ids' shape."""
+    T: int
+    k: int
+    n_keys: int
+    order: torch.Tensor
+    pos: torch.Tensor
+    offsets: torch.Tensor
+
+    @property
+    def n_rows(self) -> int:
+        return self.T * self.k
+
+    def c(self) -> _lib.RouteT:
+        return _lib.RouteT(self.T, self.k, self.n_keys, _ptr(self.order), _ptr(self.pos), _ptr(self.offsets))
+
+
+def _row_code(dtype) -> int:
+    if dtype not in _ROW_DT:
+        raise TypeError(f"unsupported row dtype {dtype}")
+    return _ROW_DT[dtype]
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor whose memory belongs to the stream the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t: torch.Tensor, what: str, rows: int, H: int, dtype, device) -> int:
+    """Check a rows x H operand of the type on the device; returns its row pitch."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{what} must be on {device} (this library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != H:
+        raise ValueError(f"{what} must be {rows} x {H}, not {tuple(t.shape)}")
+    if H > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.stride(0) if rows > 1 else H
+
+
+def _weights(t: torch.Tensor, what: str, E: int, N: int, K: int, dtype, device):
+    """Check an E x N x K operand; returns its row and expert pitches."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{what} must be on {device} (this library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape) != (E, N, K):
+        raise ValueError(f"{what} must be {E} x {N} x {K}, not {tuple(t.shape)}")
+    if K > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    ldw = t.stride(1) if N > 1 else K
+    return ldw, (t.stride(0) if E > 1 else N * ldw)
+
+
+def _route_w(R: Route, w: torch.Tensor, device) -> None:
+    if w.device != device or w.dtype != torch.float32:
+        raise TypeError(f"w must be float32 on {device}")
+    if w.numel() != R.n_rows or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {R.T} x {R.k} tensor")
+
+
+def spmm_build_route_workspace_size(T: int, k: int, n_keys: int) -> int:
+    n = C.c_size_t(0)
+    _lib.call("spmm_build_route_workspace_size", T, k, n_keys, C.byref(n))
+    return n.value
+
+
+def spmm_build_route(ids: torch.Tensor, n_keys: int, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> Route:
+    """Sort ids (T, or T x k; int32 or int64) by value.  Negative ids are dropped
+    choices; ids >= n_keys are dropped too and set SPMM_DEVERR_INDEX."""
+    _check_dev(ids, workspace)
+    if ids.dtype not in _ID_BYTES:
+        raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be T or T x k")
+    T, k = ids.shape[0], (1 if ids.dim() == 1 else ids.shape[1])
+    if ids.dim() == 2 and k > 1 and T > 0 and ids.stride(1) != 1:
+        raise ValueError("ids must have contiguous rows")
+    dev = ids.device
+    need = 0 if n_keys < 512 else spmm_build_route_workspace_size(T, k, n_keys)
+    if workspace is None and need:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    R = Route(T, k, n_keys, _empty(T * k, torch.int32, dev, stream), _empty(ids.shape, torch.int32, dev, stream),
+              _empty(max(n_keys, 0) + 1, torch.int32, dev, stream))
+    r = R.c()
+    _lib.call("spmm_build_route", _ptr(ids), _ID_BYTES[ids.dtype], ids.stride(0) if T > 1 else k, C.byref(r),
+              _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+              _stream(stream))
+    return R
+
+
+def spmm_dispatch(R: Route, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """xs[p] = x[order[p] // k] for the kept places, zero rows after them."""
+    H, dev = x.shape[-1], R.order.device
+    ldx = _rows(x, "x", R.T, H, x.dtype, dev)
+    code = _row_code(x.dtype)
+    if out is None:
+        out = _empty((R.n_rows, H), x.dtype, dev, stream)
+    ldo = _rows(out, "out", R.n_rows, H, x.dtype, dev)
+    r = R.c()
+    _lib.call("spmm_dispatch", C.byref(r), _ptr(x), ldx, _ptr(out), ldo, H, code, _stream(stream))
+    return out
+
+
+def spmm_combine(R: Route, ys: torch.Tensor, w: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """y[t] = sum_j w[t, j] ys[pos[t, j]] over the kept choices (w fp32; None: weights of 1)."""
+    H, dev = ys.shape[-1], R.order.device
+    ldys = _rows(ys, "ys", R.n_rows, H, ys.dtype, dev)
+    code = _row_code(ys.dtype)
+    if w is not None:
+        _route_w(R, w, dev)
+    if out is None:
+        out = _empty((R.T, H), ys.dtype, dev, stream)
+    ldo = _rows(out, "out", R.T, H, ys.dtype, dev)
+    r = R.c()
+    _lib.call("spmm_combine", C.byref(r), _ptr(ys), ldys, _ptr(w), _ptr(out), ldo, H, code, _stream(stream))
+    return out
+
+
+def spmm_dispatch_grad(R: Route, dxs: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of spmm_dispatch: dx[t] = sum_j dxs[pos[t, j]] (spmm_combine with weights of 1)."""
+    return spmm_combine(R, dxs, None, out, stream)
+
+
+def spmm_combine_grad(R: Route, dy: torch.Tensor, ys: torch.Tensor, w: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of spmm_combine: (dys, dw) with dys[pos[t, j]] = w[t, j] dy[t] (zero
+    rows past the kept places) and dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32, of w's shape."""
+    H, dev = dy.shape[-1], R.order.device
+    lddy = _rows(dy, "dy", R.T, H, dy.dtype, dev)
+    ldys = _rows(ys, "ys", R.n_rows, H, dy.dtype, dev)
+    code = _row_code(dy.dtype)
+    _route_w(R, w, dev)
+    if out is None:
+        out = _empty((R.n_rows, H), dy.dtype, dev, stream)
+    ldo = _rows(out, "out", R.n_rows, H, dy.dtype, dev)
+    dw = _empty(w.shape, torch.float32, dev, stream)
+    r = R.c()
+    _lib.call("spmm_combine_grad", C.byref(r), _ptr(dy), lddy, _ptr(ys), ldys, _ptr(w), _ptr(out), ldo, _ptr(dw), H,
+              code, _stream(stream))
+    return out, dw
+
+
+def spmm_embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """out[t] = scale * table[ids[t]]; a negative id (padding) gives a zero row, an id
+    past the table as well and sets SPMM_DEVERR_INDEX."""
+    V, H, dev = table.shape[0], table.shape[-1], table.device
+    ldt = _rows(table, "table", V, H, table.dtype, dev)
+    code = _row_code(table.dtype)
+    if ids.dtype not in _ID_BYTES:
+        raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
+    if ids.dim() != 1 or ids.device != dev or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous vector on {dev}")
+    T = ids.shape[0]
+    if out is None:
+        out = _empty((T, H), table.dtype, dev, stream)
+    ldo = _rows(out, "out", T, H, table.dtype, dev)
+    _lib.call("spmm_embed", _ptr(table), V, H, ldt, code, _ptr(ids), _ID_BYTES[ids.dtype], T, scale, _ptr(out), ldo,
+              _stream(stream))
+    return out
+
+
+def spmm_embed_grad_workspace_size(R: Route, H: int) -> int:
+    n = C.c_size_t(0)
+    r = R.c()
+    _lib.call("spmm_embed_grad_workspace_size", C.byref(r), H, C.byref(n))
+    return n.value
+
+
+def spmm_embed_grad(R: Route, dy: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                    accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of spmm_embed for the table, from the route of the ids (k = 1, n_keys
+    = V): scale * the sum of dy over each row's tokens.  Every row is written, or
+    with accumulate the sums are added to out.  out is dy's type (default) or fp32."""
+    H, dev = dy.shape[-1], R.order.device
+    lddy = _rows(dy, "dy", R.T, H, dy.dtype, dev)
+    code = _row_code(dy.dtype)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty((R.n_keys, H), dy.dtype, dev, stream)
+    ldo = _rows(out, "out", R.n_keys, H, out.dtype, dev)
+    need = spmm_embed_grad_workspace_size(R, H)
+    if workspace is None and need:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    r = R.c()
+    _lib.call("spmm_embed_grad", C.byref(r), _ptr(dy), lddy, H, code, scale, 1 if accumulate else 0, _ptr(out), ldo,
+              _row_code(out.dtype), _ptr(workspace),
+              0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    return out
+
+
+def spmm_experts(R: Route, xs: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """ys[p] = W[e] xs[p] for the rows p of expert e (W is E x N x K, R.n_keys = E);
+    zero rows past the kept places.  bf16 or fp16."""
+    dev, E = R.order.device, R.n_keys
+    N, K = W.shape[-2], W.shape[-1]
+    ldx = _rows(xs, "xs", R.n_rows, K, xs.dtype, dev)
+    ldw, lde = _weights(W, "W", E, N, K, xs.dtype, dev)
+    code = _row_code(xs.dtype)
+    if out is None:
+        out = _empty((R.n_rows, N), xs.dtype, dev, stream)
+    ldo = _rows(out, "out", R.n_rows, N, xs.dtype, dev)
+    r = R.c()
+    _lib.call("spmm_experts", C.byref(r), _ptr(xs), ldx, _ptr(W), ldw, lde, N, K, code, _ptr(out), ldo,
+              _stream(stream))
+    return out
+
+
+def spmm_experts_dx(R: Route, dys: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """dxs[p] = W[e]^T dys[p] for the rows p of expert e; zero rows past the kept places."""
+    dev, E = R.order.device, R.n_keys
+    N, K = W.shape[-2], W.shape[-1]
+    ldy = _rows(dys, "dys", R.n_rows, N, dys.dtype, dev)
+    ldw, lde = _weights(W, "W", E, N, K, dys.dtype, dev)
+    code = _row_code(dys.dtype)
+    if out is None:
+        out = _empty((R.n_rows, K), dys.dtype, dev, stream)
+    ldo = _rows(out, "out", R.n_rows, K, dys.dtype, dev)
+    r = R.c()
+    _lib.call("spmm_experts_dx", C.byref(r), _ptr(dys), ldy, _ptr(W), ldw, lde, N, K, code, _ptr(out), ldo,
+              _stream(stream))
+    return out
+
+
+def spmm_experts_dw(R: Route, dys: torch.Tensor, xs: torch.Tensor, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """dW[e] = sum of dys[p] xs[p]^T over the rows p of expert e (E x N x K; zeros for an unused expert)."""
+    dev, E = R.order.device, R.n_keys
+    N, K = dys.shape[-1], xs.shape[-1]
+    ldy = _rows(dys, "dys", R.n_rows, N, dys.dtype, dev)
+    ldx = _rows(xs, "xs", R.n_rows, K, dys.dtype, dev)
+    code = _row_code(dys.dtype)
+    if out is None:
+        out = _empty((E, N, K), dys.dtype, dev, stream)
+    ldw, lde = _weights(out, "out", E, N, K, dys.dtype, dev)
+    r = R.c()
+    _lib.call("spmm_experts_dw", C.byref(r), _ptr(dys), ldy, _ptr(xs), ldx, N, K, code, _ptr(out), ldw, lde,
+              _stream(stream))
+    return out
+
+
+def spmm_experts_grad(R: Route, dys: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, stream=None):
+    """Both gradients of spmm_experts: (dxs, dW)."""
+    return spmm_experts_dx(R, dys, W, stream=stream), spmm_experts_dw(R, dys, xs, stream=stream)

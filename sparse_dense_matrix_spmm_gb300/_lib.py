@@ -7,13 +7,14 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspmm_gb300.so")
 
-SPMM_BF16, SPMM_F16, SPMM_I8, SPMM_E4M3, SPMM_E5M2 = 0, 1, 2, 3, 4
+SPMM_BF16, SPMM_F16, SPMM_I8, SPMM_E4M3, SPMM_E5M2, SPMM_F32 = 0, 1, 2, 3, 4, 5
 DEVERR_TIMEOUT, DEVERR_INDEX, DEVERR_FORMAT = 1, 2, 4
 KERNEL_BCSR, KERNEL_SPARSE, KERNEL_WIDEN, KERNEL_WCSR, KERNEL_PRUNE, KERNEL_PERMUTE, KERNEL_SDDMM = 1, 2, 3, 4, 5, 6, 7
+KERNEL_ROUTE, KERNEL_ROWS, KERNEL_EXPERTS = 8, 9, 10
 STATUS = {0: "SPMM_OK", 1: "SPMM_ERR_NULL", 2: "SPMM_ERR_SHAPE", 3: "SPMM_ERR_DTYPE", 4: "SPMM_ERR_FORMAT",
           5: "SPMM_ERR_WORKSPACE", 6: "SPMM_ERR_TIMEOUT", 7: "SPMM_ERR_CUDA", 8: "SPMM_ERR_UNSUPPORTED"}
 
-P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+P, I32, I64, SZ, F32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
 
 
 class SpmmError(RuntimeError):
@@ -52,6 +53,10 @@ class TvwT(C.Structure):
                 ("tile_ptr", P), ("cols", P), ("vals", P), ("meta", P)]
 
 
+class RouteT(C.Structure):
+    _fields_ = [("T", I64), ("k", I32), ("n_keys", I64), ("order", P), ("pos", P), ("offsets", P)]
+
+
 # name -> (restype, argtypes); every function declared in include/spmm_gb300.h
 SIGNATURES = {
     "spmm_status_string": (C.c_char_p, [I32]),
@@ -86,6 +91,17 @@ SIGNATURES = {
     "spmm_permute_rows": (I32, [P, I64, P, I64, I64, I64, I32, P, I32, P]),
     "spmm_bcsr_permuted_workspace_size": (I32, [C.POINTER(BcsrT), I64, C.POINTER(SZ)]),
     "spmm_bcsr_permuted": (I32, [C.POINTER(BcsrT), P, P, I64, P, I64, I64, P, SZ, P]),
+    "spmm_build_route_workspace_size": (I32, [I64, I32, I64, C.POINTER(SZ)]),
+    "spmm_build_route": (I32, [P, I32, I64, C.POINTER(RouteT), P, SZ, P]),
+    "spmm_dispatch": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I32, P]),
+    "spmm_combine": (I32, [C.POINTER(RouteT), P, I64, P, P, I64, I64, I32, P]),
+    "spmm_combine_grad": (I32, [C.POINTER(RouteT), P, I64, P, I64, P, P, I64, P, I64, I32, P]),
+    "spmm_embed": (I32, [P, I64, I64, I64, I32, P, I32, I64, F32, P, I64, P]),
+    "spmm_embed_grad_workspace_size": (I32, [C.POINTER(RouteT), I64, C.POINTER(SZ)]),
+    "spmm_embed_grad": (I32, [C.POINTER(RouteT), P, I64, I64, I32, F32, I32, P, I64, I32, P, SZ, P]),
+    "spmm_experts": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, P, I64, P]),
+    "spmm_experts_dx": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, P, I64, P]),
+    "spmm_experts_dw": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I32, P, I64, I64, P]),
 }
 
 _lib = None

@@ -15,7 +15,7 @@ __device__ int g_device_error;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxKernelSlots = 32;
+constexpr int kMaxKernelSlots = 48;
 DeviceInfo g_info[kMaxDevices];
 bool g_info_ok[kMaxDevices];
 bool g_attr_done[kMaxDevices][kMaxKernelSlots];
@@ -603,4 +603,186 @@ spmm_status spmm_tvw(const spmm_tvw_t* A, const void* B, int64_t ldb, float* C, 
         return SPMM_ERR_UNSUPPORTED;
     return launch_tvw(A, B, ldb, C, ldc, N, reinterpret_cast<cudaStream_t>(stream));
 }
+// ---------------------------------------------------------------- one-hot operators
+
+namespace {
+constexpr int64_t kDimLimit = int64_t(1) << 31;
+
+// Sizes of a route; its arrays where `arrays` (not needed when nothing is written).
+spmm_status check_route(const spmm_route_t* R, bool arrays) {
+    if (!R) return SPMM_ERR_NULL;
+    if (R->T < 0 || R->k <= 0 || R->n_keys <= 0) return SPMM_ERR_SHAPE;
+    // both factors below 2^31 before their product is formed
+    if (R->T >= kDimLimit || R->n_keys >= kDimLimit - 1 || R->T * R->k >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (arrays && (!R->offsets || (R->T > 0 && (!R->order || !R->pos)))) return SPMM_ERR_NULL;
+    return SPMM_OK;
+}
+
+// A row-major operand of `rows` rows of H elements.
+bool bad_pitch(int64_t ld, int64_t H) { return ld < H || ld >= (int64_t(1) << 40); }
+bool misaligned(const void* p, int32_t dtype) {
+    return reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(row_elem_bytes(dtype)) != 0;
+}
+
+// Shapes of an experts' product: two row operands (pitches la, lb for rows of da
+// and db elements) and the weights or their gradient.
+spmm_status check_experts(const spmm_route_t* R, int64_t la, int64_t da, int64_t lb, int64_t db, int64_t ldw,
+                          int64_t lde, int64_t N, int64_t K, int32_t dtype) {
+    const spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (dtype != SPMM_BF16 && dtype != SPMM_F16) return SPMM_ERR_DTYPE;
+    if (N <= 0 || K <= 0 || N % 8 || K % 8) return SPMM_ERR_SHAPE;
+    if (N >= kDimLimit || K >= kDimLimit || R->n_keys > 65535) return SPMM_ERR_UNSUPPORTED;
+    if (bad_pitch(la, da) || bad_pitch(lb, db) || bad_pitch(ldw, K)) return SPMM_ERR_SHAPE;
+    if (la % 8 || lb % 8 || ldw % 8 || lde % 8) return SPMM_ERR_SHAPE;
+    // experts must not overlap: lde >= (N - 1) ldw + K, without forming the product
+    if (lde < K || lde >= (int64_t(1) << 40) || (lde - K) / ldw < N - 1) return SPMM_ERR_SHAPE;
+    return SPMM_OK;
+}
+}  // namespace
+
+spmm_status spmm_build_route_workspace_size(int64_t T, int32_t k, int64_t n_keys, size_t* bytes) {
+    if (!bytes) return SPMM_ERR_NULL;
+    const spmm_route_t R{T, k, n_keys, nullptr, nullptr, nullptr};
+    const spmm_status st = check_route(&R, false);
+    if (st != SPMM_OK) return st;
+    *bytes = route_workspace_bytes(T, k, n_keys);
+    return SPMM_OK;
+}
+
+spmm_status spmm_build_route(const void* ids, int32_t id_bytes, int64_t ldi, const spmm_route_t* R, void* workspace,
+                             size_t workspace_bytes, spmm_stream_t stream) {
+    const spmm_status st = check_route(R, true);
+    if (st != SPMM_OK) return st;
+    if (id_bytes != 4 && id_bytes != 8) return SPMM_ERR_DTYPE;
+    if (R->T > 0 && !ids) return SPMM_ERR_NULL;
+    if (bad_pitch(ldi, R->k) || reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes)) return SPMM_ERR_SHAPE;
+    const size_t need = route_workspace_bytes(R->T, R->k, R->n_keys);
+    if (need && (!workspace || workspace_bytes < need)) return SPMM_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 4) return SPMM_ERR_SHAPE;
+    return launch_build_route(ids, id_bytes, ldi, R, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_dispatch(const spmm_route_t* R, const void* x, int64_t ldx, void* xs, int64_t ldxs, int64_t H,
+                          int32_t dtype, spmm_stream_t stream) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
+    if (H < 0 || bad_pitch(ldx, H) || bad_pitch(ldxs, H)) return SPMM_ERR_SHAPE;
+    if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (R->T == 0 || H == 0) return SPMM_OK;
+    if ((st = check_route(R, true)) != SPMM_OK) return st;
+    if (!x || !xs) return SPMM_ERR_NULL;
+    if (misaligned(x, dtype) || misaligned(xs, dtype)) return SPMM_ERR_SHAPE;
+    return launch_dispatch(R, x, ldx, xs, ldxs, H, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_combine(const spmm_route_t* R, const void* ys, int64_t ldys, const float* w, void* y, int64_t ldy,
+                         int64_t H, int32_t dtype, spmm_stream_t stream) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
+    if (H < 0 || bad_pitch(ldys, H) || bad_pitch(ldy, H)) return SPMM_ERR_SHAPE;
+    if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (R->T == 0 || H == 0) return SPMM_OK;
+    if ((st = check_route(R, true)) != SPMM_OK) return st;
+    if (!ys || !y) return SPMM_ERR_NULL;
+    if (misaligned(ys, dtype) || misaligned(y, dtype) || misaligned(w, SPMM_F32)) return SPMM_ERR_SHAPE;
+    return launch_combine(R, ys, ldys, w, y, ldy, H, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_combine_grad(const spmm_route_t* R, const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                              const float* w, void* dys, int64_t lddys, float* dw, int64_t H, int32_t dtype,
+                              spmm_stream_t stream) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
+    if (H <= 0 || bad_pitch(lddy, H) || bad_pitch(ldys, H) || bad_pitch(lddys, H)) return SPMM_ERR_SHAPE;
+    if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (R->T == 0) return SPMM_OK;
+    if ((st = check_route(R, true)) != SPMM_OK) return st;
+    if (!dy || !ys || !w || !dys || !dw) return SPMM_ERR_NULL;
+    if (misaligned(dy, dtype) || misaligned(ys, dtype) || misaligned(dys, dtype) || misaligned(w, SPMM_F32) ||
+        misaligned(dw, SPMM_F32))
+        return SPMM_ERR_SHAPE;
+    return launch_combine_grad(R, dy, lddy, ys, ldys, w, dys, lddys, dw, H, dtype,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_embed(const void* table, int64_t V, int64_t H, int64_t ldt, int32_t dtype, const void* ids,
+                       int32_t id_bytes, int64_t T, float scale, void* out, int64_t ldo, spmm_stream_t stream) {
+    if (!dtype_row(dtype) || (id_bytes != 4 && id_bytes != 8)) return SPMM_ERR_DTYPE;
+    if (V <= 0 || H < 0 || T < 0 || bad_pitch(ldt, H) || bad_pitch(ldo, H)) return SPMM_ERR_SHAPE;
+    if (V >= kDimLimit || H >= kDimLimit || T >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return SPMM_OK;
+    if (!table || !ids || !out) return SPMM_ERR_NULL;
+    if (misaligned(table, dtype) || misaligned(out, dtype) ||
+        reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes))
+        return SPMM_ERR_SHAPE;
+    return launch_embed(table, V, H, ldt, dtype, ids, id_bytes, T, scale, out, ldo,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_embed_grad_workspace_size(const spmm_route_t* R, int64_t H, size_t* bytes) {
+    if (!bytes) return SPMM_ERR_NULL;
+    const spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (R->k != 1 || H < 0) return SPMM_ERR_SHAPE;
+    if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    *bytes = embed_grad_workspace_bytes(R->T, H);
+    return SPMM_OK;
+}
+
+spmm_status spmm_embed_grad(const spmm_route_t* R, const void* dy, int64_t lddy, int64_t H, int32_t dtype,
+                            float scale, int32_t accumulate, void* dtable, int64_t ldt, int32_t out_dtype,
+                            void* workspace, size_t workspace_bytes, spmm_stream_t stream) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype) || (out_dtype != dtype && out_dtype != SPMM_F32)) return SPMM_ERR_DTYPE;
+    if (R->k != 1 || H < 0 || bad_pitch(lddy, H) || bad_pitch(ldt, H) || (accumulate & ~1)) return SPMM_ERR_SHAPE;
+    if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (H == 0) return SPMM_OK;
+    if ((st = check_route(R, true)) != SPMM_OK) return st;
+    if (!dtable || (R->T > 0 && !dy)) return SPMM_ERR_NULL;
+    if (misaligned(dy, dtype) || misaligned(dtable, out_dtype)) return SPMM_ERR_SHAPE;
+    const size_t need = embed_grad_workspace_bytes(R->T, H);
+    if (need && (!workspace || workspace_bytes < need)) return SPMM_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SPMM_ERR_SHAPE;
+    return launch_embed_grad(R, dy, lddy, H, dtype, scale, accumulate != 0, dtable, ldt, out_dtype, workspace,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_experts(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw, int64_t lde,
+                         int64_t N, int64_t K, int32_t dtype, void* ys, int64_t ldy, spmm_stream_t stream) {
+    const spmm_status st = check_experts(R, ldx, K, ldy, N, ldw, lde, N, K, dtype);
+    if (st != SPMM_OK) return st;
+    if (R->T == 0) return SPMM_OK;
+    if (!R->offsets || !xs || !W || !ys) return SPMM_ERR_NULL;
+    if (!aligned16(xs) || !aligned16(W) || !aligned16(ys)) return SPMM_ERR_SHAPE;
+    return launch_experts_rows(R, xs, ldx, W, ldw, lde, N, K, false, dtype, ys, ldy,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_experts_dx(const spmm_route_t* R, const void* dys, int64_t ldy, const void* W, int64_t ldw,
+                            int64_t lde, int64_t N, int64_t K, int32_t dtype, void* dxs, int64_t ldx,
+                            spmm_stream_t stream) {
+    const spmm_status st = check_experts(R, ldy, N, ldx, K, ldw, lde, N, K, dtype);
+    if (st != SPMM_OK) return st;
+    if (R->T == 0) return SPMM_OK;
+    if (!R->offsets || !dys || !W || !dxs) return SPMM_ERR_NULL;
+    if (!aligned16(dys) || !aligned16(W) || !aligned16(dxs)) return SPMM_ERR_SHAPE;
+    return launch_experts_rows(R, dys, ldy, W, ldw, lde, N, K, true, dtype, dxs, ldx,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldy, const void* xs, int64_t ldx,
+                            int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde,
+                            spmm_stream_t stream) {
+    const spmm_status st = check_experts(R, ldy, N, ldx, K, ldw, lde, N, K, dtype);
+    if (st != SPMM_OK) return st;
+    if (!R->offsets || !dW || (R->T > 0 && (!dys || !xs))) return SPMM_ERR_NULL;
+    if (!aligned16(dys) || !aligned16(xs) || !aligned16(dW)) return SPMM_ERR_SHAPE;
+    return launch_experts_dw(R, dys, ldy, xs, ldx, N, K, dtype, dW, ldw, lde, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -60,6 +60,10 @@ spmm_status check_24_call(const spmm_24_t* A, const void* B, int64_t ldb, const 
 void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
+// Slots of set_smem_attr_once taken by the one-hot operators (0-23 belong to
+// the format kernels).
+enum : int { kSlotRouteSort = 24, kSlotExperts = 25 };
+
 // Raise a kernel's dynamic shared memory limit once per device.
 bool set_smem_attr_once(const void* kernel, int bytes, int slot);
 
@@ -117,5 +121,33 @@ spmm_status run_permute_sym(const void* dense, int64_t n, int64_t ld, int32_t dt
 size_t bcsr_permuted_ws_bytes(const spmm_bcsr_t* A, int64_t N);
 spmm_status launch_bcsr_permuted(const spmm_bcsr_t* A, const int32_t* perm, const void* B, int64_t ldb, float* C,
                                  int64_t ldc, int64_t N, void* ws, cudaStream_t s);
+
+
+// Row types of the one-hot operators: bf16, fp16, fp32.
+inline bool dtype_row(int32_t dtype) { return dtype == SPMM_BF16 || dtype == SPMM_F16 || dtype == SPMM_F32; }
+inline int row_elem_bytes(int32_t dtype) { return dtype == SPMM_F32 ? 4 : 2; }
+
+size_t route_workspace_bytes(int64_t T, int32_t k, int64_t n_keys);
+spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, const spmm_route_t* R, void* ws,
+                               cudaStream_t s);
+spmm_status launch_dispatch(const spmm_route_t* R, const void* x, int64_t ldx, void* xs, int64_t ldxs, int64_t H,
+                            int32_t dtype, cudaStream_t s);
+spmm_status launch_combine(const spmm_route_t* R, const void* ys, int64_t ldys, const float* w, void* y, int64_t ldy,
+                           int64_t H, int32_t dtype, cudaStream_t s);
+spmm_status launch_combine_grad(const spmm_route_t* R, const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                                const float* w, void* dys, int64_t lddys, float* dw, int64_t H, int32_t dtype,
+                                cudaStream_t s);
+spmm_status launch_embed(const void* table, int64_t V, int64_t H, int64_t ldt, int32_t dtype, const void* ids,
+                         int32_t id_bytes, int64_t T, float scale, void* out, int64_t ldo, cudaStream_t s);
+size_t embed_grad_workspace_bytes(int64_t T, int64_t H);
+spmm_status launch_embed_grad(const spmm_route_t* R, const void* dy, int64_t ldy, int64_t H, int32_t dtype, float scale,
+                              bool accumulate, void* out, int64_t ldo, int32_t out_dtype, void* ws, cudaStream_t s);
+// Row products of the experts: out[p] = W[e] rows[p] (N x K weights), or
+// W[e]^T rows[p] when `transposed`.
+spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t ldr, const void* W, int64_t ldw,
+                                int64_t lde, int64_t N, int64_t K, bool transposed, int32_t dtype, void* out,
+                                int64_t ldo, cudaStream_t s);
+spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
+                              int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s);
 
 }  // namespace spmm
