@@ -16,7 +16,7 @@
 // The sums are fp32 in TMEM, rounded once to the operands' type.
 //
 // Roles per CTA: warp 0 loads A, warp 1 loads B (TMA, 128-byte swizzle, one
-// ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-7
+// ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-11
 // store D (two accumulators of 256 TMEM columns, so a unit's epilogue overlaps
 // the next unit's MMAs), warp 3 writes the zero rows of dropped choices.  The
 // host knows no row counts: every role walks the work units by itself, 32
@@ -30,7 +30,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
+constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, 128 columns each
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzle row
 constexpr int kMaxTile = 256;    // columns of D per unit
 constexpr int kABytes = 128 * 128;
@@ -57,8 +58,21 @@ struct Unit {
 
 // Maps unit numbers to units.  Called by whole warps; unit numbers must not
 // decrease.  Row products: an expert with c rows has ceil(c / 256) row tiles of
-// nearly equal size times m_tiles units, row tiles fastest, so that units in
-// flight together share weights.  dw: m_tiles x n_tiles units per expert.
+// nearly equal size times m_tiles units; dw has n_tiles x m_tiles units per
+// expert.  Inside an expert units go in groups of kGroup column tiles, column
+// tiles fastest, so that the units in flight together (76 pairs) form a compact
+// patch of D and share their operands in L2: with column tiles fastest over the
+// whole of a 32768-row expert its rows came from HBM once per row tile of W.
+constexpr int kGroup = 8;
+
+// Tile i of m_tiles x n_tiles in that order.
+__device__ __forceinline__ void tile_of(int i, int m_tiles, int n_tiles, int& mt, int& nt) {
+    const int per = kGroup * m_tiles, g = i / per, rest = i - g * per;
+    const int width = min(kGroup, n_tiles - g * kGroup);
+    mt = rest / width;
+    nt = g * kGroup + rest - mt * width;
+}
+
 template <int CG, bool DW>
 struct Walk {
     const ExpertArgs& a;
@@ -82,11 +96,12 @@ struct Walk {
             const int per = a.m_tiles * a.n_tiles;
             if (u >= a.E * per) return false;
             w.e = u / per;
-            const int i = u - w.e * per, mt = i / a.n_tiles;
+            int mt, nt;
+            tile_of(u - w.e * per, a.m_tiles, a.n_tiles, mt, nt);
             w.p0 = __ldg(a.offsets + w.e);
             w.cnt = __ldg(a.offsets + w.e + 1) - w.p0;
             w.m0 = mt * 128 * CG;
-            w.n0 = (i - mt * a.n_tiles) * kMaxTile;
+            w.n0 = nt * kMaxTile;
             w.live = min(kMaxTile, a.n - w.n0);
             w.nt = (w.live + 16 * CG - 1) / (16 * CG) * (16 * CG);
             w.steps = (w.cnt + kDepth - 1) / kDepth;
@@ -106,7 +121,8 @@ struct Walk {
         w.cnt = __shfl_sync(0xffffffffu, cnt, l);
         const int tiles = (w.cnt + kMaxTile - 1) / kMaxTile;
         const int i = u - base - (__shfl_sync(0xffffffffu, incl, l) - tiles * a.m_tiles);
-        const int mt = i / tiles, nt = i - mt * tiles;
+        int mt, nt;
+        tile_of(i, a.m_tiles, tiles, mt, nt);
         const int size = ((w.cnt + tiles - 1) / tiles + 16 * CG - 1) / (16 * CG) * (16 * CG);
         w.m0 = mt * 128 * CG;
         w.n0 = nt * size;
@@ -122,40 +138,43 @@ struct Ring {
     static constexpr int kBBytes = kMaxTile / CG * 128;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = CG == 1 ? 4 : 6;
-    static constexpr int kBars = 2 * kStages + 5;
-    static constexpr int kSmem = 1024 + kStages * kStage + 4 * kStageOut + kBars * 8 + 16;
+    static constexpr int kBars = 4 * kStages + 5;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageOut + kBars * 8 + 16;
 };
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return rows::Pair<T>::pack(a, b);
+__device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
+    return rows::Pair<T>::pack(__uint_as_float(a), __uint_as_float(b));
 }
 
-// D columns [c, c + 32) of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void load32(uint32_t t, float (&v)[32]) {
-    uint32_t r0[16], r1[16];
-    tmem_ld16(t, r0);
-    tmem_ld16(t + 16, r1);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i] = __uint_as_float(r0[i]);
-        v[16 + i] = __uint_as_float(r1[i]);
-    }
-}
-
-// Row products: lane = feature, column = row of the expert.  Every column is
-// stored as 32 consecutive features by the warp.
+// Row products: TMEM lane = feature, column = row of the expert.  Blocks of 8
+// features x 8 rows are transposed on their way to shared memory (32 rows x 32
+// features, 16-byte units XOR-swizzled by row), so that each row leaves in
+// 16-byte pieces of consecutive features.
 template <typename T>
-__device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, uint32_t t, int feature) {
-    T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo + feature;
-    const bool in = feature < a.m;
-    for (int c = 0; c < w.live; c += 32) {
-        float v[32];
-        load32(t + c, v);
+__device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, uint32_t t, int c0, int c1, int row0,
+                                           int lane, uint32_t stage) {
+    T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo;
+    const int unit = lane & 3, feature = row0 + 8 * unit;
+    const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
+    for (int c = c0; c < c1; c += 32) {
+        uint32_t lo[16], hi[16];
+        tmem_ld_16x32(t + c, lo);
+        tmem_ld_16x32(t + (16u << 16) + c, hi);
+        tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (in && c + i < w.live) out[(c + i) * a.ldo] = rows::from_f32<T>(v[i]);
+        for (int b = 0; b < 4; ++b)  // rows 8 b .. 8 b + 7
+            stmatrix_x4_trans(put + b * 512, pack2<T>(lo[4 * b], lo[4 * b + 1]), pack2<T>(lo[4 * b + 2], lo[4 * b + 3]),
+                              pack2<T>(hi[4 * b], hi[4 * b + 1]), pack2<T>(hi[4 * b + 2], hi[4 * b + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 p = ld_shared_v4(stage + r * 64 + ((unit ^ ((r >> 1) & 3)) << 4));
+            // features come in groups of 8 (N % 8 == 0), so a group is stored whole or not at all
+            if (feature < a.m && c + r < c1) *reinterpret_cast<uint4*>(out + (c + r) * a.ldo + feature) = p;
+        }
+        __syncwarp();
     }
 }
 
@@ -163,45 +182,87 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, u
 // are staged in shared memory (16-byte units XOR-swizzled by row) and leave as
 // 128-byte row segments.
 template <typename T>
-__device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uint32_t t, bool zero, int row0, int lane,
-                                         uint32_t stage) {
+__device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uint32_t t, int c0, int c1, int row0,
+                                         int lane, uint32_t stage) {
     T* out = static_cast<T*>(a.out) + w.e * a.lde + w.n0;
-    for (int c = 0; c < w.live; c += 64) {
+    for (int c = c0; c < c1; c += 64) {
+        uint32_t v[4][16];
+        if (w.steps == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            if (zero) {
+            for (int h = 0; h < 4; ++h)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            } else {
-                load32(t + c + 32 * h, v);
-            }
+                for (int i = 0; i < 16; ++i) v[h][i] = 0u;
+        } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint4 p;
-                p.x = pack2<T>(v[8 * u], v[8 * u + 1]);
-                p.y = pack2<T>(v[8 * u + 2], v[8 * u + 3]);
-                p.z = pack2<T>(v[8 * u + 4], v[8 * u + 5]);
-                p.w = pack2<T>(v[8 * u + 6], v[8 * u + 7]);
-                st_shared_v4(stage + lane * 128 + (((4 * h + u) ^ (lane & 7)) << 4), p);
-            }
+            for (int h = 0; h < 4; ++h) tmem_ld16(t + c + 16 * h, v[h]);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t* f = &v[u >> 1][8 * (u & 1)];
+            st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4),
+                         make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
+                                    pack2<T>(f[6], f[7])));
         }
         __syncwarp();
         const int u = lane & 7;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3);
-            uint4 p;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(p.x), "=r"(p.y), "=r"(p.z), "=r"(p.w)
-                         : "r"(stage + r * 128 + ((u ^ (r & 7)) << 4))
-                         : "memory");
+            const uint4 p = ld_shared_v4(stage + r * 128 + ((u ^ (r & 7)) << 4));
             // columns come in groups of 8 (K % 8 == 0), so a group is stored whole or not at all
-            if (row0 + r < a.m && c + 8 * u < w.live)
+            if (row0 + r < a.m && c + 8 * u < c1)
                 *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * a.ldo + c + 8 * u) = p;
         }
         __syncwarp();
     }
+}
+
+// dw: rows [valid, end) of a stage's chunks (64 columns each, 64 rows of 128
+// bytes) become zero.  Called by a whole warp.
+__device__ __forceinline__ void clear_tail(uint32_t stage, int valid, int end, int chunks, int lane) {
+    for (int c = 0; c < chunks; ++c)
+        for (int i = lane; i < (end - valid) * 8; i += 32)
+            st_shared_v4(stage + c * 8192 + valid * 128 + i * 16, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// One CTA (CG = 1) or a pair (CG = 2) per MMA.
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if (CG == 2)
+        mma_f16_pair(d, ad, bd, idesc, acc);
+    else
+        mma_f16(d, ad, bd, idesc, acc);
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 2)
+        mma_commit_pair(bar);
+    else
+        mma_commit(bar);
+}
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+    if (CG == 2)
+        tma_load_2d_pair(dst, m, bar, c0, c1);
+    else
+        tma_load_2d(dst, m, bar, c0, c1);
+}
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+    if (CG == 2)
+        tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+    else
+        tma_load_3d(dst, m, bar, c0, c1, c2);
+}
+template <int CG>
+__device__ __forceinline__ void sync_all() {
+    if (CG == 2)
+        cluster_sync_all();
+    else
+        __syncthreads();
 }
 
 // AMN / BMN: the operand's contiguous direction is D's row / column (else the
@@ -216,24 +277,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     const uint32_t out0 = s0 + G::kStages * G::kStage;
-    const uint32_t bar0 = out0 + 4 * kStageOut;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + G::kStages * G::kStage + 4 * kStageOut + 8 * G::kBars);
+    const uint32_t bar0 = out0 + kEpiWarps * kStageOut;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + G::kStages * G::kStage + kEpiWarps * kStageOut + 8 * G::kBars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (G::kStages + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * G::kStages + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * G::kStages + 2 + b); };
     const uint32_t done_bar = bar0 + 8u * (2 * G::kStages + 4);
+    auto tail_bar = [&](int s) { return done_bar + 8u + 8u * s; };
+    auto zeroed_bar = [&](int s) { return done_bar + 8u + 8u * (G::kStages + s); };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int group = blockIdx.x, groups = gridDim.x;
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(full_bar(s), 2);
             mbar_init(empty_bar(s), 1);
+            mbar_init(tail_bar(s), 2);
+            mbar_init(zeroed_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), 4);
+            mbar_init(acce_bar(b), kEpiWarps * CG);
         }
         mbar_init(done_bar, 1);
         fence_mbar_init();
@@ -241,11 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) tma_prefetch_desc(&tmA);
     if (warp == 1 && lane == 0) tma_prefetch_desc(&tmB);
     if (warp == 2) {
-        tmem_alloc(smem_u32(tslot), 512);
-        tmem_relinquish();
+        if (CG == 2) {
+            tmem_alloc_pair(smem_u32(tslot), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tslot), 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    sync_all<CG>();
     tc_fence_after();
     const uint32_t tmem = *tslot;
     Walk<CG, DW> walk(a, lane);
@@ -257,39 +328,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         bool ok = true;
         for (int u = group; ok && walk.find(u, w); u += groups) {
-            const int nb = w.nt / CG;
+            const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank;
             for (int k = 0; k < w.steps; ++k) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) {
-                    const uint32_t st = s0 + s * G::kStage, bar = full_bar(s);
+                    const uint32_t st = s0 + s * G::kStage;
                     const int d0 = k * kDepth;
+                    // A pair's loads all complete on rank 0's barrier, which expects both CTAs' bytes.  A
+                    // dw tail that rank 1 has to clear first completes on rank 1's own barrier instead.
+                    const bool tail = CG == 2 && DW && ((w.cnt - d0) & 15) && w.cnt - d0 < kDepth;
+                    const uint32_t arrive_bar = tail && rank ? tail_bar(s) : full_bar(s);  // of this CTA
+                    const uint32_t bar = CG == 1 || tail ? arrive_bar : map_shared(arrive_bar, 0);
+                    const uint32_t both = tail ? 1 : CG;
+                    const bool arrives = rank == 0 || tail;
                     if (warp == 0) {
-                        mbar_arrive_expect_tx(bar, kABytes);
+                        if (arrives) mbar_arrive_expect_tx(arrive_bar, kABytes * both);
                         if (DW) {
-                            tma_load_2d(st, &tmA, bar, w.m0, w.p0 + d0);
-                            tma_load_2d(st + kABytes / 2, &tmA, bar, w.m0 + 64, w.p0 + d0);
+                            load_2d<CG>(st, &tmA, bar, m0, w.p0 + d0);
+                            load_2d<CG>(st + kABytes / 2, &tmA, bar, m0 + 64, w.p0 + d0);
                         } else if (AMN) {
-                            tma_load_3d(st, &tmA, bar, w.m0, d0, w.e);
-                            tma_load_3d(st + kABytes / 2, &tmA, bar, w.m0 + 64, d0, w.e);
+                            load_3d<CG>(st, &tmA, bar, m0, d0, w.e);
+                            load_3d<CG>(st + kABytes / 2, &tmA, bar, m0 + 64, d0, w.e);
                         } else {
-                            tma_load_3d(st, &tmA, bar, d0, w.m0, w.e);
+                            load_3d<CG>(st, &tmA, bar, d0, m0, w.e);
                         }
                     } else {
                         const uint32_t sb = st + kABytes;
+                        const int boxes = (nb + 63) / 64;
+                        if (arrives)
+                            mbar_arrive_expect_tx(arrive_bar,
+                                                  (DW ? boxes * 8192 : nb * 128) * both);
                         if (DW) {
-                            const int boxes = (nb + 63) / 64;
-                            mbar_arrive_expect_tx(bar, boxes * 8192);
-                            for (int i = 0; i < boxes; ++i)
-                                tma_load_2d(sb + i * 8192, &tmB, bar, w.n0 + 64 * i, w.p0 + d0);
+                            for (int i = 0; i < boxes; ++i) load_2d<CG>(sb + i * 8192, &tmB, bar, n0 + 64 * i, w.p0 + d0);
                         } else {
-                            mbar_arrive_expect_tx(bar, nb * 128);
-                            const int row = w.p0 + w.n0;
+                            const int row = w.p0 + n0;
                             int r = 0;
-                            for (; r + 64 <= nb; r += 64) tma_load_2d(sb + r * 128, &tmB, bar, d0, row + r);
-                            for (; r < nb; r += 16) tma_load_2d(sb + r * 128, &tmB16, bar, d0, row + r);
+                            for (; r + 64 <= nb; r += 64) load_2d<CG>(sb + r * 128, &tmB, bar, d0, row + r);
+                            for (; r < nb; r += 16) load_2d<CG>(sb + r * 128, &tmB16, bar, d0, row + r);
                         }
                     }
                 }
@@ -300,8 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // Leave no copy in flight: wait for the last phase armed on each slot.
-        for (int i = 0; i < armed; ++i) {
+        // Leave no copy in flight: wait for the last phase armed on each slot (rank 0 holds the
+        // barriers of both CTAs' copies).
+        for (int i = 0; rank == 0 && i < armed; ++i) {
             int idx = s - 1 - i;
             uint32_t par = ph;
             if (idx < 0) {
@@ -310,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mbar_wait(full_bar(idx), par, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
         }
-    } else if (warp == 2) {
+    } else if (warp == 2 && rank == 0) {
         // ------------------------------------------------ MMA issuer
         // K-major operand: +32 bytes per 16 of depth inside the swizzled row.
         // MN-major operand: chunks of 64 columns 8 KB apart, +16 rows per 16.
@@ -319,11 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     : smem_desc(s0 + kABytes, 16u, 1024u, SWZ_128B);
         constexpr uint32_t kAStep = AMN ? 128 : 2, kBStep = BMN ? 128 : 2;
         int s = 0, acc = 0;
-        uint32_t ph = 0, aph = 0;
+        uint32_t ph = 0, aph = 0, zph = 0;
         bool ok = true;
         for (int u = group; ok && walk.find(u, w); u += groups) {
             if (w.steps == 0) continue;
-            if (!mbar_wait(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
+            if (!(CG == 2 ? mbar_wait_cluster(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)
+                          : mbar_wait(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)))
+                break;
             tc_fence_after();
             const uint32_t d = tmem + static_cast<uint32_t>(acc * kMaxTile);
             const uint32_t idesc = idesc_f16(128 * CG, w.nt, a.bf16 != 0, AMN, BMN, false);
@@ -339,23 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (valid < kDepth) {
                         sub = (valid + 15) / 16;
                         if (valid & 15) {
-                            // rows of the next expert in the last 16: both operands become zero
-                            const int chunks = 2 + (w.nt / CG + 63) / 64;
-                            const int units = (sub * 16 - valid) * 8;
-                            for (int c = 0; c < chunks; ++c)
-                                for (int i = lane; i < units; i += 32)
-                                    st_shared_v4(s0 + s * G::kStage + c * 8192 + valid * 128 + i * 16,
-                                                 make_uint4(0, 0, 0, 0));
-                            fence_proxy_async_smem();
-                            __syncwarp();
+                            clear_tail(s0 + s * G::kStage, valid, sub * 16, 2 + (w.nt / CG + 63) / 64, lane);
+                            if (CG == 2) {
+                                if (!mbar_wait_cluster(zeroed_bar(s), (zph >> s) & 1u, a.timeout_ns, a.err,
+                                                       SPMM_DEVERR_TIMEOUT)) {
+                                    ok = false;
+                                    break;
+                                }
+                                zph ^= 1u << s;
+                                tc_fence_after();
+                            }
                         }
                     }
                 }
                 if (lane == 0) {
                     const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (G::kStage >> 4));
                     for (int kk = 0; kk < sub; ++kk)
-                        mma_f16(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u);
-                    mma_commit(empty_bar(s));
+                        mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u);
+                    commit<CG>(empty_bar(s));
                 }
                 __syncwarp();
                 if (++s == G::kStages) {
@@ -363,13 +445,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ph ^= 1u;
                 }
             }
-            if (lane == 0) mma_commit(accf_bar(acc));
+            if (lane == 0) commit<CG>(accf_bar(acc));
             __syncwarp();
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
-        if (lane == 0) mma_commit(done_bar);
+        if (lane == 0) commit<CG>(done_bar);
         __syncwarp();
+        mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
+    } else if (warp == 2) {
+        // ------------------------------------------------ rank 1 of a pair: dw clears its own tails.
+        // Tails of short units may be in flight together, so each slot has its own barriers.
+        int s = 0;
+        uint32_t ph = 0;
+        for (int u = group; DW && walk.find(u, w); u += groups) {
+            s = (s + w.steps) % G::kStages;
+            const int valid = w.cnt % kDepth;
+            if ((valid & 15) == 0) continue;
+            const int last = s == 0 ? G::kStages - 1 : s - 1;
+            if (!mbar_wait(tail_bar(last), (ph >> last) & 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
+            ph ^= 1u << last;
+            clear_tail(s0 + last * G::kStage, valid, (valid + 15) / 16 * 16, 2 + (w.nt / CG + 63) / 64, lane);
+            if (lane == 0) mbar_arrive_remote(map_shared(zeroed_bar(last), 0));
+            __syncwarp();
+        }
+        // rank 0's last commit has arrived here: none of its arrivals is still on its way at exit
         mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
     } else if (warp == 3) {
         // ------------------------------------------------ zero rows of dropped choices
@@ -381,41 +481,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------ epilogue
-        const int q = warp & 3;  // TMEM lane quarter
-        const uint32_t stage = out0 + q * kStageOut;
+        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter, half of the columns
+        const uint32_t stage = out0 + (warp - 4) * kStageOut;
         int acc = 0;
         uint32_t aph = 0;
         for (int u = group; walk.find(u, w); u += groups) {
-            const int row0 = w.m0 + 32 * q;
+            const int row0 = w.m0 + 128 * rank + 32 * q;
             const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kMaxTile);
             if (w.steps > 0) {
                 if (!mbar_wait(accf_bar(acc), aph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
                 tc_fence_after();
             }
+            // columns past the live ones of this warp's half are computed but not stored
+            const int c0 = half * (kMaxTile / 2), c1 = min(w.live, c0 + kMaxTile / 2);
             if (DW) {
                 if (a.bf16)
-                    store_dw<__nv_bfloat16>(a, w, t, w.steps == 0, row0, lane, stage);
+                    store_dw<__nv_bfloat16>(a, w, t, c0, c1, row0, lane, stage);
                 else
-                    store_dw<__half>(a, w, t, w.steps == 0, row0, lane, stage);
+                    store_dw<__half>(a, w, t, c0, c1, row0, lane, stage);
             } else if (a.bf16) {
-                store_rows<__nv_bfloat16>(a, w, t, row0 + lane);
+                store_rows<__nv_bfloat16>(a, w, t, c0, c1, row0, lane, stage);
             } else {
-                store_rows<__half>(a, w, t, row0 + lane);
+                store_rows<__half>(a, w, t, c0, c1, row0, lane, stage);
             }
             if (w.steps == 0) continue;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce_bar(acc));
+            if (lane == 0) {
+                if (rank == 0)
+                    mbar_arrive(acce_bar(acc));
+                else
+                    mbar_arrive_remote(map_shared(acce_bar(acc), 0));
+            }
+            __syncwarp();
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
     }
 
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    sync_all<CG>();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (CG == 2)
+            tmem_dealloc_pair(tmem, 512);
+        else
+            tmem_dealloc(tmem, 512);
     }
 }
 
@@ -437,12 +549,22 @@ spmm_status launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
                    int64_t units, const DeviceInfo* dev, cudaStream_t s) {
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
     const auto kern = experts_kernel<CG, AMN, BMN>;
-    const int slot = kSlotExperts + (BMN ? 2 : AMN ? 1 : 0);
+    const int slot = kSlotExperts + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
     if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), Ring<CG>::kSmem, slot)) return SPMM_ERR_CUDA;
-    const int grid = static_cast<int>(units < dev->sms ? units : dev->sms);
+    const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<CG>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = CG;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = CG == 2 ? 1 : 0;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    kern<<<grid, kThreads, Ring<CG>::kSmem, s>>>(tmA, tmB, tmB16, a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmB16, a);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
 }
@@ -470,9 +592,13 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128) ||
         !rows_map(&tmB, dtype, rows, ldr, n, a.depth, 64) || !rows_map(&tmB16, dtype, rows, ldr, n, a.depth, 16))
         return SPMM_ERR_CUDA;
-    a.m_tiles = (a.m + 127) / 128;
+    const bool pair = a.m > 128;
+    a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     // at most this many units: one partial row tile per expert with rows
     const int64_t units = (n / kMaxTile + (n < E ? n : E)) * a.m_tiles;
+    if (pair)
+        return transposed ? launch<2, true, false>(tmA, tmB, tmB16, a, units, dev, s)
+                          : launch<2, false, false>(tmA, tmB, tmB16, a, units, dev, s);
     return transposed ? launch<1, true, false>(tmA, tmB, tmB16, a, units, dev, s)
                       : launch<1, false, false>(tmA, tmB, tmB16, a, units, dev, s);
 }
@@ -494,14 +620,17 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
     a.timeout_ns = kWaitTimeoutNs;
-    a.m_tiles = (a.m + 127) / 128;
+    const bool pair = a.m > 128;
+    a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     a.n_tiles = (a.n + kMaxTile - 1) / kMaxTile;
     CUtensorMap tmA, tmB;
     // without rows every gradient is zero and no operand is read; the maps then cover the output's memory
     if (!rows_map(&tmA, dtype, n ? dys : dW, n ? ldd : ldw, n ? n : 1, n ? N : K, kDepth) ||
         !rows_map(&tmB, dtype, n ? xs : dW, n ? ldx : ldw, n ? n : 1, K, kDepth))
         return SPMM_ERR_CUDA;
-    return launch<1, true, true>(tmA, tmB, tmB, a, static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles, dev, s);
+    const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
+    return pair ? launch<2, true, true>(tmA, tmB, tmB, a, units, dev, s)
+                : launch<1, true, true>(tmA, tmB, tmB, a, units, dev, s);
 }
 
 }  // namespace spmm
