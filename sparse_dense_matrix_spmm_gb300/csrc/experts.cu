@@ -18,9 +18,10 @@
 // Roles per CTA: warp 0 loads A, warp 1 loads B (TMA, 128-byte swizzle, one
 // ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-11
 // store D (two accumulators of 256 TMEM columns, so a unit's epilogue overlaps
-// the next unit's MMAs), warp 3 writes the zero rows of dropped choices.  The
-// host knows no row counts: every role walks the work units by itself, 32
-// experts' offsets at a time.
+// the next unit's MMAs).  The host knows no row counts: warp 3 finds this CTA's
+// work units, 32 experts' offsets at a time, and announces them to the other
+// warps through a ring of four (a search per role cost every role its latency
+// per unit); at the end it writes the zero rows of dropped choices.
 #include "internal.h"
 #include "rowvec.cuh"
 #include "sm103.cuh"
@@ -36,6 +37,7 @@ constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzl
 constexpr int kMaxTile = 256;    // columns of D per unit
 constexpr int kABytes = 128 * 128;
 constexpr int kStageOut = 4096;  // per epilogue warp
+constexpr int kUnits = 4;        // work units announced ahead
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -138,8 +140,8 @@ struct Ring {
     static constexpr int kBBytes = kMaxTile / CG * 128;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = CG == 1 ? 4 : 6;
-    static constexpr int kBars = 4 * kStages + 5;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageOut + kBars * 8 + 16;
+    static constexpr int kBars = 4 * kStages + 5 + 2 * kUnits;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageOut + kBars * 8 + 16 + kUnits * static_cast<int>(sizeof(Unit));
 };
 
 template <typename T>
@@ -172,7 +174,7 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, u
             const int r = 8 * i + (lane >> 2);
             const uint4 p = ld_shared_v4(stage + r * 64 + ((unit ^ ((r >> 1) & 3)) << 4));
             // features come in groups of 8 (N % 8 == 0), so a group is stored whole or not at all
-            if (feature < a.m && c + r < c1) *reinterpret_cast<uint4*>(out + (c + r) * a.ldo + feature) = p;
+            if (feature < a.m && c + r < c1) __stcs(reinterpret_cast<uint4*>(out + (c + r) * a.ldo + feature), p);
         }
         __syncwarp();
     }
@@ -212,7 +214,7 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uin
             const uint4 p = ld_shared_v4(stage + r * 128 + ((u ^ (r & 7)) << 4));
             // columns come in groups of 8 (K % 8 == 0), so a group is stored whole or not at all
             if (row0 + r < a.m && c + 8 * u < c1)
-                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * a.ldo + c + 8 * u) = p;
+                __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * a.ldo + c + 8 * u), p);
         }
         __syncwarp();
     }
@@ -286,6 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t done_bar = bar0 + 8u * (2 * G::kStages + 4);
     auto tail_bar = [&](int s) { return done_bar + 8u + 8u * s; };
     auto zeroed_bar = [&](int s) { return done_bar + 8u + 8u * (G::kStages + s); };
+    auto unitf_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + i); };
+    auto unite_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + kUnits + i); };
+    Unit* ring = reinterpret_cast<Unit*>(tslot + 4);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
@@ -300,6 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
             mbar_init(acce_bar(b), kEpiWarps * CG);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(unitf_bar(i), 1);
+            mbar_init(unite_bar(i), 3 + kEpiWarps);  // every warp but the walking one
         }
         mbar_init(done_bar, 1);
         fence_mbar_init();
@@ -319,15 +328,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     sync_all<CG>();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    Walk<CG, DW> walk(a, lane);
     Unit w;
+    // the next unit for this warp; false after the last one
+    int ui = 0;
+    uint32_t uph = 0;
+    auto next_unit = [&]() {
+        if (!mbar_wait(unitf_bar(ui), uph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) return false;
+        w = ring[ui];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(unite_bar(ui));
+        if (++ui == kUnits) {
+            ui = 0;
+            uph ^= 1u;
+        }
+        return w.e >= 0;
+    };
 
     if (warp < 2) {
         // ------------------------------------------------ producers: A (warp 0), B (warp 1)
         int s = 0, armed = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = group; ok && walk.find(u, w); u += groups) {
+        while (ok && next_unit()) {
             const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank;
             for (int k = 0; k < w.steps; ++k) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, acc = 0;
         uint32_t ph = 0, aph = 0, zph = 0;
         bool ok = true;
-        for (int u = group; ok && walk.find(u, w); u += groups) {
+        while (ok && next_unit()) {
             if (w.steps == 0) continue;
             if (!(CG == 2 ? mbar_wait_cluster(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)
                           : mbar_wait(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)))
@@ -408,34 +430,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t d = tmem + static_cast<uint32_t>(acc * kMaxTile);
             const uint32_t idesc = idesc_f16(128 * CG, w.nt, a.bf16 != 0, AMN, BMN, false);
-            for (int k = 0; k < w.steps; ++k) {
+            // whole stages; the loop stays warp-uniform around the one issuing thread, which keeps the
+            // descriptors in uniform registers
+            const int whole = DW ? w.cnt / kDepth : w.steps;
+            for (int k = 0; k < whole; ++k) {
                 if (!mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                int sub = 4;  // MMAs of 16 depth; TMA zero-filled what lies past a row product's depth
-                if (DW) {
-                    const int valid = w.cnt - k * kDepth;
-                    if (valid < kDepth) {
-                        sub = (valid + 15) / 16;
-                        if (valid & 15) {
-                            clear_tail(s0 + s * G::kStage, valid, sub * 16, 2 + (w.nt / CG + 63) / 64, lane);
-                            if (CG == 2) {
-                                if (!mbar_wait_cluster(zeroed_bar(s), (zph >> s) & 1u, a.timeout_ns, a.err,
-                                                       SPMM_DEVERR_TIMEOUT)) {
-                                    ok = false;
-                                    break;
-                                }
-                                zph ^= 1u << s;
-                                tc_fence_after();
-                            }
-                        }
-                    }
-                }
                 if (lane == 0) {
                     const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (G::kStage >> 4));
-                    for (int kk = 0; kk < sub; ++kk)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
                         mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u);
                     commit<CG>(empty_bar(s));
                 }
@@ -445,6 +452,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ph ^= 1u;
                 }
             }
+            if (DW && ok && whole < w.steps) {
+                // the tail: MMAs of 16 rows up to the expert's last, what follows it cleared
+                const int valid = w.cnt - whole * kDepth, sub = (valid + 15) / 16;
+                ok = mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
+                if (valid & 15) {
+                    clear_tail(s0 + s * G::kStage, valid, sub * 16, 2 + (w.nt / CG + 63) / 64, lane);
+                    if (CG == 2) {
+                        ok = ok && mbar_wait_cluster(zeroed_bar(s), (zph >> s) & 1u, a.timeout_ns, a.err,
+                                                     SPMM_DEVERR_TIMEOUT);
+                        zph ^= 1u << s;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                if (lane == 0 && ok) {
+                    const uint64_t so = static_cast<uint32_t>(s) * (G::kStage >> 4);
+                    for (int kk = 0; kk < sub; ++kk)
+                        mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc,
+                                (whole | kk) != 0 ? 1u : 0u);
+                    commit<CG>(empty_bar(s));
+                }
+                if (++s == G::kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            __syncwarp();
             if (lane == 0) commit<CG>(accf_bar(acc));
             __syncwarp();
             acc ^= 1;
@@ -458,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Tails of short units may be in flight together, so each slot has its own barriers.
         int s = 0;
         uint32_t ph = 0;
-        for (int u = group; DW && walk.find(u, w); u += groups) {
+        while (next_unit()) {
+            if (!DW) continue;
             s = (s + w.steps) % G::kStages;
             const int valid = w.cnt % kDepth;
             if ((valid & 15) == 0) continue;
@@ -472,7 +507,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rank 0's last commit has arrived here: none of its arrivals is still on its way at exit
         mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
     } else if (warp == 3) {
-        // ------------------------------------------------ zero rows of dropped choices
+        // ------------------------------------------------ work units, and the zero rows of dropped choices
+        Walk<CG, DW> walk(a, lane);
+        bool more = true;
+        for (int u = group; more; u += groups) {
+            more = walk.find(u, w);
+            if (!more) w.e = -1;
+            if (!mbar_wait(unite_bar(ui), uph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
+            if (lane == 0) {
+                ring[ui] = w;
+                mbar_arrive(unitf_bar(ui));
+            }
+            __syncwarp();
+            if (++ui == kUnits) {
+                ui = 0;
+                uph ^= 1u;
+            }
+        }
         if (!DW) {
             for (int64_t p = __ldg(a.offsets + a.E) + static_cast<int64_t>(blockIdx.x); p < a.R; p += gridDim.x) {
                 uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + p * a.ldo);
@@ -485,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stage = out0 + (warp - 4) * kStageOut;
         int acc = 0;
         uint32_t aph = 0;
-        for (int u = group; walk.find(u, w); u += groups) {
+        while (next_unit()) {
             const int row0 = w.m0 + 128 * rank + 32 * q;
             const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kMaxTile);
             if (w.steps > 0) {
