@@ -232,11 +232,12 @@ __device__ __forceinline__ void clear_tail(uint32_t stage, int valid, int end, i
 
 // One CTA (CG = 1) or a pair (CG = 2) per MMA.
 template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc,
+                                    uint32_t issue) {
     if (CG == 2)
-        mma_f16_pair(d, ad, bd, idesc, acc);
+        mma_f16_pair(d, ad, bd, idesc, acc, issue);
     else
-        mma_f16(d, ad, bd, idesc, acc);
+        mma_f16_issue(d, ad, bd, idesc, acc, issue);
 }
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -439,13 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (G::kStage >> 4));
+                const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (G::kStage >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u);
-                    commit<CG>(empty_bar(s));
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u,
+                            lane == 0);
+                if (lane == 0) commit<CG>(empty_bar(s));
                 __syncwarp();
                 if (++s == G::kStages) {
                     s = 0;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t so = static_cast<uint32_t>(s) * (G::kStage >> 4);
                     for (int kk = 0; kk < sub; ++kk)
                         mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc,
-                                (whole | kk) != 0 ? 1u : 0u);
+                                (whole | kk) != 0 ? 1u : 0u, 1u);
                     commit<CG>(empty_bar(s));
                 }
                 if (++s == G::kStages) {
