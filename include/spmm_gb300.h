@@ -494,7 +494,8 @@ SPMM_API spmm_status spmm_bcsr_permuted(const spmm_bcsr_t *A, const int32_t *per
  * nothing to write returns SPMM_OK without launching.  A dimension of 2^31 or
  * more, or T k >= 2^31, -> SPMM_ERR_UNSUPPORTED (row offsets are 64-bit). */
 
-/* Workspace bytes spmm_build_route needs (0 when n_keys < 512). */
+/* Workspace bytes spmm_build_route needs (0 for few choices of fewer than 512
+ * keys). */
 SPMM_API spmm_status spmm_build_route_workspace_size(int64_t T, int32_t k, int64_t n_keys, size_t *bytes);
 /* Sorts ids[T][k] (device, id_bytes 4 or 8 per signed id, row pitch ldi) into
  * R->order, R->pos and R->offsets (device arrays of the caller; R->T, R->k and

@@ -614,7 +614,7 @@ def spmm_build_route(ids: torch.Tensor, n_keys: int, workspace: Optional[torch.T
     if ids.dim() == 2 and k > 1 and T > 0 and ids.stride(1) != 1:
         raise ValueError("ids must have contiguous rows")
     dev = ids.device
-    need = 0 if n_keys < 512 else spmm_build_route_workspace_size(T, k, n_keys)
+    need = spmm_build_route_workspace_size(T, k, n_keys)
     if workspace is None and need:
         workspace = _empty(need, torch.uint8, dev, stream)
     R = Route(T, k, n_keys, _empty(T * k, torch.int32, dev, stream), _empty(ids.shape, torch.int32, dev, stream),

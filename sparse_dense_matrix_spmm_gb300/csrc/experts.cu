@@ -617,6 +617,7 @@ spmm_status launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
     trace_begin(SPMM_KERNEL_EXPERTS, s);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmB16, a);
     trace_end(SPMM_KERNEL_EXPERTS, s);
+    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by the next call
     return cuda_status(e);
 }
 

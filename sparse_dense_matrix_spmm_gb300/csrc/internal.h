@@ -60,12 +60,36 @@ spmm_status check_24_call(const spmm_24_t* A, const void* B, int64_t ldb, const 
 void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
-// Slots of set_smem_attr_once taken by the one-hot operators (0-23 belong to
-// the format kernels).
-enum : int { kSlotRouteSort = 24, kSlotExperts = 25 };
+// First of the six slots of set_smem_attr_once that the experts' kernels take
+// (0-23 belong to the format kernels).
+enum : int { kSlotExperts = 24 };
 
 // Raise a kernel's dynamic shared memory limit once per device.
 bool set_smem_attr_once(const void* kernel, int bytes, int slot);
+
+// Launch that may overlap the end of the kernel before it in the stream (the
+// kernel calls ptx::grid_dep_wait before it touches memory), on clusters of
+// `cluster` CTAs.  An error is returned and cleared.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by the next call
+    return e;
+}
 
 // Kernel launchers implemented in the per-format translation units.  Arguments
 // are already validated by the C-ABI layer.

@@ -18,144 +18,275 @@ namespace {
 using namespace rows;
 
 // ---------------------------------------------------------------- sort
-// Least-significant-digit radix sort with 9-bit digits in one CTA.  Every warp
-// owns a consecutive piece of the input, so "earlier warp, then earlier lane" is
-// input order and each pass is stable.  A pass counts digits per warp, turns the
-// counts into first places (digits, then warps, in order) and writes each
-// element at its digit's next place in its warp.
+// Least-significant-digit radix sort, up to 9 bits per pass.  The digits of
+// every CTA's stretch of the input are counted, then each CTA adds up the counts
+// before its own (smaller digits, then earlier CTAs) and writes its elements in
+// input order at their digits' places.  Placing an element counts its next digit
+// for the CTA that will read it there, so only the first pass has a counting
+// launch.  Inside a tile a warp owns consecutive elements and ranks them with
+// one ballot per digit bit, so the order is that of the input and nothing
+// depends on the order of atomics.  Up to kSmall elements run in one CTA and one
+// launch, where launches would cost more than the work.
+// The kernels are bound by latency (launches and chains of dependent loads).
+// One cluster of 8 CTAs that ranked with match_any and counted in distributed
+// shared memory took one launch but 56 us for 131072 elements (its 8 SMs' issue
+// slots), and in one CTA 10.3 us for 2048 against 6.8 us here.
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kSortWarps = 32;
+constexpr int kSortThreads = 512;  // one per bin
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kItems = 4;          // per thread and tile
+constexpr int kTile = kSortThreads * kItems;
+constexpr int kSmall = 2 * kTile;
+constexpr int kMaxCtas = 128;  // each reads every CTA's counts (256 CTAs for 524288 elements: 30 us in those reads)
 
 struct SortArgs {
     const void* ids;
-    int64_t ldi;      // row pitch of ids in elements
-    int32_t wide;     // ids are 64-bit
-    int32_t k, n, n_keys, passes;
+    int64_t ldi;   // row pitch of ids in elements
+    int32_t wide;  // ids are 64-bit
+    int32_t k, n, n_keys, passes, bits;
+    int32_t chunk;  // elements per CTA, a multiple of kTile
     int32_t *order, *pos, *offsets;
-    int32_t *key_buf[2], *idx_buf[2];  // between passes
+    int32_t *keys0, *idx0, *keys1, *idx1;  // results of even and odd passes
+    int32_t* table;                    // [passes][CTAs][bins] digit counts
     int* err;
 };
 
 // Key of flat index f: its id, or n_keys (sorted last) when the choice is dropped.
 __device__ __forceinline__ int32_t load_key(const SortArgs& a, int32_t f) {
-    const int32_t t = f / a.k;
-    const int64_t at = t * a.ldi + (f - t * a.k);
-    const int64_t v = a.wide ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
+    int64_t at = f;
+    if (a.ldi != a.k) {
+        const int32_t t = f / a.k;
+        at = t * a.ldi + (f - t * a.k);
+    }
+    const int64_t v =
+        a.wide ? __ldg(static_cast<const int64_t*>(a.ids) + at) : __ldg(static_cast<const int32_t*>(a.ids) + at);
     if (v >= 0 && v < a.n_keys) return static_cast<int32_t>(v);
     if (v >= 0) atomicOr(a.err, SPMM_DEVERR_INDEX);
     return a.n_keys;
 }
 
-__global__ void __launch_bounds__(kSortWarps * 32, 1) route_sort_kernel(const SortArgs a) {
-    extern __shared__ int32_t smem[];
-    int32_t(*hist)[kBins] = reinterpret_cast<int32_t(*)[kBins]>(smem);  // [warps][kBins]
-    int32_t* total = smem + kSortWarps * kBins;                        // [kBins]
+// Input of a pass: the ids, or the result of the pass before (written by other
+// SMs or earlier in this kernel, so read past L1).
+__device__ __forceinline__ int32_t pass_key(const SortArgs& a, int pass, int32_t i) {
+    return pass ? __ldcg(((pass & 1) ? a.keys0 : a.keys1) + i) : load_key(a, i);
+}
+
+__device__ __forceinline__ int32_t warp_scan(int32_t v, int lane) {  // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+struct SortShared {
+    int32_t hist[kSortWarps][kBins];
+    int32_t first[kBins];
+    int32_t sums[kSortWarps];
+};
+
+// Digit counts of elements [i0, i1) into s.first.
+__device__ __forceinline__ void count_digits(const SortArgs& a, int pass, int32_t i0, int32_t i1, SortShared& s) {
+    const int bins = 1 << a.bits, shift = pass * a.bits;
+    s.first[threadIdx.x] = 0;
+    __syncthreads();
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
+        atomicAdd(&s.first[(pass_key(a, pass, static_cast<int32_t>(i)) >> shift) & (bins - 1)], 1);
+    __syncthreads();
+}
+
+// This thread's digit: `all` elements of it in the input, `below` of them in
+// earlier CTAs.  Leaves the first place of the CTA's elements in s.first.
+__device__ __forceinline__ void first_places(const SortArgs& a, int32_t all, int32_t below, bool write_offsets,
+                                             SortShared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int piece = ((a.n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int f0 = min(a.n, warp * piece), f1 = min(a.n, f0 + piece);
-    const uint32_t below = (1u << lane) - 1u;
-    if (a.passes > 1)
-        for (int e = threadIdx.x; e <= a.n_keys; e += blockDim.x) a.offsets[e] = 0;
-    for (int pass = 0; pass < a.passes; ++pass) {
-        const int shift = pass * kDigitBits;
-        const bool last = pass + 1 == a.passes;
-        const int32_t* src_key = a.key_buf[(pass + 1) & 1];
-        const int32_t* src_idx = a.idx_buf[(pass + 1) & 1];
-        for (int b = lane; b < kBins; b += 32) hist[warp][b] = 0;
+    const int32_t incl = warp_scan(all, lane);
+    if (lane == 31) s.sums[warp] = incl;
+    __syncthreads();
+    int32_t start = incl - all;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w)
+        if (w < warp) start += s.sums[w];
+    s.first[threadIdx.x] = start + below;
+    if (write_offsets && static_cast<int>(threadIdx.x) <= a.n_keys) a.offsets[threadIdx.x] = start;
+    __syncthreads();
+}
+
+// A thread's elements of a tile: consecutive ones per warp.  Key -1 past the end.
+struct Items {
+    int32_t key[kItems], idx[kItems];
+    __device__ __forceinline__ void load(const SortArgs& a, int pass, int64_t tile, int32_t i1) {
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const int64_t i = tile + (threadIdx.x >> 5) * (32 * kItems) + j * 32 + (threadIdx.x & 31);
+            const int32_t at = static_cast<int32_t>(i);
+            key[j] = i < i1 ? pass_key(a, pass, at) : -1;
+            idx[j] = i < i1 && pass ? __ldcg(((pass & 1) ? a.idx0 : a.idx1) + at) : at;
+        }
+    }
+};
+
+// Writes elements [i0, i1) at their places, a tile at a time; `it` holds the
+// first tile.
+__device__ __forceinline__ void place_elements(const SortArgs& a, int pass, int32_t i0, int32_t i1, Items& it,
+                                               int32_t* next_table, SortShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int bins = 1 << a.bits, shift = pass * a.bits;
+    const bool last = pass + 1 == a.passes;
+    const uint32_t before = (1u << lane) - 1u;
+    for (int64_t tile = i0; tile < i1; tile += kTile) {
+        for (int b = lane; b < bins; b += 32) s.hist[warp][b] = 0;
         __syncwarp();
-        for (int i = f0; i < f1; i += 32) {
-            const bool live = i + lane < f1;
-            int digit = -1;
-            if (live) {
-                const int32_t key = pass ? src_key[i + lane] : load_key(a, i + lane);
-                digit = (key >> shift) & (kBins - 1);
+        int32_t rank[kItems];
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const bool live = it.key[j] >= 0;
+            const int digit = (it.key[j] >> shift) & (bins - 1);
+            uint32_t peers = __ballot_sync(0xffffffffu, live);  // lanes with the same digit
+#pragma unroll
+            for (int b = 0; b < kDigitBits; ++b) {
+                if (b < a.bits) {
+                    const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1);
+                    peers &= (digit >> b) & 1 ? set : ~set;
+                }
             }
-            const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-            if (live && (peers & below) == 0) hist[warp][digit] += __popc(peers);
+            rank[j] = __popc(peers & before);
+            if (live) rank[j] += s.hist[warp][digit];
+            __syncwarp();
+            if (live && (peers & before) == 0) s.hist[warp][digit] += __popc(peers);
             __syncwarp();
         }
         __syncthreads();
-        for (int b = threadIdx.x; b < kBins; b += blockDim.x) {
-            int32_t s = 0;
+        if (static_cast<int>(threadIdx.x) < bins) {
+            int32_t run = s.first[threadIdx.x];
+#pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const int32_t c = hist[w][b];
-                hist[w][b] = s;
-                s += c;
-            }
-            total[b] = s;
-        }
-        __syncthreads();
-        if (warp == 0) {  // exclusive sums over the digits, 16 per lane
-            int32_t s = 0;
-            for (int i = 0; i < kBins / 32; ++i) s += total[lane * (kBins / 32) + i];
-            int32_t run = s;
-            for (int d = 1; d < 32; d <<= 1) {
-                const int32_t o = __shfl_up_sync(0xffffffffu, run, d);
-                if (lane >= d) run += o;
-            }
-            run -= s;
-            for (int i = 0; i < kBins / 32; ++i) {
-                const int32_t c = total[lane * (kBins / 32) + i];
-                total[lane * (kBins / 32) + i] = run;
+                const int32_t c = s.hist[w][threadIdx.x];
+                s.hist[w][threadIdx.x] = run;
                 run += c;
             }
+            s.first[threadIdx.x] = run;
         }
         __syncthreads();
-        if (a.passes == 1)
-            for (int b = threadIdx.x; b <= a.n_keys; b += blockDim.x) a.offsets[b] = total[b];
-        for (int i = f0; i < f1; i += 32) {
-            const bool live = i + lane < f1;
-            int digit = -1;
-            int32_t key = 0, f = 0;
-            if (live) {
-                key = pass ? src_key[i + lane] : load_key(a, i + lane);
-                f = pass ? src_idx[i + lane] : i + lane;
-                digit = (key >> shift) & (kBins - 1);
-                if (a.passes > 1 && pass == 0) atomicAdd(a.offsets + key, 1);
-            }
-            const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-            int32_t p = 0;
-            if (live) p = total[digit] + hist[warp][digit] + __popc(peers & below);
-            __syncwarp();
-            if (live && (peers & below) == 0) hist[warp][digit] += __popc(peers);
-            __syncwarp();
-            if (!live) continue;
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const int32_t key = it.key[j], f = it.idx[j];
+            if (key < 0) continue;
+            const int32_t p = s.hist[warp][(key >> shift) & (bins - 1)] + rank[j];
             if (last) {
                 a.order[p] = f;
                 a.pos[f] = key < a.n_keys ? p : -1;
             } else {
-                a.key_buf[pass & 1][p] = key;
-                a.idx_buf[pass & 1][p] = f;
+                ((pass & 1) ? a.idx1 : a.idx0)[p] = f;
             }
+            if (a.passes > 1) ((pass & 1) ? a.keys1 : a.keys0)[p] = key;
+            if (next_table) atomicAdd(next_table + p / a.chunk * bins + ((key >> (shift + a.bits)) & (bins - 1)), 1);
         }
+        if (tile + kTile < i1) it.load(a, pass, tile + kTile, i1);
         __syncthreads();
-    }
-    if (a.passes > 1) {  // offsets holds the counts: exclusive sums in place, a block of threads at a time
-        int32_t carry = 0;
-        for (int e0 = 0; e0 <= a.n_keys; e0 += blockDim.x) {
-            const int e = e0 + threadIdx.x;
-            const int32_t c = e <= a.n_keys ? __ldcg(a.offsets + e) : 0;
-            int32_t run = c;
-            for (int d = 1; d < 32; d <<= 1) {
-                const int32_t o = __shfl_up_sync(0xffffffffu, run, d);
-                if (lane >= d) run += o;
-            }
-            if (lane == 31) total[warp] = run;
-            __syncthreads();
-            int32_t before = carry, all = 0;
-            for (int w = 0; w < kSortWarps; ++w) {
-                if (w < warp) before += total[w];
-                all += total[w];
-            }
-            if (e <= a.n_keys) a.offsets[e] = before + run - c;
-            carry += all;
-            __syncthreads();
-        }
     }
 }
 
-constexpr int kSortSmem = (kSortWarps + 1) * kBins * 4;
+// All passes in one CTA.
+__global__ void __launch_bounds__(kSortThreads) route_small_kernel(const SortArgs a) {
+    __shared__ SortShared s;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    for (int pass = 0; pass < a.passes; ++pass) {
+        Items it;
+        it.load(a, pass, 0, a.n);
+        count_digits(a, pass, 0, a.n, s);
+        const int32_t all = s.first[threadIdx.x];
+        first_places(a, all, 0, a.passes == 1, s);
+        place_elements(a, pass, 0, a.n, it, nullptr, s);
+    }
+}
+
+// Counts of the first pass, and zeros for those of the others.
+__global__ void __launch_bounds__(kSortThreads) route_count_kernel(const SortArgs a) {
+    __shared__ SortShared s;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int bins = 1 << a.bits;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+    count_digits(a, 0, static_cast<int32_t>(i0), static_cast<int32_t>(min(i0 + a.chunk, int64_t(a.n))), s);
+    if (static_cast<int>(threadIdx.x) < bins) {
+        int32_t* mine = a.table + blockIdx.x * bins + threadIdx.x;
+        *mine = s.first[threadIdx.x];
+        for (int pass = 1; pass < a.passes; ++pass) mine[pass * gridDim.x * bins] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) route_place_kernel(const SortArgs a, int pass) {
+    __shared__ SortShared s;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int bins = 1 << a.bits, cta = blockIdx.x, ctas = gridDim.x;
+    int32_t* table = a.table + pass * ctas * bins;
+    const int32_t i0 = cta * a.chunk, i1 = static_cast<int32_t>(min(int64_t(i0) + a.chunk, int64_t(a.n)));
+    Items it;  // in flight while the counts are added up
+    it.load(a, pass, i0, i1);
+    int32_t all = 0, below = 0;
+    // digits that occur: the last pass has no key above n_keys
+    const int used = pass + 1 == a.passes ? (a.n_keys >> (pass * a.bits)) + 1 : bins;
+    if (static_cast<int>(threadIdx.x) < used) {
+        // 16 loads in flight; every CTA starts at its own row, or they would all queue at one L2 slice
+        for (int c0 = 0; c0 < ctas; c0 += 16) {
+            int32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int c = c0 + i + cta < ctas ? c0 + i + cta : c0 + i + cta - ctas;
+                v[i] = c0 + i < ctas ? __ldcg(table + c * bins + threadIdx.x) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                all += v[i];
+                if (c0 + i + cta >= ctas) below += v[i];  // row c0 + i + cta - ctas, before cta's
+            }
+        }
+    }
+    first_places(a, all, below, a.passes == 1 && cta == 0, s);
+    place_elements(a, pass, i0, i1, it,
+                   pass + 1 < a.passes ? table + ctas * bins : nullptr, s);
+}
+
+// More than one pass: offsets[e] is the number of sorted keys below e.  A CTA
+// finds the place of its first key 256 probes at a time; its threads search on
+// from there in doubling steps, on lines that are then in L1.  (Counting with
+// atomics and scanning n_keys counts in the sort's few CTAs took 45 us for
+// 131072 keys.)
+constexpr int kOffsetThreads = 256;
+
+__global__ void __launch_bounds__(kOffsetThreads)
+    route_offsets_kernel(const int32_t* sorted, int32_t n, int32_t n_keys, int32_t* offsets) {
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t e0 = static_cast<int64_t>(blockIdx.x) * kOffsetThreads, e = e0 + threadIdx.x;
+    int64_t lo = 0, hi = n;  // the answer for e0 lies in [lo, hi]
+    while (lo < hi) {
+        const int64_t step = (hi - lo + kOffsetThreads - 1) / kOffsetThreads, at = lo + threadIdx.x * step;
+        const int64_t below = __syncthreads_count(at < hi && __ldcg(sorted + at) < e0);
+        hi = min(hi, lo + below * step);
+        if (below) lo += (below - 1) * step + 1;
+    }
+    if (e > n_keys) return;
+    int64_t step = 1;
+    while (lo + step <= n && __ldg(sorted + lo + step - 1) < e) {
+        lo += step;
+        step *= 2;
+    }
+    hi = min(int64_t(n), lo + step - 1);
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (__ldg(sorted + mid) < e)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    offsets[e] = static_cast<int32_t>(lo);
+}
 
 // ---------------------------------------------------------------- rows
 struct RowArgs {
@@ -265,17 +396,42 @@ int row_threads(int64_t H, int v) {
 
 }  // namespace
 
+namespace {
+struct SortPlan {
+    int passes, bits, ctas, chunk;
+};
+SortPlan sort_plan(int64_t n, int64_t n_keys) {
+    SortPlan p{};
+    int total = 1;  // bits of the largest key, n_keys itself
+    while (n_keys >> total) ++total;
+    p.passes = (total + kDigitBits - 1) / kDigitBits;
+    p.bits = (total + p.passes - 1) / p.passes;
+    if (n <= kSmall) {
+        p.ctas = 1;
+        p.chunk = kSmall;
+        return p;
+    }
+    const int64_t tiles = (n + kTile - 1) / kTile;
+    const int64_t per = (tiles + kMaxCtas - 1) / kMaxCtas;
+    p.chunk = static_cast<int>(per * kTile);
+    p.ctas = static_cast<int>((tiles + per - 1) / per);
+    return p;
+}
+}  // namespace
+
 size_t route_workspace_bytes(int64_t T, int32_t k, int64_t n_keys) {
-    return n_keys < kBins ? 0 : static_cast<size_t>(T) * k * 16;
+    const int64_t n = T * k;
+    const SortPlan p = sort_plan(n, n_keys);
+    return (p.passes > 1 ? static_cast<size_t>(n) * 16 : 0) +
+           (p.ctas > 1 ? static_cast<size_t>(p.ctas) * sizeof(int32_t) * p.passes << p.bits : 0);
 }
 
 spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, const spmm_route_t* R, void* ws,
                                cudaStream_t s) {
     const DeviceInfo* dev = device_info();
     if (!dev) return SPMM_ERR_CUDA;
-    if (!set_smem_attr_once(reinterpret_cast<const void*>(route_sort_kernel), kSortSmem, kSlotRouteSort))
-        return SPMM_ERR_CUDA;
     const int32_t n = static_cast<int32_t>(R->T * R->k);
+    const SortPlan p = sort_plan(n, R->n_keys);
     SortArgs a{};
     a.ids = ids;
     a.ldi = ldi;
@@ -283,21 +439,37 @@ spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, c
     a.k = R->k;
     a.n = n;
     a.n_keys = static_cast<int32_t>(R->n_keys);
-    a.passes = 1;
-    while (a.passes * kDigitBits < 31 && (R->n_keys >> (a.passes * kDigitBits))) ++a.passes;
+    a.passes = p.passes;
+    a.bits = p.bits;
+    a.chunk = p.chunk;
     a.order = R->order;
     a.pos = R->pos;
     a.offsets = R->offsets;
     int32_t* w = static_cast<int32_t*>(ws);
-    for (int i = 0; i < 2 && w; ++i) {
-        a.key_buf[i] = w + static_cast<int64_t>(2 * i) * n;
-        a.idx_buf[i] = w + static_cast<int64_t>(2 * i + 1) * n;
+    if (p.passes > 1) {
+        a.keys0 = w;
+        a.idx0 = w + static_cast<int64_t>(n);
+        a.keys1 = w + 2 * static_cast<int64_t>(n);
+        a.idx1 = w + 3 * static_cast<int64_t>(n);
+        w += 4 * static_cast<int64_t>(n);
     }
+    a.table = w;
     a.err = dev->err;
     trace_begin(SPMM_KERNEL_ROUTE, s);
-    route_sort_kernel<<<1, kSortWarps * 32, kSortSmem, s>>>(a);
+    cudaError_t e = cudaSuccess;
+    if (p.ctas == 1) {
+        e = launch_chained(route_small_kernel, 1, kSortThreads, 0, 1, s, a);
+    } else {
+        e = launch_chained(route_count_kernel, p.ctas, kSortThreads, 0, 1, s, a);
+        for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass)
+            e = launch_chained(route_place_kernel, p.ctas, kSortThreads, 0, 1, s, a, pass);
+    }
+    if (p.passes > 1 && e == cudaSuccess)
+        e = launch_chained(route_offsets_kernel, static_cast<unsigned>(R->n_keys / kOffsetThreads + 1),
+                           kOffsetThreads, 0, 1, s,
+                           (p.passes & 1) ? a.keys0 : a.keys1, n, a.n_keys, a.offsets);
     trace_end(SPMM_KERNEL_ROUTE, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 static RowArgs row_args(const spmm_route_t* R, int64_t H) {

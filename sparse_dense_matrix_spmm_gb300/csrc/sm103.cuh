@@ -19,6 +19,14 @@ __device__ __forceinline__ uint64_t globaltimer() {
     return t;
 }
 
+// Programmatic dependent launch: a kernel launched by launch_chained may start
+// while the kernel before it in the stream still runs.  grid_dep_wait returns
+// once every earlier kernel has finished and its writes are visible; nothing of
+// theirs may be read or overwritten before it.  grid_dep_launch lets the next
+// kernel's CTAs be scheduled.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
