@@ -289,6 +289,9 @@ __global__ void __launch_bounds__(kOffsetThreads)
 }
 
 // ---------------------------------------------------------------- rows
+constexpr int kRowThreads = 256;
+constexpr int kBatch = 4;  // rows of a token in flight per thread
+
 struct RowArgs {
     const int32_t *order, *pos, *offsets;
     int64_t T, H, n_keys;
@@ -304,94 +307,126 @@ struct RowArgs {
 // Rows past the last kept place are written as zeros, spread over the grid.
 template <typename T, int V>
 __device__ __forceinline__ void zero_tail(const RowArgs& a, T* out) {
-    for (int64_t p = a.offsets[a.n_keys] + blockIdx.x; p < a.T * a.k; p += gridDim.x)
+    for (int64_t p = __ldg(a.offsets + a.n_keys) + static_cast<int64_t>(blockIdx.x); p < a.T * a.k; p += gridDim.x)
         for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V)
-            Vec<T, V>::store(out + p * a.ldo + c, Vec<T, V>::zero());
+            Vec<T, V>::store_cs(out + p * a.ldo + c, Vec<T, V>::zero());
 }
 
 // One CTA per token: its row is read once and written at its k places.
 template <typename T, int V>
-__global__ void dispatch_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
     using X = Vec<T, V>;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const T* x = static_cast<const T*>(a.a) + blockIdx.x * a.lda;
     T* out = static_cast<T*>(a.out);
     const int32_t* pos = a.pos + static_cast<int64_t>(blockIdx.x) * a.k;
-    for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-        const typename X::Raw v = X::load(x + c);
+    for (int64_t c = threadIdx.x * V; c < a.H; c += 2 * blockDim.x * V) {
+        const int64_t c1 = c + blockDim.x * V;
+        const bool two = c1 < a.H;
+        const typename X::Raw v0 = X::load(x + c), v1 = two ? X::load(x + c1) : X::zero();
         for (int j = 0; j < a.k; ++j) {
-            const int64_t p = pos[j];
-            if (p >= 0) X::store(out + p * a.ldo + c, v);
+            const int64_t p = __ldg(pos + j);
+            if (p < 0) continue;
+            X::store_cs(out + p * a.ldo + c, v0);
+            if (two) X::store_cs(out + p * a.ldo + c1, v1);
         }
     }
     zero_tail<T, V>(a, out);
 }
 
-// One CTA per token: its k rows summed in fp32 with their weights, rounded once.
+// One CTA per token: its k rows summed in fp32 with their weights, j ascending,
+// and rounded once.  Four rows are in flight per thread.
 template <typename T, int V>
-__global__ void combine_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
     using X = Vec<T, V>;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const T* ys = static_cast<const T*>(a.a);
     T* y = static_cast<T*>(a.out) + blockIdx.x * a.ldo;
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.k;
     for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
         float acc[V] = {};
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = a.pos[f0 + j];
-            if (p < 0) continue;
-            const float w = a.w ? a.w[f0 + j] : 1.f;
-            float v[V];
-            X::unpack(X::load(ys + p * a.lda + c), v);
+        for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+            typename X::Raw r[kBatch];
+            float w[kBatch];
+            bool live[kBatch];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t p = j0 + j < a.k ? __ldg(a.pos + f0 + j0 + j) : -1;
+                live[j] = p >= 0;
+                r[j] = live[j] ? X::load(ys + p * a.lda + c) : X::zero();
+                w[j] = a.w && live[j] ? __ldg(a.w + f0 + j0 + j) : 1.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (!live[j]) continue;  // not 0 * w: a weight may be infinite
+                float v[V];
+                X::unpack(r[j], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[i], acc[i]);
+            }
         }
         X::store(y + c, X::pack(acc));
     }
 }
 
-// One CTA per token: for each of its k places dys = w dy and the dot product of
-// dy with ys, summed in fp32 over the CTA.
+// One CTA per token: dys = w dy at its k places and the k dot products of dy
+// with ys, each summed in fp32 per thread, then over the CTA in a fixed order.
 template <typename T, int V>
-__global__ void combine_grad_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs a) {
     using X = Vec<T, V>;
-    __shared__ float part[32];
+    __shared__ float part[kBatch][kRowThreads / 32];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const T* dy = static_cast<const T*>(a.a) + blockIdx.x * a.lda;
     const T* ys = static_cast<const T*>(a.b);
     T* dys = static_cast<T*>(a.out);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.k;
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t p = a.pos[f0 + j];
-        const float w = a.w ? a.w[f0 + j] : 1.f;
-        float dot = 0.f;
-        if (p >= 0) {
-            for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-                float d[V], v[V];
-                X::unpack(X::load(dy + c), d);
-                X::unpack(X::load(ys + p * a.ldb + c), v);
+    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+        int64_t p[kBatch];
+        float w[kBatch], dot[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            p[j] = j0 + j < a.k ? __ldg(a.pos + f0 + j0 + j) : -1;
+            w[j] = p[j] >= 0 ? __ldg(a.w + f0 + j0 + j) : 0.f;
+            dot[j] = 0.f;
+        }
+        for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
+            typename X::Raw r[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) r[j] = p[j] >= 0 ? X::load(ys + p[j] * a.ldb + c) : X::zero();
+            float d[V];
+            X::unpack(X::load(dy + c), d);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (p[j] < 0) continue;
+                float v[V];
+                X::unpack(r[j], v);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    dot = fmaf(d[i], v[i], dot);
-                    d[i] *= w;
+                    dot[j] = fmaf(d[i], v[i], dot[j]);
+                    v[i] = w[j] * d[i];
                 }
-                X::store(dys + p * a.ldo + c, X::pack(d));
+                X::store_cs(dys + p[j] * a.ldo + c, X::pack(v));
             }
         }
-        for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        if (lane == 0) part[warp] = dot;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+            for (int s = 16; s; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+            if (lane == 0) part[j][warp] = dot[j];
+        }
         __syncthreads();
-        if (threadIdx.x == 0 && a.dw) {
+        if (static_cast<int>(threadIdx.x) < kBatch && j0 + static_cast<int>(threadIdx.x) < a.k) {
             float s = 0.f;
-            for (int i = 0; i < (blockDim.x + 31) / 32; ++i) s += part[i];
-            a.dw[f0 + j] = s;
+            for (int i = 0; i < warps; ++i) s += part[threadIdx.x][i];
+            a.dw[f0 + j0 + threadIdx.x] = s;
         }
         __syncthreads();
     }
     zero_tail<T, V>(a, dys);
-}
-
-int row_threads(int64_t H, int v) {
-    const int64_t n = (H + v - 1) / v;
-    return n >= 512 ? 512 : static_cast<int>((n + 31) / 32 * 32);
 }
 
 }  // namespace
@@ -494,11 +529,12 @@ spmm_status launch_dispatch(const spmm_route_t* R, const void* x, int64_t ldx, v
     const int es = row_elem_bytes(dtype);
     const bool v = rows16(x, ldx, H, es) && rows16(xs, ldxs, H, es);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1);
+    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
-    SPMM_ROWS_TYPED(dtype, v, dispatch_kernel, grid, threads, s, a);
+    cudaError_t e;
+    SPMM_ROWS_TYPED(e, dtype, v, dispatch_kernel, grid, threads, s, a);
     trace_end(SPMM_KERNEL_ROWS, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 spmm_status launch_combine(const spmm_route_t* R, const void* ys, int64_t ldys, const float* w, void* y, int64_t ldy,
@@ -512,11 +548,12 @@ spmm_status launch_combine(const spmm_route_t* R, const void* ys, int64_t ldys, 
     const int es = row_elem_bytes(dtype);
     const bool v = rows16(ys, ldys, H, es) && rows16(y, ldy, H, es);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1);
+    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
-    SPMM_ROWS_TYPED(dtype, v, combine_kernel, grid, threads, s, a);
+    cudaError_t e;
+    SPMM_ROWS_TYPED(e, dtype, v, combine_kernel, grid, threads, s, a);
     trace_end(SPMM_KERNEL_ROWS, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 spmm_status launch_combine_grad(const spmm_route_t* R, const void* dy, int64_t lddy, const void* ys, int64_t ldys,
@@ -534,11 +571,12 @@ spmm_status launch_combine_grad(const spmm_route_t* R, const void* dy, int64_t l
     const int es = row_elem_bytes(dtype);
     const bool v = rows16(dy, lddy, H, es) && rows16(ys, ldys, H, es) && rows16(dys, lddys, H, es);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1);
+    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
-    SPMM_ROWS_TYPED(dtype, v, combine_grad_kernel, grid, threads, s, a);
+    cudaError_t e;
+    SPMM_ROWS_TYPED(e, dtype, v, combine_grad_kernel, grid, threads, s, a);
     trace_end(SPMM_KERNEL_ROWS, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 }  // namespace spmm

@@ -58,6 +58,7 @@ struct Vec {
     using Raw = uint4;
     static __device__ __forceinline__ Raw load(const T* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
     static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
+    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { __stcs(reinterpret_cast<uint4*>(p), r); }
     static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
     static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[V]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -89,6 +90,7 @@ struct Vec<T, 1> {
     using Raw = T;
     static __device__ __forceinline__ Raw load(const T* p) { return __ldg(p); }
     static __device__ __forceinline__ void store(T* p, const Raw& r) { *p = r; }
+    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { *p = r; }
     static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
     static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_f32<T>(r); }
     static __device__ __forceinline__ Raw pack(const float (&f)[1]) { return from_f32<T>(f[0]); }
@@ -106,6 +108,10 @@ struct Vec<float, 8> {
     static __device__ __forceinline__ void store(float* p, const Raw& r) {
         reinterpret_cast<uint4*>(p)[0] = r.lo;
         reinterpret_cast<uint4*>(p)[1] = r.hi;
+    }
+    static __device__ __forceinline__ void store_cs(float* p, const Raw& r) {
+        __stcs(reinterpret_cast<uint4*>(p), r.lo);
+        __stcs(reinterpret_cast<uint4*>(p) + 1, r.hi);
     }
     static __device__ __forceinline__ Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
     static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
@@ -131,15 +137,20 @@ inline bool rows16(const void* p, int64_t ld, int64_t H, int es) {
 
 }  // namespace spmm
 
-// KERNEL<T, V> for a row type and vector width chosen at run time.
-#define SPMM_ROWS_TYPED(dtype, vec, KERNEL, grid, threads, s, args)                                                  \
-    do {                                                                                                             \
-        if ((dtype) == SPMM_F32)                                                                                     \
-            vec ? KERNEL<float, 4><<<grid, threads, 0, s>>>(args) : KERNEL<float, 1><<<grid, threads, 0, s>>>(args); \
-        else if ((dtype) == SPMM_F16)                                                                                \
-            vec ? KERNEL<__half, 8><<<grid, threads, 0, s>>>(args)                                                   \
-                : KERNEL<__half, 1><<<grid, threads, 0, s>>>(args);                                                  \
-        else                                                                                                         \
-            vec ? KERNEL<__nv_bfloat16, 8><<<grid, threads, 0, s>>>(args)                                            \
-                : KERNEL<__nv_bfloat16, 1><<<grid, threads, 0, s>>>(args);                                           \
+// Threads of a CTA that moves rows of H elements, V at a time.
+inline int row_threads(int64_t H, int V, int most) {
+    const int64_t n = ((H + V - 1) / V + 31) / 32 * 32;
+    return static_cast<int>(n < most ? n : most);
+}
+
+// Launch KERNEL<T, V> for a row type and vector width chosen at run time.
+#define SPMM_ROWS_TYPED(status, dtype, vec, KERNEL, grid, threads, s, args)                                      \
+    do {                                                                                                         \
+        if ((dtype) == SPMM_F32)                                                                                 \
+            status = launch_chained(vec ? KERNEL<float, 4> : KERNEL<float, 1>, grid, threads, 0, 1, s, args);    \
+        else if ((dtype) == SPMM_F16)                                                                            \
+            status = launch_chained(vec ? KERNEL<__half, 8> : KERNEL<__half, 1>, grid, threads, 0, 1, s, args);  \
+        else                                                                                                     \
+            status = launch_chained(vec ? KERNEL<__nv_bfloat16, 8> : KERNEL<__nv_bfloat16, 1>, grid, threads, 0, \
+                                    1, s, args);                                                                 \
     } while (0)
