@@ -200,6 +200,8 @@ typedef struct {
  *   order[R]            flat indices sorted stably by id, dropped ones last
  *   pos[R]              place of flat index f in order; -1 if dropped
  *   offsets[n_keys + 1] first place of each key; offsets[n_keys] = kept choices
+ *   keys[R]             the sorted ids, n_keys for dropped choices (may be null;
+ *                       spmm_embed_grad needs it)
  * It stands for the R x T matrix P with P[p][order[p] / k] = 1 for p <
  * offsets[n_keys] and zero rows after. */
 typedef struct {
@@ -209,6 +211,7 @@ typedef struct {
     int32_t *order;   /* [T k]        */
     int32_t *pos;     /* [T k]        */
     int32_t *offsets; /* [n_keys + 1] */
+    int32_t *keys;    /* [T k] or null */
 } spmm_route_t;
 
 /* ---------------------------------------------------------------- utilities */
@@ -498,8 +501,8 @@ SPMM_API spmm_status spmm_bcsr_permuted(const spmm_bcsr_t *A, const int32_t *per
  * keys). */
 SPMM_API spmm_status spmm_build_route_workspace_size(int64_t T, int32_t k, int64_t n_keys, size_t *bytes);
 /* Sorts ids[T][k] (device, id_bytes 4 or 8 per signed id, row pitch ldi) into
- * R->order, R->pos and R->offsets (device arrays of the caller; R->T, R->k and
- * R->n_keys are inputs).  Negative ids are dropped choices; an id >= n_keys is
+ * R->order, R->pos, R->offsets and, unless it is null, R->keys (device arrays of
+ * the caller; R->T, R->k and R->n_keys are inputs).  Negative ids are dropped choices; an id >= n_keys is
  * dropped as well and sets SPMM_DEVERR_INDEX.  Equal ids keep their flat order. */
 SPMM_API spmm_status spmm_build_route(const void *ids, int32_t id_bytes, int64_t ldi, const spmm_route_t *R,
                                       void *workspace, size_t workspace_bytes, spmm_stream_t stream);
@@ -529,7 +532,7 @@ SPMM_API spmm_status spmm_embed(const void *table, int64_t V, int64_t H, int64_t
 /* Workspace bytes spmm_embed_grad needs. */
 SPMM_API spmm_status spmm_embed_grad_workspace_size(const spmm_route_t *R, int64_t H, size_t *bytes);
 /* Gradient of spmm_embed for the table: dtable[v] = scale * sum of dy[t] over the
- * tokens with id v, for the route R of the ids (R->k == 1, R->n_keys = V).
+ * tokens with id v, for the route R of the ids (R->k == 1, R->n_keys = V, with keys).
  * accumulate = 0 writes every row (zeros for a row without tokens); accumulate =
  * 1 adds to the rows that have tokens and leaves the others alone.  dtable is
  * V x H of dy's type or fp32 (out_dtype). */

@@ -530,21 +530,24 @@ _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 @dataclass
 class Route:
     """T x k ids sorted by value: order (flat indices, dropped ones last), pos
-    (place of each flat index, -1 if dropped) and offsets (first place per key).
-    All int32 on the device; pos has the ids' shape."""
+    (place of each flat index, -1 if dropped), offsets (first place per key) and,
+    for k = 1, keys (the sorted ids, n_keys if dropped).  All int32 on the device;
+    pos has the ids' shape."""
     T: int
     k: int
     n_keys: int
     order: torch.Tensor
     pos: torch.Tensor
     offsets: torch.Tensor
+    keys: Optional[torch.Tensor] = None
 
     @property
     def n_rows(self) -> int:
         return self.T * self.k
 
     def c(self) -> _lib.RouteT:
-        return _lib.RouteT(self.T, self.k, self.n_keys, _ptr(self.order), _ptr(self.pos), _ptr(self.offsets))
+        return _lib.RouteT(self.T, self.k, self.n_keys, _ptr(self.order), _ptr(self.pos), _ptr(self.offsets),
+                           _ptr(self.keys))
 
 
 def _row_code(dtype) -> int:
@@ -618,7 +621,8 @@ def spmm_build_route(ids: torch.Tensor, n_keys: int, workspace: Optional[torch.T
     if workspace is None and need:
         workspace = _empty(need, torch.uint8, dev, stream)
     R = Route(T, k, n_keys, _empty(T * k, torch.int32, dev, stream), _empty(ids.shape, torch.int32, dev, stream),
-              _empty(max(n_keys, 0) + 1, torch.int32, dev, stream))
+              _empty(max(n_keys, 0) + 1, torch.int32, dev, stream),
+              _empty(T, torch.int32, dev, stream) if k == 1 else None)
     r = R.c()
     _lib.call("spmm_build_route", _ptr(ids), _ID_BYTES[ids.dtype], ids.stride(0) if T > 1 else k, C.byref(r),
               _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),

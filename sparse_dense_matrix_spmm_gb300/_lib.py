@@ -54,7 +54,7 @@ class TvwT(C.Structure):
 
 
 class RouteT(C.Structure):
-    _fields_ = [("T", I64), ("k", I32), ("n_keys", I64), ("order", P), ("pos", P), ("offsets", P)]
+    _fields_ = [("T", I64), ("k", I32), ("n_keys", I64), ("order", P), ("pos", P), ("offsets", P), ("keys", P)]
 
 
 # name -> (restype, argtypes); every function declared in include/spmm_gb300.h

@@ -643,7 +643,7 @@ spmm_status check_experts(const spmm_route_t* R, int64_t la, int64_t da, int64_t
 
 spmm_status spmm_build_route_workspace_size(int64_t T, int32_t k, int64_t n_keys, size_t* bytes) {
     if (!bytes) return SPMM_ERR_NULL;
-    const spmm_route_t R{T, k, n_keys, nullptr, nullptr, nullptr};
+    const spmm_route_t R{T, k, n_keys, nullptr, nullptr, nullptr, nullptr};
     const spmm_status st = check_route(&R, false);
     if (st != SPMM_OK) return st;
     *bytes = route_workspace_bytes(T, k, n_keys);
@@ -743,7 +743,7 @@ spmm_status spmm_embed_grad(const spmm_route_t* R, const void* dy, int64_t lddy,
     if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
     if (H == 0) return SPMM_OK;
     if ((st = check_route(R, true)) != SPMM_OK) return st;
-    if (!dtable || (R->T > 0 && !dy)) return SPMM_ERR_NULL;
+    if (!dtable || (R->T > 0 && (!dy || !R->keys))) return SPMM_ERR_NULL;
     if (misaligned(dy, dtype) || misaligned(dtable, out_dtype)) return SPMM_ERR_SHAPE;
     const size_t need = embed_grad_workspace_bytes(R->T, H);
     if (need && (!workspace || workspace_bytes < need)) return SPMM_ERR_WORKSPACE;

@@ -2,17 +2,18 @@
 // matrix of token ids.
 //   lookup    out    = scale P table          (out[t] = scale table[ids[t]])
 //   gradient  dtable = scale P^T dy           (sums over the tokens of each row)
-// The gradient takes the ids sorted by value (a route with k = 1 over V keys),
-// so every table row is written once, by one CTA, with its tokens added in a
-// fixed order: no atomics on values, the same bits on every run.  A frequent
-// token would leave its row to one CTA for long, so sums of whole chunks of 32
-// sorted tokens that lie inside one row's run are formed first, in parallel, and
-// sums of 32 such chunks in a second step; the row's CTA adds at most 31 tokens,
-// 31 chunks and the groups on each side.  Both kernels are bound by HBM: the
-// gradient by writing V rows.
+// The gradient takes the ids sorted by value (a route with k = 1 over V keys) and
+// reads every row of dy once: a CTA adds up 32 consecutive sorted tokens, writes
+// the rows whose tokens all lie among them, and leaves a partial sum at either
+// end; a second launch joins the partial sums of rows that cross a boundary.  So
+// a frequent token is as parallel as rare ones (one CTA per table row left a row
+// of 1700 tokens to one CTA, 0.7 ms), nothing is added with atomics, and the
+// result has the same bits on every run.  Rows without tokens are zeroed by the
+// first launch's other CTAs, in address order beside the sums: the operator is
+// bound by writing V rows to HBM.
 #include "internal.h"
 #include "rowvec.cuh"
-#include "sm103.cuh"
+#include "sm103_more.cuh"
 
 namespace spmm {
 namespace {
@@ -21,7 +22,9 @@ using namespace rows;
 
 constexpr int kRowThreads = 256;
 constexpr int kFlight = 8;   // rows in flight per thread while summing
-constexpr int kChunk = 32;   // sorted tokens per partial sum, and partial sums per group
+constexpr int kJoin = 16;    // partial sums in flight per thread
+constexpr int kChunk = 32;   // sorted tokens per CTA
+constexpr int kZeroRows = 4; // table rows per CTA that zeroes
 
 struct EmbedArgs {
     const void* table;
@@ -65,129 +68,126 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
 }
 
 struct EmbedGradArgs {
-    const int32_t *order, *offsets;
-    int64_t T, V, H;
+    const int32_t *order, *keys, *offsets;
+    int64_t T, V, H, chunks;
     const void* dy;
     int64_t ldy;
     float scale;
     bool accumulate;
     void* out;
     int64_t ldo;
-    float *chunks, *groups;  // [T / 32][Hp], [T / 1024][Hp]
+    float* partial;  // [chunks][2][Hp]: the run that entered the chunk, the run that leaves it
     int64_t Hp;
 };
 
-// acc += rows at(0) .. at(n - 1) of p, in order.
-template <typename T, int V, typename At>
-__device__ __forceinline__ void add_rows(const T* p, int n, At at, float (&acc)[V]) {
+// out = base + scale acc, the base only when accumulating.
+template <int V, typename TO>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int64_t c, const float (&acc)[V]) {
+    using O = Vec<TO, V>;
+    TO* out = static_cast<TO*>(a.out) + v * a.ldo + c;
+    float f[V] = {};
+    if (a.accumulate) O::unpack(*reinterpret_cast<const typename O::Raw*>(out), f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = fmaf(a.scale, acc[k], f[k]);
+    O::store_cs(out, O::pack(f));
+}
+
+// Blocks [0, chunks x pieces): sums of a chunk's tokens over a piece of the
+// columns.  The blocks after them zero rows without tokens.
+template <typename T, int V, typename TO>
+__global__ void __launch_bounds__(kRowThreads) embed_grad_kernel(const EmbedGradArgs a, int pieces) {
     using X = Vec<T, V>;
+    using O = Vec<TO, V>;
+    __shared__ int32_t token[kChunk], key[kChunk + 2];  // key[i + 1] of token i; neighbours at the ends
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t block = blockIdx.x;
+    if (block >= a.chunks * pieces) {
+        const int64_t v0 = (block - a.chunks * pieces) * kZeroRows;
+        int32_t start[kZeroRows + 1];
+#pragma unroll
+        for (int i = 0; i <= kZeroRows; ++i) start[i] = __ldg(a.offsets + (v0 + i < a.V ? v0 + i : a.V));
+#pragma unroll
+        for (int i = 0; i < kZeroRows; ++i) {
+            if (v0 + i >= a.V || start[i] != start[i + 1]) continue;
+            TO* out = static_cast<TO*>(a.out) + (v0 + i) * a.ldo;
+            for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) O::store_cs(out + c, O::zero());
+        }
+        return;
+    }
+    const int64_t chunk = block / pieces, p0 = chunk * kChunk;
+    const int64_t kept = __ldg(a.offsets + a.V);
+    if (p0 >= kept) return;
+    const int n = static_cast<int>(kept - p0 < kChunk ? kept - p0 : kChunk);
+    if (threadIdx.x < 32) {
+        const int64_t p = p0 + threadIdx.x;
+        token[threadIdx.x] = p < kept ? __ldg(a.order + p) : 0;
+        key[threadIdx.x + 1] = p < kept ? __ldg(a.keys + p) : -1;
+        if (threadIdx.x == 0) {
+            key[0] = p0 > 0 ? __ldg(a.keys + p0 - 1) : -1;
+            key[kChunk + 1] = p0 + kChunk < kept ? __ldg(a.keys + p0 + kChunk) : -1;
+        }
+    }
+    __syncthreads();
+    const int64_t c = ((block - chunk * pieces) * blockDim.x + threadIdx.x) * V;
+    if (c >= a.H) return;
+    const T* dy = static_cast<const T*>(a.dy) + c;
+    bool entered = key[0] == key[1];  // the current run began in an earlier chunk
+    float acc[V] = {};
     for (int i0 = 0; i0 < n; i0 += kFlight) {
         typename X::Raw r[kFlight];
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) r[i] = i0 + i < n ? X::load(p + at(i0 + i)) : X::zero();
+        for (int i = 0; i < kFlight; ++i) r[i] = i0 + i < n ? X::load(dy + token[i0 + i] * a.ldy) : X::zero();
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
+            if (i0 + i >= n) break;
             float f[V];
             X::unpack(r[i], f);
 #pragma unroll
             for (int k = 0; k < V; ++k) acc[k] += f[k];
+            const int32_t v = key[i0 + i + 1];
+            const bool leaves = i0 + i + 1 == n && key[n + 1] == v;
+            if (!leaves && key[i0 + i + 2] == v) continue;
+            if (entered || leaves)
+                Vec<float, V>::store(a.partial + (2 * chunk + (entered ? 0 : 1)) * a.Hp + c, Vec<float, V>::pack(acc));
+            else
+                write_row<V, TO>(a, v, c, acc);
+            entered = false;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = 0.f;
         }
     }
 }
 
-// The row whose run holds sorted place p: the last v with offsets[v] <= p, by a
-// 32-way search of one warp.
-__device__ __forceinline__ int64_t row_of(const int32_t* offsets, int64_t V, int64_t p, int lane) {
-    int64_t lo = 0, hi = V;  // offsets[lo] <= p < offsets[hi]
-    while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 31) / 32, at = lo + step * lane;
-        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldg(offsets + at) <= p);
-        lo += step * (31 - __clz(le));
-        hi = lo + step < hi ? lo + step : hi;
-    }
-    return lo;
-}
-
-// Sums of whole chunks (LEVEL 0: of tokens, LEVEL 1: of chunks) inside one run.
-// Grid (units, column pieces).
-template <typename T, int V, int LEVEL>
-__global__ void __launch_bounds__(kRowThreads) embed_partial_kernel(const EmbedGradArgs a) {
-    constexpr int64_t kSpan = LEVEL ? kChunk * kChunk : kChunk;
-    __shared__ int32_t row[kChunk];
-    __shared__ int whole;
+// Block (chunk - 1, piece): the run that crosses into `chunk` from the chunk it
+// began in.
+template <int V, typename TO>
+__global__ void __launch_bounds__(kRowThreads) embed_join_kernel(const EmbedGradArgs a) {
+    using F = Vec<float, V>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t p0 = blockIdx.x * kSpan;
-    if (threadIdx.x < 32) {
-        bool inside = p0 + kSpan <= __ldg(a.offsets + a.V);
-        if (inside) inside = __ldg(a.offsets + row_of(a.offsets, a.V, p0, threadIdx.x) + 1) >= p0 + kSpan;
-        if (threadIdx.x == 0) whole = inside;
-        if (!LEVEL && inside) row[threadIdx.x] = __ldg(a.order + p0 + threadIdx.x);
-    }
-    __syncthreads();
-    if (!whole) return;
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x) + 1, p = chunk * kChunk;
+    if (p >= __ldg(a.offsets + a.V)) return;
+    const int32_t v = __ldg(a.keys + p);
+    if (__ldg(a.keys + p - 1) != v || __ldg(a.offsets + v) < p - kChunk) return;
+    const int64_t last = (__ldg(a.offsets + v + 1) - 1) / kChunk;
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
     if (c >= a.H) return;
-    float acc[V] = {};
-    if (LEVEL) {
-        const float* src = a.chunks + blockIdx.x * kChunk * a.Hp + c;
-        add_rows<float, V>(src, kChunk, [&](int i) { return i * a.Hp; }, acc);
-        Vec<float, V>::store(a.groups + blockIdx.x * a.Hp + c, Vec<float, V>::pack(acc));
-    } else {
-        add_rows<T, V>(static_cast<const T*>(a.dy) + c, kChunk, [&](int i) { return row[i] * a.ldy; }, acc);
-        Vec<float, V>::store(a.chunks + blockIdx.x * a.Hp + c, Vec<float, V>::pack(acc));
-    }
-}
-
-// kRows table rows per CTA.
-constexpr int kRows = 4;
-
-template <typename T, int V, typename TO>
-__global__ void __launch_bounds__(kRowThreads) embed_grad_kernel(const EmbedGradArgs a) {
-    using O = Vec<TO, V>;
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kRows;
-    int32_t start[kRows + 1];
+    float acc[V];
+    F::unpack(F::load(a.partial + (2 * chunk - 1) * a.Hp + c), acc);
+    for (int64_t q = chunk; q <= last; q += kJoin) {
+        typename F::Raw r[kJoin];
 #pragma unroll
-    for (int i = 0; i <= kRows; ++i) start[i] = __ldg(a.offsets + (v0 + i < a.V ? v0 + i : a.V));
-    const T* dy = static_cast<const T*>(a.dy);
+        for (int i = 0; i < kJoin; ++i) r[i] = q + i <= last ? F::load(a.partial + 2 * (q + i) * a.Hp + c) : F::zero();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int32_t p0 = start[i], p1 = start[i + 1];
-        if (v0 + i >= a.V) return;
-        TO* out = static_cast<TO*>(a.out) + (v0 + i) * a.ldo;
-        if (p0 == p1) {
-            if (!a.accumulate)
-                for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) O::store_cs(out + c, O::zero());
-            continue;
-        }
-        // tokens up to the first whole chunk, chunks up to the first whole group, groups, and back
-        const int32_t c0 = (p0 + kChunk - 1) / kChunk, c1 = max(c0, p1 / kChunk);
-        const bool chunked = c0 < c1;
-        const int32_t g0 = (c0 + kChunk - 1) / kChunk, g1 = max(g0, c1 / kChunk);
-        const bool grouped = g0 < g1;
-        const int32_t t_end = chunked ? c0 * kChunk : p1, c_end = grouped ? g0 * kChunk : c1;
-        for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-            float acc[V] = {};
-            const auto token = [&](int32_t p) { return static_cast<int64_t>(__ldg(a.order + p)) * a.ldy; };
-            add_rows<T, V>(dy + c, t_end - p0, [&](int k) { return token(p0 + k); }, acc);
-            if (chunked) {
-                add_rows<float, V>(a.chunks + c, c_end - c0, [&](int k) { return (c0 + k) * a.Hp; }, acc);
-                if (grouped) {
-                    add_rows<float, V>(a.groups + c, g1 - g0, [&](int k) { return (g0 + k) * a.Hp; }, acc);
-                    add_rows<float, V>(a.chunks + c, c1 - g1 * kChunk, [&](int k) { return (g1 * kChunk + k) * a.Hp; },
-                                       acc);
-                }
-                add_rows<T, V>(dy + c, p1 - c1 * kChunk, [&](int k) { return token(c1 * kChunk + k); }, acc);
-            }
-            float base[V] = {};
-            if (a.accumulate) O::unpack(*reinterpret_cast<const typename O::Raw*>(out + c), base);
+        for (int i = 0; i < kJoin; ++i) {
+            float f[V];
+            F::unpack(r[i], f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] = fmaf(a.scale, acc[k], base[k]);
-            O::store_cs(out + c, O::pack(acc));
+            for (int k = 0; k < V; ++k) acc[k] += f[k];
         }
     }
+    write_row<V, TO>(a, v, c, acc);
 }
 
 int64_t padded(int64_t H) { return (H + 7) / 8 * 8; }
@@ -195,17 +195,18 @@ int64_t padded(int64_t H) { return (H + 7) / 8 * 8; }
 template <typename T, int V, typename TO>
 cudaError_t embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
     const int threads = row_threads(a.H, V, kRowThreads);
-    const unsigned pieces = static_cast<unsigned>((a.H + threads * V - 1) / (threads * V));
-    cudaError_t e = cudaSuccess;
-    if (a.T >= kChunk)
-        e = launch_chained(embed_partial_kernel<T, V, 0>, dim3(static_cast<unsigned>(a.T / kChunk), pieces), threads, 0, 1,
-                           s, a);
-    if (a.T >= kChunk * kChunk && e == cudaSuccess)
-        e = launch_chained(embed_partial_kernel<T, V, 1>, dim3(static_cast<unsigned>(a.T / (kChunk * kChunk)), pieces),
-                           threads, 0, 1, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_chained(embed_grad_kernel<T, V, TO>, static_cast<unsigned>((a.V + kRows - 1) / kRows), threads, 0, 1, s,
-                          a);
+    const int64_t pieces = (a.H + threads * V - 1) / (threads * V);
+    const int64_t zeros = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
+    const int64_t blocks = a.chunks * pieces + zeros;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks >= (int64_t(1) << 31) || pieces >= 65536) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_chained(embed_grad_kernel<T, V, TO>, static_cast<unsigned>(blocks), threads, 0, 1, s, a,
+                                         static_cast<int>(pieces));
+    if (e != cudaSuccess || a.chunks < 2) return e;
+    constexpr int VJ = V > 4 ? 4 : V;  // 16 bytes of a partial sum
+    const int jthreads = row_threads(a.H, VJ, kRowThreads);
+    const dim3 grid(static_cast<unsigned>(a.chunks - 1), static_cast<unsigned>((a.H + jthreads * VJ - 1) / (jthreads * VJ)));
+    return launch_chained(embed_join_kernel<VJ, TO>, grid, jthreads, 0, 1, s, a);
 }
 
 template <typename T, int V>
@@ -232,13 +233,14 @@ spmm_status launch_embed(const void* table, int64_t V, int64_t H, int64_t ldt, i
 }
 
 size_t embed_grad_workspace_bytes(int64_t T, int64_t H) {
-    return static_cast<size_t>(T / kChunk + T / (kChunk * kChunk)) * padded(H) * sizeof(float);
+    return static_cast<size_t>((T + kChunk - 1) / kChunk) * 2 * padded(H) * sizeof(float);
 }
 
 spmm_status launch_embed_grad(const spmm_route_t* R, const void* dy, int64_t ldy, int64_t H, int32_t dtype, float scale,
                               bool accumulate, void* out, int64_t ldo, int32_t out_dtype, void* ws, cudaStream_t s) {
     EmbedGradArgs a{};
     a.order = R->order;
+    a.keys = R->keys;
     a.offsets = R->offsets;
     a.T = R->T;
     a.V = R->n_keys;
@@ -250,8 +252,8 @@ spmm_status launch_embed_grad(const spmm_route_t* R, const void* dy, int64_t ldy
     a.out = out;
     a.ldo = ldo;
     a.Hp = padded(H);
-    a.chunks = static_cast<float*>(ws);
-    a.groups = a.chunks + R->T / kChunk * a.Hp;
+    a.chunks = (R->T + kChunk - 1) / kChunk;
+    a.partial = static_cast<float*>(ws);
     const bool v = rows16(dy, ldy, H, row_elem_bytes(dtype)) && rows16(out, ldo, H, row_elem_bytes(out_dtype));
     const bool f32 = out_dtype == SPMM_F32;
     cudaError_t e;

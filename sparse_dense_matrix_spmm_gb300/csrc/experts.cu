@@ -24,7 +24,7 @@
 // per unit); at the end it writes the zero rows of dropped choices.
 #include "internal.h"
 #include "rowvec.cuh"
-#include "sm103.cuh"
+#include "sm103_more.cuh"
 
 namespace spmm {
 namespace {

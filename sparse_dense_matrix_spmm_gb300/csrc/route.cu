@@ -10,7 +10,7 @@
 // All three move each row once and are bound by HBM.
 #include "internal.h"
 #include "rowvec.cuh"
-#include "sm103.cuh"
+#include "sm103_more.cuh"
 
 namespace spmm {
 namespace {
@@ -46,7 +46,7 @@ struct SortArgs {
     int32_t wide;  // ids are 64-bit
     int32_t k, n, n_keys, passes, bits;
     int32_t chunk;  // elements per CTA, a multiple of kTile
-    int32_t *order, *pos, *offsets;
+    int32_t *order, *pos, *offsets, *keys;  // keys: the sorted keys, or null
     int32_t *keys0, *idx0, *keys1, *idx1;  // results of even and odd passes
     int32_t* table;                    // [passes][CTAs][bins] digit counts
     int* err;
@@ -181,7 +181,8 @@ __device__ __forceinline__ void place_elements(const SortArgs& a, int pass, int3
             } else {
                 ((pass & 1) ? a.idx1 : a.idx0)[p] = f;
             }
-            if (a.passes > 1) ((pass & 1) ? a.keys1 : a.keys0)[p] = key;
+            int32_t* keys = last ? a.keys : (pass & 1) ? a.keys1 : a.keys0;
+            if (keys) keys[p] = key;
             if (next_table) atomicAdd(next_table + p / a.chunk * bins + ((key >> (shift + a.bits)) & (bins - 1)), 1);
         }
         if (tile + kTile < i1) it.load(a, pass, tile + kTile, i1);
@@ -480,12 +481,14 @@ spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, c
     a.order = R->order;
     a.pos = R->pos;
     a.offsets = R->offsets;
+    a.keys = R->keys;
     int32_t* w = static_cast<int32_t*>(ws);
     if (p.passes > 1) {
         a.keys0 = w;
         a.idx0 = w + static_cast<int64_t>(n);
         a.keys1 = w + 2 * static_cast<int64_t>(n);
         a.idx1 = w + 3 * static_cast<int64_t>(n);
+        if (!a.keys) a.keys = (p.passes & 1) ? a.keys0 : a.keys1;  // the offsets are searched in them
         w += 4 * static_cast<int64_t>(n);
     }
     a.table = w;
@@ -502,7 +505,7 @@ spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, c
     if (p.passes > 1 && e == cudaSuccess)
         e = launch_chained(route_offsets_kernel, static_cast<unsigned>(R->n_keys / kOffsetThreads + 1),
                            kOffsetThreads, 0, 1, s,
-                           (p.passes & 1) ? a.keys0 : a.keys1, n, a.n_keys, a.offsets);
+                           a.keys, n, a.n_keys, a.offsets);
     trace_end(SPMM_KERNEL_ROUTE, s);
     return cuda_status(e);
 }

@@ -96,6 +96,27 @@ struct Vec<T, 1> {
     static __device__ __forceinline__ Raw pack(const float (&f)[1]) { return from_f32<T>(f[0]); }
 };
 
+// Four 16-bit values next to four fp32 ones: 8 bytes at once.
+template <typename T>
+struct Vec4x16 {
+    using Raw = uint2;
+    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { __stcs(reinterpret_cast<uint2*>(p), r); }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[4]) {
+        const float2 a = Pair<T>::unpack(r.x), b = Pair<T>::unpack(r.y);
+        f[0] = a.x;
+        f[1] = a.y;
+        f[2] = b.x;
+        f[3] = b.y;
+    }
+    static __device__ __forceinline__ Raw pack(const float (&f)[4]) {
+        return make_uint2(Pair<T>::pack(f[0], f[1]), Pair<T>::pack(f[2], f[3]));
+    }
+};
+template <>
+struct Vec<__half, 4> : Vec4x16<__half> {};
+template <>
+struct Vec<__nv_bfloat16, 4> : Vec4x16<__nv_bfloat16> {};
+
 // Eight fp32 values next to eight 16-bit ones: 32 bytes as two 16-byte moves.
 template <>
 struct Vec<float, 8> {

@@ -27,6 +27,9 @@ def _same_route(R, ids, n_keys):
     assert np.array_equal(R.order.cpu().numpy(), order)
     assert np.array_equal(R.pos.cpu().numpy(), pos)
     assert np.array_equal(R.offsets.cpu().numpy(), offsets)
+    if R.k == 1:
+        flat = np.asarray(ids).reshape(-1)[order]
+        assert np.array_equal(R.keys.cpu().numpy(), np.where((flat < 0) | (flat >= n_keys), n_keys, flat))
 
 
 @pytest.mark.parametrize("dtype", [np.int32, np.int64])

@@ -11,9 +11,9 @@ def L():
     return _lib.load()
 
 
-def _route(T=10, k=2, E=4, order=16, pos=16, offsets=16):
+def _route(T=10, k=2, E=4, order=16, pos=16, offsets=16, keys=16):
     from sparse_dense_matrix_spmm_gb300 import _lib
-    return ctypes.byref(_lib.RouteT(T, k, E, order, pos, offsets))
+    return ctypes.byref(_lib.RouteT(T, k, E, order, pos, offsets, keys))
 
 
 NULL, SHAPE, DTYPE, WORKSPACE, UNSUPPORTED = 1, 2, 3, 5, 8
@@ -21,7 +21,7 @@ NULL, SHAPE, DTYPE, WORKSPACE, UNSUPPORTED = 1, 2, 3, 5, 8
 
 def test_layout():
     from sparse_dense_matrix_spmm_gb300 import _lib
-    assert ctypes.sizeof(_lib.RouteT) == 8 + 8 + 8 + 8 * 3
+    assert ctypes.sizeof(_lib.RouteT) == 8 + 8 + 8 + 8 * 4
 
 
 def test_build_route(L):
@@ -77,6 +77,8 @@ def test_embed(L):
     assert g(_route(**one), 16, 64, 64, 0, 1.0, 2, 16, 64, 0, 16, 1 << 30, None) == SHAPE     # accumulate
     assert g(_route(**one), 16, 64, 64, 0, 1.0, 0, 16, 64, 1, 16, 1 << 30, None) == DTYPE     # bf16 to fp16
     assert g(_route(**one), 16, 64, 64, 0, 1.0, 0, None, 64, 0, 16, 1 << 30, None) == NULL
+    assert g(_route(keys=None, **one), 16, 64, 64, 0, 1.0, 0, 16, 64, 0, 16, 1 << 30, None) == NULL
+    assert g(_route(**one), 16, 64, 64, 0, 1.0, 0, 16, 64, 0, 16, 8, None) == WORKSPACE
     assert g(_route(**one), 16, 60, 64, 0, 1.0, 0, 16, 64, 0, 16, 1 << 30, None) == SHAPE
 
 
