@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass, field
+from functools import cached_property
 from typing import Optional
 
 import torch
@@ -527,7 +528,7 @@ _ROW_DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.f
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-@dataclass
+@dataclass(frozen=True)
 class Route:
     """T x k ids sorted by value: order (flat indices, dropped ones last), pos
     (place of each flat index, -1 if dropped), offsets (first place per key) and,
@@ -549,41 +550,55 @@ class Route:
         return _lib.RouteT(self.T, self.k, self.n_keys, _ptr(self.order), _ptr(self.pos), _ptr(self.offsets),
                            _ptr(self.keys))
 
+    @cached_property
+    def _ref(self):
+        """The C struct, marshalled once: a route does not change after it is built."""
+        return C.byref(self.c())
 
+
+# At decoding sizes the kernels take 2-4 us, so the wrappers below spend as little
+# as they can: addresses go to ctypes as integers, the stream handle comes without
+# a Stream object (3 us), and a route's struct is built once.
 def _row_code(dtype) -> int:
-    if dtype not in _ROW_DT:
+    code = _ROW_DT.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported row dtype {dtype}")
-    return _ROW_DT[dtype]
+    return code
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor whose memory belongs to the stream the kernel runs on."""
+def _handle(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """A new tensor on like's device whose memory belongs to the stream the kernel runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rows(t: torch.Tensor, what: str, rows: int, H: int, dtype, device) -> int:
     """Check a rows x H operand of the type on the device; returns its row pitch."""
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{what} must be on {device} (this library has no CPU path)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != H:
+    if t.shape != (rows, H):
         raise ValueError(f"{what} must be {rows} x {H}, not {tuple(t.shape)}")
-    if H > 1 and rows > 0 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and H > 1 and rows > 0:
         raise ValueError(f"{what} must have contiguous rows")
-    return t.stride(0) if rows > 1 else H
+    return ld if rows > 1 else H
 
 
 def _weights(t: torch.Tensor, what: str, E: int, N: int, K: int, dtype, device):
     """Check an E x N x K operand; returns its row and expert pitches."""
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{what} must be on {device} (this library has no CPU path)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape) != (E, N, K):
+    if t.shape != (E, N, K):
         raise ValueError(f"{what} must be {E} x {N} x {K}, not {tuple(t.shape)}")
     if K > 1 and t.stride(2) != 1:
         raise ValueError(f"{what} must have contiguous rows")
@@ -591,11 +606,12 @@ def _weights(t: torch.Tensor, what: str, E: int, N: int, K: int, dtype, device):
     return ldw, (t.stride(0) if E > 1 else N * ldw)
 
 
-def _route_w(R: Route, w: torch.Tensor, device) -> None:
-    if w.device != device or w.dtype != torch.float32:
+def _route_w(R: Route, w: torch.Tensor, device) -> int:
+    if w.device != device or w.dtype is not torch.float32:
         raise TypeError(f"w must be float32 on {device}")
     if w.numel() != R.n_rows or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous {R.T} x {R.k} tensor")
+    return w.data_ptr()
 
 
 def spmm_build_route_workspace_size(T: int, k: int, n_keys: int) -> int:
@@ -604,58 +620,63 @@ def spmm_build_route_workspace_size(T: int, k: int, n_keys: int) -> int:
     return n.value
 
 
+def _workspace(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor, stream):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one if one is needed."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _empty(like, need, torch.uint8, stream)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def spmm_build_route(ids: torch.Tensor, n_keys: int, workspace: Optional[torch.Tensor] = None,
                      stream=None) -> Route:
     """Sort ids (T, or T x k; int32 or int64) by value.  Negative ids are dropped
     choices; ids >= n_keys are dropped too and set SPMM_DEVERR_INDEX."""
-    _check_dev(ids, workspace)
+    _check_dev(ids)
     if ids.dtype not in _ID_BYTES:
         raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
-    if ids.dim() not in (1, 2):
+    shape = ids.shape
+    if len(shape) not in (1, 2):
         raise ValueError("ids must be T or T x k")
-    T, k = ids.shape[0], (1 if ids.dim() == 1 else ids.shape[1])
-    if ids.dim() == 2 and k > 1 and T > 0 and ids.stride(1) != 1:
+    T, k = shape[0], (1 if len(shape) == 1 else shape[1])
+    if k > 1 and T > 0 and ids.stride(1) != 1:
         raise ValueError("ids must have contiguous rows")
-    dev = ids.device
     need = spmm_build_route_workspace_size(T, k, n_keys)
-    if workspace is None and need:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    R = Route(T, k, n_keys, _empty(T * k, torch.int32, dev, stream), _empty(ids.shape, torch.int32, dev, stream),
-              _empty(max(n_keys, 0) + 1, torch.int32, dev, stream),
-              _empty(T, torch.int32, dev, stream) if k == 1 else None)
-    r = R.c()
-    _lib.call("spmm_build_route", _ptr(ids), _ID_BYTES[ids.dtype], ids.stride(0) if T > 1 else k, C.byref(r),
-              _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-              _stream(stream))
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, ids, stream)
+    i32 = torch.int32
+    R = Route(T, k, n_keys, _empty(ids, T * k, i32, stream), _empty(ids, shape, i32, stream),
+              _empty(ids, n_keys + 1, i32, stream), _empty(ids, T, i32, stream) if k == 1 else None)
+    _lib.call("spmm_build_route", ids.data_ptr(), _ID_BYTES[ids.dtype], ids.stride(0) if T > 1 else k, R._ref, ws_ptr,
+              ws_bytes, _handle(stream, ids.device))
     return R
 
 
 def spmm_dispatch(R: Route, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """xs[p] = x[order[p] // k] for the kept places, zero rows after them."""
-    H, dev = x.shape[-1], R.order.device
-    ldx = _rows(x, "x", R.T, H, x.dtype, dev)
-    code = _row_code(x.dtype)
+    H, dev, dt, rows = x.shape[-1], R.order.device, x.dtype, R.n_rows
+    code, ldx = _row_code(dt), _rows(x, "x", R.T, H, dt, dev)
     if out is None:
-        out = _empty((R.n_rows, H), x.dtype, dev, stream)
-    ldo = _rows(out, "out", R.n_rows, H, x.dtype, dev)
-    r = R.c()
-    _lib.call("spmm_dispatch", C.byref(r), _ptr(x), ldx, _ptr(out), ldo, H, code, _stream(stream))
+        out, ldo = _empty(x, (rows, H), dt, stream), H
+    else:
+        ldo = _rows(out, "out", rows, H, dt, dev)
+    _lib.call("spmm_dispatch", R._ref, x.data_ptr(), ldx, out.data_ptr(), ldo, H, code, _handle(stream, dev))
     return out
 
 
 def spmm_combine(R: Route, ys: torch.Tensor, w: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     """y[t] = sum_j w[t, j] ys[pos[t, j]] over the kept choices (w fp32; None: weights of 1)."""
-    H, dev = ys.shape[-1], R.order.device
-    ldys = _rows(ys, "ys", R.n_rows, H, ys.dtype, dev)
-    code = _row_code(ys.dtype)
-    if w is not None:
-        _route_w(R, w, dev)
+    H, dev, dt = ys.shape[-1], R.order.device, ys.dtype
+    code, ldys = _row_code(dt), _rows(ys, "ys", R.n_rows, H, dt, dev)
+    w_ptr = None if w is None else _route_w(R, w, dev)
     if out is None:
-        out = _empty((R.T, H), ys.dtype, dev, stream)
-    ldo = _rows(out, "out", R.T, H, ys.dtype, dev)
-    r = R.c()
-    _lib.call("spmm_combine", C.byref(r), _ptr(ys), ldys, _ptr(w), _ptr(out), ldo, H, code, _stream(stream))
+        out, ldo = _empty(ys, (R.T, H), dt, stream), H
+    else:
+        ldo = _rows(out, "out", R.T, H, dt, dev)
+    _lib.call("spmm_combine", R._ref, ys.data_ptr(), ldys, w_ptr, out.data_ptr(), ldo, H, code, _handle(stream, dev))
     return out
 
 
@@ -668,18 +689,16 @@ def spmm_combine_grad(R: Route, dy: torch.Tensor, ys: torch.Tensor, w: torch.Ten
                       out: Optional[torch.Tensor] = None, stream=None):
     """Gradients of spmm_combine: (dys, dw) with dys[pos[t, j]] = w[t, j] dy[t] (zero
     rows past the kept places) and dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32, of w's shape."""
-    H, dev = dy.shape[-1], R.order.device
-    lddy = _rows(dy, "dy", R.T, H, dy.dtype, dev)
-    ldys = _rows(ys, "ys", R.n_rows, H, dy.dtype, dev)
-    code = _row_code(dy.dtype)
-    _route_w(R, w, dev)
+    H, dev, dt, rows = dy.shape[-1], R.order.device, dy.dtype, R.n_rows
+    code, lddy, ldys = _row_code(dt), _rows(dy, "dy", R.T, H, dt, dev), _rows(ys, "ys", rows, H, dt, dev)
+    w_ptr = _route_w(R, w, dev)
     if out is None:
-        out = _empty((R.n_rows, H), dy.dtype, dev, stream)
-    ldo = _rows(out, "out", R.n_rows, H, dy.dtype, dev)
-    dw = _empty(w.shape, torch.float32, dev, stream)
-    r = R.c()
-    _lib.call("spmm_combine_grad", C.byref(r), _ptr(dy), lddy, _ptr(ys), ldys, _ptr(w), _ptr(out), ldo, _ptr(dw), H,
-              code, _stream(stream))
+        out, ldo = _empty(dy, (rows, H), dt, stream), H
+    else:
+        ldo = _rows(out, "out", rows, H, dt, dev)
+    dw = _empty(w, w.shape, torch.float32, stream)
+    _lib.call("spmm_combine_grad", R._ref, dy.data_ptr(), lddy, ys.data_ptr(), ldys, w_ptr, out.data_ptr(), ldo,
+              dw.data_ptr(), H, code, _handle(stream, dev))
     return out, dw
 
 
@@ -687,26 +706,26 @@ def spmm_embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: 
                stream=None) -> torch.Tensor:
     """out[t] = scale * table[ids[t]]; a negative id (padding) gives a zero row, an id
     past the table as well and sets SPMM_DEVERR_INDEX."""
-    V, H, dev = table.shape[0], table.shape[-1], table.device
-    ldt = _rows(table, "table", V, H, table.dtype, dev)
-    code = _row_code(table.dtype)
-    if ids.dtype not in _ID_BYTES:
+    V, H, dev, dt = table.shape[0], table.shape[-1], table.device, table.dtype
+    code, ldt = _row_code(dt), _rows(table, "table", V, H, dt, dev)
+    id_bytes = _ID_BYTES.get(ids.dtype)
+    if id_bytes is None:
         raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
     if ids.dim() != 1 or ids.device != dev or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous vector on {dev}")
     T = ids.shape[0]
     if out is None:
-        out = _empty((T, H), table.dtype, dev, stream)
-    ldo = _rows(out, "out", T, H, table.dtype, dev)
-    _lib.call("spmm_embed", _ptr(table), V, H, ldt, code, _ptr(ids), _ID_BYTES[ids.dtype], T, scale, _ptr(out), ldo,
-              _stream(stream))
+        out, ldo = _empty(table, (T, H), dt, stream), H
+    else:
+        ldo = _rows(out, "out", T, H, dt, dev)
+    _lib.call("spmm_embed", table.data_ptr(), V, H, ldt, code, ids.data_ptr(), id_bytes, T, scale, out.data_ptr(), ldo,
+              _handle(stream, dev))
     return out
 
 
 def spmm_embed_grad_workspace_size(R: Route, H: int) -> int:
     n = C.c_size_t(0)
-    r = R.c()
-    _lib.call("spmm_embed_grad_workspace_size", C.byref(r), H, C.byref(n))
+    _lib.call("spmm_embed_grad_workspace_size", R._ref, H, C.byref(n))
     return n.value
 
 
@@ -715,21 +734,17 @@ def spmm_embed_grad(R: Route, dy: torch.Tensor, scale: float = 1.0, out: Optiona
     """Gradient of spmm_embed for the table, from the route of the ids (k = 1, n_keys
     = V): scale * the sum of dy over each row's tokens.  Every row is written, or
     with accumulate the sums are added to out.  out is dy's type (default) or fp32."""
-    H, dev = dy.shape[-1], R.order.device
-    lddy = _rows(dy, "dy", R.T, H, dy.dtype, dev)
-    code = _row_code(dy.dtype)
+    H, dev, dt = dy.shape[-1], R.order.device, dy.dtype
+    code, lddy = _row_code(dt), _rows(dy, "dy", R.T, H, dt, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty((R.n_keys, H), dy.dtype, dev, stream)
-    ldo = _rows(out, "out", R.n_keys, H, out.dtype, dev)
-    need = spmm_embed_grad_workspace_size(R, H)
-    if workspace is None and need:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    r = R.c()
-    _lib.call("spmm_embed_grad", C.byref(r), _ptr(dy), lddy, H, code, scale, 1 if accumulate else 0, _ptr(out), ldo,
-              _row_code(out.dtype), _ptr(workspace),
-              0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+        out, ldo = _empty(dy, (R.n_keys, H), dt, stream), H
+    else:
+        ldo = _rows(out, "out", R.n_keys, H, out.dtype, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, spmm_embed_grad_workspace_size(R, H), dy, stream)
+    _lib.call("spmm_embed_grad", R._ref, dy.data_ptr(), lddy, H, code, scale, 1 if accumulate else 0, out.data_ptr(),
+              ldo, _row_code(out.dtype), ws_ptr, ws_bytes, _handle(stream, dev))
     return out
 
 
@@ -737,51 +752,46 @@ def spmm_experts(R: Route, xs: torch.Tensor, W: torch.Tensor, out: Optional[torc
                  stream=None) -> torch.Tensor:
     """ys[p] = W[e] xs[p] for the rows p of expert e (W is E x N x K, R.n_keys = E);
     zero rows past the kept places.  bf16 or fp16."""
-    dev, E = R.order.device, R.n_keys
+    dev, dt, rows = R.order.device, xs.dtype, R.n_rows
     N, K = W.shape[-2], W.shape[-1]
-    ldx = _rows(xs, "xs", R.n_rows, K, xs.dtype, dev)
-    ldw, lde = _weights(W, "W", E, N, K, xs.dtype, dev)
-    code = _row_code(xs.dtype)
+    code, ldx = _row_code(dt), _rows(xs, "xs", rows, K, dt, dev)
+    ldw, lde = _weights(W, "W", R.n_keys, N, K, dt, dev)
     if out is None:
-        out = _empty((R.n_rows, N), xs.dtype, dev, stream)
-    ldo = _rows(out, "out", R.n_rows, N, xs.dtype, dev)
-    r = R.c()
-    _lib.call("spmm_experts", C.byref(r), _ptr(xs), ldx, _ptr(W), ldw, lde, N, K, code, _ptr(out), ldo,
-              _stream(stream))
+        out, ldo = _empty(xs, (rows, N), dt, stream), N
+    else:
+        ldo = _rows(out, "out", rows, N, dt, dev)
+    _lib.call("spmm_experts", R._ref, xs.data_ptr(), ldx, W.data_ptr(), ldw, lde, N, K, code, out.data_ptr(), ldo,
+              _handle(stream, dev))
     return out
 
 
 def spmm_experts_dx(R: Route, dys: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """dxs[p] = W[e]^T dys[p] for the rows p of expert e; zero rows past the kept places."""
-    dev, E = R.order.device, R.n_keys
+    dev, dt, rows = R.order.device, dys.dtype, R.n_rows
     N, K = W.shape[-2], W.shape[-1]
-    ldy = _rows(dys, "dys", R.n_rows, N, dys.dtype, dev)
-    ldw, lde = _weights(W, "W", E, N, K, dys.dtype, dev)
-    code = _row_code(dys.dtype)
+    code, ldy = _row_code(dt), _rows(dys, "dys", rows, N, dt, dev)
+    ldw, lde = _weights(W, "W", R.n_keys, N, K, dt, dev)
     if out is None:
-        out = _empty((R.n_rows, K), dys.dtype, dev, stream)
-    ldo = _rows(out, "out", R.n_rows, K, dys.dtype, dev)
-    r = R.c()
-    _lib.call("spmm_experts_dx", C.byref(r), _ptr(dys), ldy, _ptr(W), ldw, lde, N, K, code, _ptr(out), ldo,
-              _stream(stream))
+        out, ldo = _empty(dys, (rows, K), dt, stream), K
+    else:
+        ldo = _rows(out, "out", rows, K, dt, dev)
+    _lib.call("spmm_experts_dx", R._ref, dys.data_ptr(), ldy, W.data_ptr(), ldw, lde, N, K, code, out.data_ptr(), ldo,
+              _handle(stream, dev))
     return out
 
 
 def spmm_experts_dw(R: Route, dys: torch.Tensor, xs: torch.Tensor, out: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """dW[e] = sum of dys[p] xs[p]^T over the rows p of expert e (E x N x K; zeros for an unused expert)."""
-    dev, E = R.order.device, R.n_keys
+    dev, dt, rows, E = R.order.device, dys.dtype, R.n_rows, R.n_keys
     N, K = dys.shape[-1], xs.shape[-1]
-    ldy = _rows(dys, "dys", R.n_rows, N, dys.dtype, dev)
-    ldx = _rows(xs, "xs", R.n_rows, K, dys.dtype, dev)
-    code = _row_code(dys.dtype)
+    code, ldy, ldx = _row_code(dt), _rows(dys, "dys", rows, N, dt, dev), _rows(xs, "xs", rows, K, dt, dev)
     if out is None:
-        out = _empty((E, N, K), dys.dtype, dev, stream)
-    ldw, lde = _weights(out, "out", E, N, K, dys.dtype, dev)
-    r = R.c()
-    _lib.call("spmm_experts_dw", C.byref(r), _ptr(dys), ldy, _ptr(xs), ldx, N, K, code, _ptr(out), ldw, lde,
-              _stream(stream))
+        out = _empty(dys, (E, N, K), dt, stream)
+    ldw, lde = _weights(out, "out", E, N, K, dt, dev)
+    _lib.call("spmm_experts_dw", R._ref, dys.data_ptr(), ldy, xs.data_ptr(), ldx, N, K, code, out.data_ptr(), ldw, lde,
+              _handle(stream, dev))
     return out
 
 
