@@ -52,6 +52,22 @@ struct ExpertArgs {
     uint64_t timeout_ns;
 };
 
+// Tensor maps of B.  Row products load an expert's rows in boxes of 128, 64, 32
+// and 16 rows (box_rows); dw uses the first map for its 64 x 64 boxes.
+struct BMaps {
+    CUtensorMap m[4];
+};
+// The next box for `rest` rows (a multiple of 16): at most two boxes and 16
+// unused rows per 128.  Boxes of exactly the rows needed (64 and 16) took 207 us
+// where this takes 188 us (448 rows per expert): every box costs about as
+// much as 32 rows.
+__host__ __device__ constexpr int box_of(int rest) { return rest > 96 ? 0 : rest > 48 ? 1 : rest > 16 ? 2 : 3; }
+__host__ __device__ constexpr int boxed_rows(int nb) {
+    int n = 0;
+    while (n < nb) n += 128 >> box_of(nb - n);
+    return n;
+}
+
 // A work unit: D rows m0.. and columns n0.. (row products: rows p0 + n0 ..) of
 // expert e, `nt` columns computed and `live` of them stored, `steps` stages.
 struct Unit {
@@ -272,8 +288,7 @@ __device__ __forceinline__ void sync_all() {
 // depth).  BMN is dw.
 template <int CG, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
-    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmB16, const ExpertArgs a) {
+    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB, const ExpertArgs a) {
     using G = Ring<CG>;
     constexpr bool DW = BMN;
     extern __shared__ uint8_t smem_raw[];
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) tma_prefetch_desc(&tmA);
-    if (warp == 1 && lane == 0) tma_prefetch_desc(&tmB);
+    if (warp == 1 && lane == 0) tma_prefetch_desc(&tmB.m[0]);
     if (warp == 2) {
         if (CG == 2) {
             tmem_alloc_pair(smem_u32(tslot), 512);
@@ -329,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sync_all<CG>();
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    grid_dep_launch();
+    grid_dep_wait();  // the setup above ran beside the kernel before
     Unit w;
     // the next unit for this warp; false after the last one
     int ui = 0;
@@ -351,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         bool ok = true;
         while (ok && next_unit()) {
-            const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank;
+            const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank, loaded = boxed_rows(nb);
             for (int k = 0; k < w.steps; ++k) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
@@ -381,16 +398,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         const uint32_t sb = st + kABytes;
                         const int boxes = (nb + 63) / 64;
-                        if (arrives)
-                            mbar_arrive_expect_tx(arrive_bar,
-                                                  (DW ? boxes * 8192 : nb * 128) * both);
+                        if (arrives) mbar_arrive_expect_tx(arrive_bar, (DW ? boxes * 8192 : loaded * 128) * both);
                         if (DW) {
-                            for (int i = 0; i < boxes; ++i) load_2d<CG>(sb + i * 8192, &tmB, bar, n0 + 64 * i, w.p0 + d0);
+                            for (int i = 0; i < boxes; ++i)
+                                load_2d<CG>(sb + i * 8192, &tmB.m[0], bar, n0 + 64 * i, w.p0 + d0);
                         } else {
-                            const int row = w.p0 + n0;
-                            int r = 0;
-                            for (; r + 64 <= nb; r += 64) load_2d<CG>(sb + r * 128, &tmB, bar, d0, row + r);
-                            for (; r < nb; r += 16) load_2d<CG>(sb + r * 128, &tmB16, bar, d0, row + r);
+                            for (int r = 0; r < nb;) {
+                                const int b = box_of(nb - r);
+                                load_2d<CG>(sb + r * 128, &tmB.m[b], bar, d0, w.p0 + n0 + r);
+                                r += 128 >> b;
+                            }
                         }
                     }
                 }
@@ -596,28 +613,16 @@ bool rows_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t ld, int64_
 }
 
 template <int CG, bool AMN, bool BMN>
-spmm_status launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB16, const ExpertArgs& a,
-                   int64_t units, const DeviceInfo* dev, cudaStream_t s) {
+spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const ExpertArgs& a, int64_t units,
+                   const DeviceInfo* dev, cudaStream_t s) {
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
     const auto kern = experts_kernel<CG, AMN, BMN>;
     const int slot = kSlotExperts + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
     if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), Ring<CG>::kSmem, slot)) return SPMM_ERR_CUDA;
     const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<CG>::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = CG;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmB16, a);
+    const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, Ring<CG>::kSmem, CG, s, tmA, tmB, a);
     trace_end(SPMM_KERNEL_EXPERTS, s);
-    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by the next call
     return cuda_status(e);
 }
 
@@ -640,19 +645,20 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
     a.timeout_ns = kWaitTimeoutNs;
-    CUtensorMap tmA, tmB, tmB16;
-    if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128) ||
-        !rows_map(&tmB, dtype, rows, ldr, n, a.depth, 64) || !rows_map(&tmB16, dtype, rows, ldr, n, a.depth, 16))
-        return SPMM_ERR_CUDA;
+    CUtensorMap tmA;
+    BMaps tmB;
+    if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128)) return SPMM_ERR_CUDA;
+    for (int i = 0; i < 4; ++i)
+        if (!rows_map(&tmB.m[i], dtype, rows, ldr, n, a.depth, 128u >> i)) return SPMM_ERR_CUDA;
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     // at most this many units: one partial row tile per expert with rows
     const int64_t units = (n / kMaxTile + (n < E ? n : E)) * a.m_tiles;
     if (pair)
-        return transposed ? launch<2, true, false>(tmA, tmB, tmB16, a, units, dev, s)
-                          : launch<2, false, false>(tmA, tmB, tmB16, a, units, dev, s);
-    return transposed ? launch<1, true, false>(tmA, tmB, tmB16, a, units, dev, s)
-                      : launch<1, false, false>(tmA, tmB, tmB16, a, units, dev, s);
+        return transposed ? launch<2, true, false>(tmA, tmB, a, units, dev, s)
+                          : launch<2, false, false>(tmA, tmB, a, units, dev, s);
+    return transposed ? launch<1, true, false>(tmA, tmB, a, units, dev, s)
+                      : launch<1, false, false>(tmA, tmB, a, units, dev, s);
 }
 
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
@@ -675,14 +681,15 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     a.n_tiles = (a.n + kMaxTile - 1) / kMaxTile;
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA;
+    BMaps tmB{};
     // without rows every gradient is zero and no operand is read; the maps then cover the output's memory
     if (!rows_map(&tmA, dtype, n ? dys : dW, n ? ldd : ldw, n ? n : 1, n ? N : K, kDepth) ||
-        !rows_map(&tmB, dtype, n ? xs : dW, n ? ldx : ldw, n ? n : 1, K, kDepth))
+        !rows_map(&tmB.m[0], dtype, n ? xs : dW, n ? ldx : ldw, n ? n : 1, K, kDepth))
         return SPMM_ERR_CUDA;
     const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
-    return pair ? launch<2, true, true>(tmA, tmB, tmB, a, units, dev, s)
-                : launch<1, true, true>(tmA, tmB, tmB, a, units, dev, s);
+    return pair ? launch<2, true, true>(tmA, tmB, a, units, dev, s)
+                : launch<1, true, true>(tmA, tmB, a, units, dev, s);
 }
 
 }  // namespace spmm
