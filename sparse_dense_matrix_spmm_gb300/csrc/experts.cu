@@ -167,23 +167,36 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
 
 // Row products: TMEM lane = feature, column = row of the expert.  Blocks of 8
 // features x 8 rows are transposed on their way to shared memory (32 rows x 32
-// features, 16-byte units XOR-swizzled by row), so that each row leaves in
-// 16-byte pieces of consecutive features.
+// features, 16-byte units XOR-swizzled by row).  A box of 32 live rows leaves as
+// one TMA store; the last rows of a tile, whose successors belong to another
+// expert, in 16-byte pieces.
 template <typename T>
-__device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, uint32_t t, int c0, int c1, int row0,
-                                           int lane, uint32_t stage) {
+__device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
+                                           int c0, int c1, int row0, int lane, uint32_t stage0) {
     T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo;
     const int unit = lane & 3, feature = row0 + 8 * unit;
-    const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
-    for (int c = c0; c < c1; c += 32) {
+    uint32_t stage = stage0;
+    for (int c = c0; c < c1; c += 32, stage ^= kStageOut / 2) {
+        const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
         uint32_t lo[16], hi[16];
         tmem_ld_16x32(t + c, lo);
         tmem_ld_16x32(t + (16u << 16) + c, hi);
         tmem_ld_wait();
+        if (lane == 0) bulk_wait_read<1>();  // the store before last has read this buffer
+        __syncwarp();
 #pragma unroll
         for (int b = 0; b < 4; ++b)  // rows 8 b .. 8 b + 7
             stmatrix_x4_trans(put + b * 512, pack2<T>(lo[4 * b], lo[4 * b + 1]), pack2<T>(lo[4 * b + 2], lo[4 * b + 3]),
                               pack2<T>(hi[4 * b], hi[4 * b + 1]), pack2<T>(hi[4 * b + 2], hi[4 * b + 3]));
+        if (c + 32 <= c1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (row0 < a.m) tma_store_2d(tmOut, stage, row0, w.p0 + w.n0 + c);
+                bulk_commit();
+            }
+            continue;
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -196,13 +209,12 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const Unit& w, u
     }
 }
 
-// dw: lane = row of dW, columns contiguous.  64 columns of the warp's 32 rows
-// are staged in shared memory (16-byte units XOR-swizzled by row) and leave as
-// 128-byte row segments.
+// dw: TMEM lane = row of dW, columns contiguous.  64 columns of the warp's 32
+// rows are staged in shared memory (16-byte units XOR-swizzled by row) and leave
+// as one TMA store, which drops what lies past dW's edges.
 template <typename T>
-__device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uint32_t t, int c0, int c1, int row0,
-                                         int lane, uint32_t stage) {
-    T* out = static_cast<T*>(a.out) + w.e * a.lde + w.n0;
+__device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
+                                         int c0, int c1, int row0, int lane, uint32_t stage) {
     for (int c = c0; c < c1; c += 64) {
         uint32_t v[4][16];
         if (w.steps == 0) {
@@ -215,6 +227,8 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uin
             for (int h = 0; h < 4; ++h) tmem_ld16(t + c + 16 * h, v[h]);
             tmem_ld_wait();
         }
+        if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+        __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const uint32_t* f = &v[u >> 1][8 * (u & 1)];
@@ -222,17 +236,12 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const Unit& w, uin
                          make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
                                     pack2<T>(f[6], f[7])));
         }
+        fence_proxy_async_smem();
         __syncwarp();
-        const int u = lane & 7;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            const uint4 p = ld_shared_v4(stage + r * 128 + ((u ^ (r & 7)) << 4));
-            // columns come in groups of 8 (K % 8 == 0), so a group is stored whole or not at all
-            if (row0 + r < a.m && c + 8 * u < c1)
-                __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * a.ldo + c + 8 * u), p);
+        if (lane == 0) {
+            if (row0 < a.m) tma_store_3d(tmOut, stage, w.n0 + c, row0, w.e);
+            bulk_commit();
         }
-        __syncwarp();
     }
 }
 
@@ -288,7 +297,8 @@ __device__ __forceinline__ void sync_all() {
 // depth).  BMN is dw.
 template <int CG, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
-    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB, const ExpertArgs a) {
+    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
+                   const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a) {
     using G = Ring<CG>;
     constexpr bool DW = BMN;
     extern __shared__ uint8_t smem_raw[];
@@ -331,6 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0 && lane == 0) tma_prefetch_desc(&tmA);
     if (warp == 1 && lane == 0) tma_prefetch_desc(&tmB.m[0]);
+    // The setup above runs beside the end of the kernel before.  TMEM is taken only after it has
+    // ended (it may still want TMEM of its own) and before the next kernel may start.
+    grid_dep_wait();
     if (warp == 2) {
         if (CG == 2) {
             tmem_alloc_pair(smem_u32(tslot), 512);
@@ -345,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     grid_dep_launch();
-    grid_dep_wait();  // the setup above ran beside the kernel before
     Unit w;
     // the next unit for this warp; false after the last one
     int ui = 0;
@@ -564,13 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = half * (kMaxTile / 2), c1 = min(w.live, c0 + kMaxTile / 2);
             if (DW) {
                 if (a.bf16)
-                    store_dw<__nv_bfloat16>(a, w, t, c0, c1, row0, lane, stage);
+                    store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
                 else
-                    store_dw<__half>(a, w, t, c0, c1, row0, lane, stage);
+                    store_dw<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
             } else if (a.bf16) {
-                store_rows<__nv_bfloat16>(a, w, t, c0, c1, row0, lane, stage);
+                store_rows<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
             } else {
-                store_rows<__half>(a, w, t, c0, c1, row0, lane, stage);
+                store_rows<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
             }
             if (w.steps == 0) continue;
             tc_fence_before();
@@ -585,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
+        if (lane == 0) bulk_wait<0>();  // this warp's stores have completed
     }
 
     tc_fence_before();
@@ -613,15 +626,16 @@ bool rows_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t ld, int64_
 }
 
 template <int CG, bool AMN, bool BMN>
-spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const ExpertArgs& a, int64_t units,
-                   const DeviceInfo* dev, cudaStream_t s) {
+spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const CUtensorMap& tmOut, const ExpertArgs& a,
+                   int64_t units, const DeviceInfo* dev, cudaStream_t s) {
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
     const auto kern = experts_kernel<CG, AMN, BMN>;
     const int slot = kSlotExperts + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
     if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), Ring<CG>::kSmem, slot)) return SPMM_ERR_CUDA;
     const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, Ring<CG>::kSmem, CG, s, tmA, tmB, a);
+    const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, Ring<CG>::kSmem, CG, s, tmA, tmB,
+                                         tmOut, a);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
 }
@@ -645,20 +659,23 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
     a.timeout_ns = kWaitTimeoutNs;
-    CUtensorMap tmA;
+    CUtensorMap tmA, tmOut;
     BMaps tmB;
     if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128)) return SPMM_ERR_CUDA;
     for (int i = 0; i < 4; ++i)
         if (!rows_map(&tmB.m[i], dtype, rows, ldr, n, a.depth, 128u >> i)) return SPMM_ERR_CUDA;
+    if (!encode_tmap_2d(&tmOut, half_type(dtype), out, static_cast<uint64_t>(a.m), static_cast<uint64_t>(n),
+                        static_cast<uint64_t>(ldo) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return SPMM_ERR_CUDA;
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     // at most this many units: one partial row tile per expert with rows
     const int64_t units = (n / kMaxTile + (n < E ? n : E)) * a.m_tiles;
     if (pair)
-        return transposed ? launch<2, true, false>(tmA, tmB, a, units, dev, s)
-                          : launch<2, false, false>(tmA, tmB, a, units, dev, s);
-    return transposed ? launch<1, true, false>(tmA, tmB, a, units, dev, s)
-                      : launch<1, false, false>(tmA, tmB, a, units, dev, s);
+        return transposed ? launch<2, true, false>(tmA, tmB, tmOut, a, units, dev, s)
+                          : launch<2, false, false>(tmA, tmB, tmOut, a, units, dev, s);
+    return transposed ? launch<1, true, false>(tmA, tmB, tmOut, a, units, dev, s)
+                      : launch<1, false, false>(tmA, tmB, tmOut, a, units, dev, s);
 }
 
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
@@ -681,15 +698,16 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     a.n_tiles = (a.n + kMaxTile - 1) / kMaxTile;
-    CUtensorMap tmA;
+    CUtensorMap tmA, tmOut;
     BMaps tmB{};
+    if (!weights_map(&tmOut, dtype, dW, ldw, lde, N, K, a.E, 32)) return SPMM_ERR_CUDA;
     // without rows every gradient is zero and no operand is read; the maps then cover the output's memory
     if (!rows_map(&tmA, dtype, n ? dys : dW, n ? ldd : ldw, n ? n : 1, n ? N : K, kDepth) ||
         !rows_map(&tmB.m[0], dtype, n ? xs : dW, n ? ldx : ldw, n ? n : 1, K, kDepth))
         return SPMM_ERR_CUDA;
     const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
-    return pair ? launch<2, true, true>(tmA, tmB, a, units, dev, s)
-                : launch<1, true, true>(tmA, tmB, a, units, dev, s);
+    return pair ? launch<2, true, true>(tmA, tmB, tmOut, a, units, dev, s)
+                : launch<1, true, true>(tmA, tmB, tmOut, a, units, dev, s);
 }
 
 }  // namespace spmm
