@@ -659,16 +659,18 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
     a.timeout_ns = kWaitTimeoutNs;
+    const bool pair = a.m > 128;
+    a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     CUtensorMap tmA, tmOut;
-    BMaps tmB;
+    BMaps tmB{};
     if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128)) return SPMM_ERR_CUDA;
-    for (int i = 0; i < 4; ++i)
+    // the boxes that a tile of an expert with at most n rows can ask for (encoding a map costs the host 1-2 us)
+    const int64_t most = ((n < kMaxTile ? n : kMaxTile) + 31) / 32 * 32 / (pair ? 2 : 1);
+    for (int i = box_of(static_cast<int>(most)); i < 4; ++i)
         if (!rows_map(&tmB.m[i], dtype, rows, ldr, n, a.depth, 128u >> i)) return SPMM_ERR_CUDA;
     if (!encode_tmap_2d(&tmOut, half_type(dtype), out, static_cast<uint64_t>(a.m), static_cast<uint64_t>(n),
                         static_cast<uint64_t>(ldo) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return SPMM_ERR_CUDA;
-    const bool pair = a.m > 128;
-    a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     // at most this many units: one partial row tile per expert with rows
     const int64_t units = (n / kMaxTile + (n < E ? n : E)) * a.m_tiles;
     if (pair)
