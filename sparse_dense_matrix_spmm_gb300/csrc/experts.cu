@@ -34,9 +34,9 @@ using namespace ptx;
 constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, 128 columns each
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzle row
-constexpr int kMaxTile = 256;    // columns of D per unit
 constexpr int kABytes = 128 * 128;
-constexpr int kStageOut = 4096;  // per epilogue warp
+constexpr int kSmemMax = 232448;  // 227 KB, the most a CTA can have
+constexpr int kFewRows = 16;     // rows per expert up to which row tiles are 64 instead of 256
 constexpr int kUnits = 4;        // work units announced ahead
 
 struct ExpertArgs {
@@ -91,7 +91,7 @@ __device__ __forceinline__ void tile_of(int i, int m_tiles, int n_tiles, int& mt
     nt = g * kGroup + rest - mt * width;
 }
 
-template <int CG, bool DW>
+template <int CG, int TILE, bool DW>
 struct Walk {
     const ExpertArgs& a;
     int lane, e0 = 0, base = 0, start = 0, cnt = 0, incl = 0;
@@ -102,7 +102,7 @@ struct Walk {
         const int e = e0 + lane;
         start = e < a.E ? __ldg(a.offsets + e) : 0;
         cnt = e < a.E ? __ldg(a.offsets + e + 1) - start : 0;
-        incl = (cnt + kMaxTile - 1) / kMaxTile * a.m_tiles;
+        incl = (cnt + TILE - 1) / TILE * a.m_tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -119,8 +119,8 @@ struct Walk {
             w.p0 = __ldg(a.offsets + w.e);
             w.cnt = __ldg(a.offsets + w.e + 1) - w.p0;
             w.m0 = mt * 128 * CG;
-            w.n0 = nt * kMaxTile;
-            w.live = min(kMaxTile, a.n - w.n0);
+            w.n0 = nt * TILE;
+            w.live = min(TILE, a.n - w.n0);
             w.nt = (w.live + 16 * CG - 1) / (16 * CG) * (16 * CG);
             w.steps = (w.cnt + kDepth - 1) / kDepth;
             return true;
@@ -137,7 +137,7 @@ struct Walk {
         w.e = e0 + l;
         w.p0 = __shfl_sync(0xffffffffu, start, l);
         w.cnt = __shfl_sync(0xffffffffu, cnt, l);
-        const int tiles = (w.cnt + kMaxTile - 1) / kMaxTile;
+        const int tiles = (w.cnt + TILE - 1) / TILE;
         const int i = u - base - (__shfl_sync(0xffffffffu, incl, l) - tiles * a.m_tiles);
         int mt, nt;
         tile_of(i, a.m_tiles, tiles, mt, nt);
@@ -151,13 +151,20 @@ struct Walk {
     }
 };
 
-template <int CG>
+// Shared memory: the ring of stages, as deep as fits, two staging buffers per
+// epilogue warp (32 x 32 results of a row product, 32 x 64 of dw), barriers, units.
+template <int CG, int TILE, bool DW>
 struct Ring {
-    static constexpr int kBBytes = kMaxTile / CG * 128;
+    static constexpr int kBBytes = TILE / CG * 128;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = CG == 1 ? 4 : 6;
+    static constexpr int kBox = DW ? 4096 : 2048;  // one staging buffer
+    static constexpr int kOut = 2 * kBox;
+    static constexpr int kStages = (kSmemMax - 1024 - kEpiWarps * kOut - 1536) / kStage;
     static constexpr int kBars = 4 * kStages + 5 + 2 * kUnits;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageOut + kBars * 8 + 16 + kUnits * static_cast<int>(sizeof(Unit));
+    static constexpr int kBarOff = kStages * kStage + kEpiWarps * kOut;
+    static constexpr int kUnitOff = kBarOff + kBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kUnitOff + kUnits * static_cast<int>(sizeof(Unit));
+    static_assert(kSmem <= kSmemMax && kStages <= 16, "fits an SM; barrier phases fit a word");
 };
 
 template <typename T>
@@ -172,11 +179,11 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
 // expert, in 16-byte pieces.
 template <typename T>
 __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
-                                           int c0, int c1, int row0, int lane, uint32_t stage0) {
+                                           int c0, int c1, int row0, int lane, uint32_t buffers) {
     T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo;
     const int unit = lane & 3, feature = row0 + 8 * unit;
-    uint32_t stage = stage0;
-    for (int c = c0; c < c1; c += 32, stage ^= kStageOut / 2) {
+    for (int c = c0, odd = 0; c < c1; c += 32, odd ^= 1) {
+        const uint32_t stage = buffers + odd * 2048;
         const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
         uint32_t lo[16], hi[16];
         tmem_ld_16x32(t + c, lo);
@@ -214,8 +221,9 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
 // as one TMA store, which drops what lies past dW's edges.
 template <typename T>
 __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
-                                         int c0, int c1, int row0, int lane, uint32_t stage) {
-    for (int c = c0; c < c1; c += 64) {
+                                         int c0, int c1, int row0, int lane, uint32_t buffers) {
+    for (int c = c0, odd = 0; c < c1; c += 64, odd ^= 1) {
+        const uint32_t stage = buffers + odd * 4096;
         uint32_t v[4][16];
         if (w.steps == 0) {
 #pragma unroll
@@ -227,7 +235,7 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap*
             for (int h = 0; h < 4; ++h) tmem_ld16(t + c + 16 * h, v[h]);
             tmem_ld_wait();
         }
-        if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+        if (lane == 0) bulk_wait_read<1>();  // the store before last has read this buffer
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -295,18 +303,18 @@ __device__ __forceinline__ void sync_all() {
 
 // AMN / BMN: the operand's contiguous direction is D's row / column (else the
 // depth).  BMN is dw.
-template <int CG, bool AMN, bool BMN>
+template <int CG, int TILE, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
                    const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a) {
-    using G = Ring<CG>;
     constexpr bool DW = BMN;
+    using G = Ring<CG, TILE, DW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     const uint32_t out0 = s0 + G::kStages * G::kStage;
-    const uint32_t bar0 = out0 + kEpiWarps * kStageOut;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + G::kStages * G::kStage + kEpiWarps * kStageOut + 8 * G::kBars);
+    const uint32_t bar0 = s0 + G::kBarOff;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 8 * G::kBars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (G::kStages + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * G::kStages + b); };
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto zeroed_bar = [&](int s) { return done_bar + 8u + 8u * (G::kStages + s); };
     auto unitf_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + i); };
     auto unite_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + kUnits + i); };
-    Unit* ring = reinterpret_cast<Unit*>(tslot + 4);
+    Unit* ring = reinterpret_cast<Unit*>(smem + G::kUnitOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
@@ -346,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dep_wait();
     if (warp == 2) {
         if (CG == 2) {
-            tmem_alloc_pair(smem_u32(tslot), 512);
+            tmem_alloc_pair(smem_u32(tslot), 2 * TILE);
             tmem_relinquish_pair();
         } else {
-            tmem_alloc(smem_u32(tslot), 512);
+            tmem_alloc(smem_u32(tslot), 2 * TILE);
             tmem_relinquish();
         }
     }
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : mbar_wait(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)))
                 break;
             tc_fence_after();
-            const uint32_t d = tmem + static_cast<uint32_t>(acc * kMaxTile);
+            const uint32_t d = tmem + static_cast<uint32_t>(acc * TILE);
             const uint32_t idesc = idesc_f16(128 * CG, w.nt, a.bf16 != 0, AMN, BMN, false);
             // whole stages; the loop stays warp-uniform around the one issuing thread, which keeps the
             // descriptors in uniform registers
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
     } else if (warp == 3) {
         // ------------------------------------------------ work units, and the zero rows of dropped choices
-        Walk<CG, DW> walk(a, lane);
+        Walk<CG, TILE, DW> walk(a, lane);
         bool more = true;
         for (int u = group; more; u += groups) {
             more = walk.find(u, w);
@@ -562,18 +570,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------ epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter, half of the columns
-        const uint32_t stage = out0 + (warp - 4) * kStageOut;
+        const uint32_t stage = out0 + (warp - 4) * G::kOut;
         int acc = 0;
         uint32_t aph = 0;
         while (next_unit()) {
             const int row0 = w.m0 + 128 * rank + 32 * q;
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kMaxTile);
+            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * TILE);
             if (w.steps > 0) {
                 if (!mbar_wait(accf_bar(acc), aph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
                 tc_fence_after();
             }
             // columns past the live ones of this warp's half are computed but not stored
-            const int c0 = half * (kMaxTile / 2), c1 = min(w.live, c0 + kMaxTile / 2);
+            const int c0 = half * (TILE / 2), c1 = min(w.live, c0 + TILE / 2);
             if (DW) {
                 if (a.bf16)
                     store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
@@ -606,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
         tc_fence_after();
         if (CG == 2)
-            tmem_dealloc_pair(tmem, 512);
+            tmem_dealloc_pair(tmem, 2 * TILE);
         else
-            tmem_dealloc(tmem, 512);
+            tmem_dealloc(tmem, 2 * TILE);
     }
 }
 
@@ -625,16 +633,17 @@ bool rows_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t ld, int64_
                           static_cast<uint64_t>(ld) * 2, kDepth, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int CG, bool AMN, bool BMN>
+template <int CG, int TILE, bool AMN, bool BMN>
 spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const CUtensorMap& tmOut, const ExpertArgs& a,
                    int64_t units, const DeviceInfo* dev, cudaStream_t s) {
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
-    const auto kern = experts_kernel<CG, AMN, BMN>;
-    const int slot = kSlotExperts + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
-    if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), Ring<CG>::kSmem, slot)) return SPMM_ERR_CUDA;
+    const auto kern = experts_kernel<CG, TILE, AMN, BMN>;
+    constexpr int smem = Ring<CG, TILE, BMN>::kSmem;
+    constexpr int slot = kSlotExperts + (TILE < 256 ? 6 : 0) + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
+    if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, slot)) return SPMM_ERR_CUDA;
     const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, Ring<CG>::kSmem, CG, s, tmA, tmB,
+    const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, smem, CG, s, tmA, tmB,
                                          tmOut, a);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
@@ -661,23 +670,27 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     a.timeout_ns = kWaitTimeoutNs;
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
+    const int tile = pair && n <= E * kFewRows ? 64 : 256;
     CUtensorMap tmA, tmOut;
     BMaps tmB{};
     if (!weights_map(&tmA, dtype, W, ldw, lde, N, K, E, transposed ? kDepth : 128)) return SPMM_ERR_CUDA;
     // the boxes that a tile of an expert with at most n rows can ask for (encoding a map costs the host 1-2 us)
-    const int64_t most = ((n < kMaxTile ? n : kMaxTile) + 31) / 32 * 32 / (pair ? 2 : 1);
+    const int64_t most = ((n < tile ? n : tile) + 31) / 32 * 32 / (pair ? 2 : 1);
     for (int i = box_of(static_cast<int>(most)); i < 4; ++i)
         if (!rows_map(&tmB.m[i], dtype, rows, ldr, n, a.depth, 128u >> i)) return SPMM_ERR_CUDA;
     if (!encode_tmap_2d(&tmOut, half_type(dtype), out, static_cast<uint64_t>(a.m), static_cast<uint64_t>(n),
                         static_cast<uint64_t>(ldo) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return SPMM_ERR_CUDA;
     // at most this many units: one partial row tile per expert with rows
-    const int64_t units = (n / kMaxTile + (n < E ? n : E)) * a.m_tiles;
+    const int64_t units = (n / tile + (n < E ? n : E)) * a.m_tiles;
+    if (tile == 64)
+        return transposed ? launch<2, 64, true, false>(tmA, tmB, tmOut, a, units, dev, s)
+                          : launch<2, 64, false, false>(tmA, tmB, tmOut, a, units, dev, s);
     if (pair)
-        return transposed ? launch<2, true, false>(tmA, tmB, tmOut, a, units, dev, s)
-                          : launch<2, false, false>(tmA, tmB, tmOut, a, units, dev, s);
-    return transposed ? launch<1, true, false>(tmA, tmB, tmOut, a, units, dev, s)
-                      : launch<1, false, false>(tmA, tmB, tmOut, a, units, dev, s);
+        return transposed ? launch<2, 256, true, false>(tmA, tmB, tmOut, a, units, dev, s)
+                          : launch<2, 256, false, false>(tmA, tmB, tmOut, a, units, dev, s);
+    return transposed ? launch<1, 256, true, false>(tmA, tmB, tmOut, a, units, dev, s)
+                      : launch<1, 256, false, false>(tmA, tmB, tmOut, a, units, dev, s);
 }
 
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
@@ -699,7 +712,7 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     a.timeout_ns = kWaitTimeoutNs;
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
-    a.n_tiles = (a.n + kMaxTile - 1) / kMaxTile;
+    a.n_tiles = (a.n + 255) / 256;
     CUtensorMap tmA, tmOut;
     BMaps tmB{};
     if (!weights_map(&tmOut, dtype, dW, ldw, lde, N, K, a.E, 32)) return SPMM_ERR_CUDA;
@@ -708,8 +721,8 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
         !rows_map(&tmB.m[0], dtype, n ? xs : dW, n ? ldx : ldw, n ? n : 1, K, kDepth))
         return SPMM_ERR_CUDA;
     const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
-    return pair ? launch<2, true, true>(tmA, tmB, tmOut, a, units, dev, s)
-                : launch<1, true, true>(tmA, tmB, tmOut, a, units, dev, s);
+    return pair ? launch<2, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s)
+                : launch<1, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s);
 }
 
 }  // namespace spmm

@@ -60,7 +60,7 @@ spmm_status check_24_call(const spmm_24_t* A, const void* B, int64_t ldb, const 
 void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
-// First of the six slots of set_smem_attr_once that the experts' kernels take
+// First of the twelve slots of set_smem_attr_once that the experts' kernels take
 // (0-23 belong to the format kernels).
 enum : int { kSlotExperts = 24 };
 
