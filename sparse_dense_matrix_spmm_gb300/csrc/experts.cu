@@ -37,6 +37,7 @@ constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzl
 constexpr int kABytes = 128 * 128;
 constexpr int kSmemMax = 232448;  // 227 KB, the most a CTA can have
 constexpr int kFewRows = 16;     // rows per expert up to which row tiles are 64 instead of 256
+constexpr int kVecMost = 16;     // rows in all up to which the forward product runs on CUDA cores
 constexpr int kUnits = 4;        // work units announced ahead
 
 struct ExpertArgs {
@@ -179,10 +180,11 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
 // expert, in 16-byte pieces.
 template <typename T>
 __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
-                                           int c0, int c1, int row0, int lane, uint32_t buffers) {
+                                           int c0, int c1, int row0, int lane, uint32_t buffers,
+                                           int& odd) {
     T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo;
     const int unit = lane & 3, feature = row0 + 8 * unit;
-    for (int c = c0, odd = 0; c < c1; c += 32, odd ^= 1) {
+    for (int c = c0; c < c1; c += 32, odd ^= 1) {
         const uint32_t stage = buffers + odd * 2048;
         const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
         uint32_t lo[16], hi[16];
@@ -212,6 +214,7 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
             // features come in groups of 8 (N % 8 == 0), so a group is stored whole or not at all
             if (feature < a.m && c + r < c1) __stcs(reinterpret_cast<uint4*>(out + (c + r) * a.ldo + feature), p);
         }
+        if (lane == 0) bulk_commit();  // an empty group: one per use of a buffer
         __syncwarp();
     }
 }
@@ -221,8 +224,8 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
 // as one TMA store, which drops what lies past dW's edges.
 template <typename T>
 __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
-                                         int c0, int c1, int row0, int lane, uint32_t buffers) {
-    for (int c = c0, odd = 0; c < c1; c += 64, odd ^= 1) {
+                                         int c0, int c1, int row0, int lane, uint32_t buffers, int& odd) {
+    for (int c = c0; c < c1; c += 64, odd ^= 1) {
         const uint32_t stage = buffers + odd * 4096;
         uint32_t v[4][16];
         if (w.steps == 0) {
@@ -572,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter, half of the columns
         const uint32_t stage = out0 + (warp - 4) * G::kOut;
         int acc = 0;
+        int odd = 0;  // the staging buffers alternate across units too: only the newest store may be unread
         uint32_t aph = 0;
         while (next_unit()) {
             const int row0 = w.m0 + 128 * rank + 32 * q;
@@ -584,13 +588,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = half * (TILE / 2), c1 = min(w.live, c0 + TILE / 2);
             if (DW) {
                 if (a.bf16)
-                    store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
+                    store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
                 else
-                    store_dw<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
+                    store_dw<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
             } else if (a.bf16) {
-                store_rows<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
+                store_rows<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
             } else {
-                store_rows<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage);
+                store_rows<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
             }
             if (w.steps == 0) continue;
             tc_fence_before();
@@ -618,6 +622,113 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
             tmem_dealloc(tmem, 2 * TILE);
     }
+}
+
+// ---------------------------------------------------------------- a token or two
+// The forward product of very few rows: dot products on CUDA cores.  A pair of
+// the kernel above streams weights at 60-67 GB/s per SM whatever its depth of
+// stages, and one token with 8 experts of 1536 features makes 48 pairs; here
+// every warp takes two weight rows, so the read spreads over all SMs.  Measured
+// (one token, 8 of 128 experts, 1536 x 4096 bf16): 20.3 us against 22.9 us, 2 of
+// 16 experts, 4096 x 14336: 38 us (6.2 TB/s) against 60 us; two tokens 32 us
+// against 43 us.  At four tokens the two are even, and rows that share an expert
+// read its weights once per four rows here (16 tokens, 2 of 8 experts: 67 us
+// against 44 us), hence the limit of 16 rows.
+struct VecArgs {
+    const int32_t* offsets;
+    int32_t E;
+    const void *xs, *W;
+    int64_t ldx, ldw, lde;
+    int32_t N, K;
+    void* out;
+    int64_t ldo;
+};
+constexpr int kVecWarps = 8, kVecRows = 4, kVecFeatures = 2 * kVecWarps;
+
+// Two weight rows with C rows of xs.
+template <typename T, int C>
+__device__ __forceinline__ void dot_rows(const VecArgs& a, const T* w0, const T* w1, const T* x, T* out, bool two,
+                                         int lane) {
+    using V = rows::Vec<T, 8>;
+    float acc[2][C] = {};
+    constexpr int kFlight = 2;  // per weight row; 4 spilled at four CTAs per SM
+    for (int k0 = lane * 8; k0 < a.K; k0 += 256 * kFlight) {
+        uint4 r[2][kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int k = k0 + 256 * i;
+            r[0][i] = k < a.K ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : V::zero();
+            r[1][i] = k < a.K ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : V::zero();
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int k = k0 + 256 * i;
+            if (k >= a.K) break;
+            float f0[8], f1[8];
+            V::unpack(r[0][i], f0);
+            V::unpack(r[1][i], f1);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float v[8];
+                V::unpack(V::load(x + c * a.ldx + k), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[0][c] = fmaf(f0[j], v[j], acc[0][c]);
+                    acc[1][c] = fmaf(f1[j], v[j], acc[1][c]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int s = 16; s; s >>= 1) {
+            acc[0][c] += __shfl_xor_sync(0xffffffffu, acc[0][c], s);
+            acc[1][c] += __shfl_xor_sync(0xffffffffu, acc[1][c], s);
+        }
+        if (lane == 0) {
+            out[c * a.ldo] = rows::from_f32<T>(acc[0][c]);
+            if (two) out[c * a.ldo + 1] = rows::from_f32<T>(acc[1][c]);
+        }
+    }
+}
+
+// Grid (16 features, sorted place): the CTAs of an expert's first place and of
+// every fourth after it take up to four of its rows, the others leave; places of
+// dropped choices are zeroed.
+template <typename T>
+__global__ void __launch_bounds__(kVecWarps * 32, 4) experts_vec_kernel(const VecArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int p = blockIdx.y, n = (blockIdx.x * kVecWarps + warp) * 2;
+    if (n >= a.N) return;
+    T* out = static_cast<T*>(a.out) + p * a.ldo + n;
+    const bool two = n + 1 < a.N;
+    if (p >= __ldg(a.offsets + a.E)) {
+        if (lane < 2 && (lane == 0 || two)) out[lane] = rows::from_f32<T>(0.f);
+        return;
+    }
+    int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + step * lane;
+        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldg(a.offsets + at) <= p);
+        lo += step * (31 - __clz(le));
+        hi = min(hi, lo + step);
+    }
+    if ((p - __ldg(a.offsets + lo)) % kVecRows) return;
+    const int rows = min(kVecRows, __ldg(a.offsets + lo + 1) - p);
+    const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
+    const T* w0 = static_cast<const T*>(a.W) + lo * a.lde + n * a.ldw;
+    const T* w1 = two ? w0 + a.ldw : w0;
+    if (rows == 1)
+        dot_rows<T, 1>(a, w0, w1, x, out, two, lane);
+    else if (rows == 2)
+        dot_rows<T, 2>(a, w0, w1, x, out, two, lane);
+    else if (rows == 3)
+        dot_rows<T, 3>(a, w0, w1, x, out, two, lane);
+    else
+        dot_rows<T, 4>(a, w0, w1, x, out, two, lane);
 }
 
 bool weights_map(CUtensorMap* map, int32_t dtype, const void* W, int64_t ldw, int64_t lde, int64_t N, int64_t K,
@@ -657,6 +768,17 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     const DeviceInfo* dev = device_info();
     if (!dev) return SPMM_ERR_CUDA;
     const int64_t n = R->T * R->k, E = R->n_keys;
+    if (!transposed && n <= kVecMost) {
+        const VecArgs v{R->offsets, static_cast<int32_t>(E), rows, W,   ldr, ldw, lde, static_cast<int32_t>(N),
+                        static_cast<int32_t>(K), out, ldo};
+        const dim3 grid(static_cast<unsigned>((N + kVecFeatures - 1) / kVecFeatures), static_cast<unsigned>(n));
+        trace_begin(SPMM_KERNEL_EXPERTS, s);
+        const cudaError_t e = dtype == SPMM_BF16
+                                  ? launch_chained(experts_vec_kernel<__nv_bfloat16>, grid, kVecWarps * 32, 0, 1, s, v)
+                                  : launch_chained(experts_vec_kernel<__half>, grid, kVecWarps * 32, 0, 1, s, v);
+        trace_end(SPMM_KERNEL_EXPERTS, s);
+        return cuda_status(e);
+    }
     ExpertArgs a{};
     a.offsets = R->offsets;
     a.E = static_cast<int32_t>(E);

@@ -13,7 +13,7 @@ CASES = [
     ([1], 0, 8, 8), ([0, 1, 0], 0, 16, 24), ([1, 1, 1, 1, 1, 1, 1, 1], 0, 136, 264), ([0, 0, 0], 5, 64, 64),
     ([15, 16, 17, 0, 31, 33], 3, 128, 64), ([63, 64, 65, 1], 0, 72, 200), ([127, 128, 129], 2, 256, 128),
     ([255, 3, 257, 300], 1, 264, 328), ([600, 0, 0, 37], 0, 520, 1000), ([5, 2, 0, 7, 1, 3, 6, 4] * 4, 9, 384, 512),
-    ([1030], 0, 1536, 520),
+    ([1030], 0, 1536, 520), ([5, 2, 0, 7], 2, 200, 584), ([0, 16], 0, 40, 2056), ([0] * 40 + [1, 3], 0, 24, 64),
 ]
 
 
@@ -113,6 +113,28 @@ def test_large_product_sampled():
     # the same bits on every run
     assert torch.equal(spmm.spmm_experts(R, xs, W), ys)
     assert torch.equal(spmm.spmm_experts_dw(R, dys, xs), dw)
+
+
+@pytest.mark.parametrize("N,K,rows", [(264, 328, 5), (520, 72, 70), (712, 200, 33)])
+def test_many_units_per_cta(N, K, rows):
+    """Hundreds of experts, so that every CTA stores many tiles in a row, with odd numbers of
+    64-column and 32-row boxes in them (a staging buffer reused before its store had read it)."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    E = 300
+    R, offsets = _case([rows + e % 3 for e in range(E)], 4, 5)
+    xs, dys = matrix((R.n_rows, K), "bf16", 1), matrix((R.n_rows, N), "bf16", 2)
+    W = matrix((E, N, K), "bf16", 3, K ** -0.5)
+    ys, (dx, dw) = spmm.spmm_experts(R, xs, W), spmm.spmm_experts_grad(R, dys, xs, W)
+    for _ in range(3):
+        assert torch.equal(spmm.spmm_experts_dw(R, dys, xs), dw)
+        assert torch.equal(spmm.spmm_experts(R, xs, W), ys)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        X, D, V = f64(xs[a:b]), f64(dys[a:b]), f64(W[e])
+        check(ys[a:b], X @ V.T, np.abs(X) @ np.abs(V).T, K, "bf16", f"ys of {e}")
+        check(dx[a:b], D @ V, np.abs(D) @ np.abs(V), N, "bf16", f"dxs of {e}")
+        check(dw[e], D.T @ X, np.abs(D).T @ np.abs(X), b - a, "bf16", f"dW of {e}")
 
 
 def test_many_experts_single_tokens():
