@@ -15,7 +15,7 @@
 // multiplying by zero would not do).
 // The sums are fp32 in TMEM, rounded once to the operands' type.
 //
-// Roles per CTA: warp 0 loads A, warp 1 loads B (TMA, 128-byte swizzle, one
+// Roles per CTA: warps 0, 1, 12 and 13 load A and B (TMA, 128-byte swizzle, one
 // ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-11
 // store D (two accumulators of 256 TMEM columns, so a unit's epilogue overlaps
 // the next unit's MMAs).  The host knows no row counts: warp 3 finds this CTA's
@@ -32,7 +32,8 @@ namespace {
 using namespace ptx;
 
 constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, 128 columns each
-constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kMoreProducers = 4 + kEpiWarps;  // first warp of the second pair of producers
+constexpr int kThreads = 32 * (kMoreProducers + 2);
 constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzle row
 constexpr int kABytes = 128 * 128;
 constexpr int kSmemMax = 232448;  // 227 KB, the most a CTA can have
@@ -268,12 +269,12 @@ __device__ __forceinline__ void clear_tail(uint32_t stage, int valid, int end, i
 
 // One CTA (CG = 1) or a pair (CG = 2) per MMA.
 template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc,
-                                    uint32_t issue) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                    uint32_t idesc, uint32_t acc, uint32_t issue) {
     if (CG == 2)
-        mma_f16_pair(d, ad, bd, idesc, acc, issue);
+        mma_f16_pair(d, a_lo, a_hi, b_lo, b_hi, idesc, acc, issue);
     else
-        mma_f16_issue(d, ad, bd, idesc, acc, issue);
+        mma_f16_single(d, a_lo, a_hi, b_lo, b_hi, idesc, acc, issue);
 }
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -334,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
-            mbar_init(full_bar(s), 2);
+            mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
-            mbar_init(tail_bar(s), 2);
+            mbar_init(tail_bar(s), 1);
             mbar_init(zeroed_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(unitf_bar(i), 1);
-            mbar_init(unite_bar(i), 3 + kEpiWarps);  // every warp but the walking one
+            mbar_init(unite_bar(i), kThreads / 32 - 1);  // every warp but the walking one
         }
         mbar_init(done_bar, 1);
         fence_mbar_init();
@@ -385,30 +386,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w.e >= 0;
     };
 
-    if (warp < 2) {
-        // ------------------------------------------------ producers: A (warp 0), B (warp 1)
+    if (warp < 2 || warp >= kMoreProducers) {
+        // ------------------------------------------------ producers
+        // Two pairs of warps, one for even and one for odd steps (counted over all units); in a pair one
+        // warp loads A and the other B.  A TMA instruction costs its warp 100-200 clk, and a single pair
+        // with two boxes per operand needed 560 clk a step where the MMAs need 520.
+        const bool loads_a = (warp & 1) == 0;
+        int turn = warp >= kMoreProducers;  // steps until this warp's next one, modulo 2
         int s = 0, armed = 0;
         uint32_t ph = 0;
+        const uint32_t full0 = CG == 2 ? map_shared(full_bar(0), 0) : full_bar(0);
         bool ok = true;
         while (ok && next_unit()) {
-            const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank, loaded = boxed_rows(nb);
-            for (int k = 0; k < w.steps; ++k) {
-                if (!mbar_wait(empty_bar(s), ph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
+            const int nb = w.nt / CG, m0 = w.m0 + 128 * rank, n0 = w.n0 + nb * rank;
+            const uint32_t b_bytes = DW ? (nb + 63) / 64 * 8192 : boxed_rows(nb) * 128;
+            for (int k = 0; k < w.steps; ++k, turn ^= 1) {
+                if (turn == 0 && !mbar_wait(empty_bar(s), ph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (turn == 0 && lane == 0) {
                     const uint32_t st = s0 + s * G::kStage;
                     const int d0 = k * kDepth;
-                    // A pair's loads all complete on rank 0's barrier, which expects both CTAs' bytes.  A
-                    // dw tail that rank 1 has to clear first completes on rank 1's own barrier instead.
+                    // A pair's loads all complete on rank 0's barrier.  A dw tail that rank 1 has to clear
+                    // first completes on rank 1's own barrier instead.
                     const bool tail = CG == 2 && DW && ((w.cnt - d0) & 15) && w.cnt - d0 < kDepth;
-                    const uint32_t arrive_bar = tail && rank ? tail_bar(s) : full_bar(s);  // of this CTA
-                    const uint32_t bar = CG == 1 || tail ? arrive_bar : map_shared(arrive_bar, 0);
-                    const uint32_t both = tail ? 1 : CG;
-                    const bool arrives = rank == 0 || tail;
-                    if (warp == 0) {
-                        if (arrives) mbar_arrive_expect_tx(arrive_bar, kABytes * both);
+                    const uint32_t own = tail && rank ? tail_bar(s) : full_bar(s);
+                    const uint32_t bar = CG == 1 || tail ? own : full0 + 8u * s;
+                    if (loads_a) {
+                        // the one arrival of the phase, for both warps' copies (and both CTAs', unless
+                        // they wait apart); copies that land before it only lower the count first
+                        if (rank == 0 || tail)
+                            mbar_arrive_expect_tx(own, (kABytes + b_bytes) * (tail ? 1 : CG));
                         if (DW) {
                             load_2d<CG>(st, &tmA, bar, m0, w.p0 + d0);
                             load_2d<CG>(st + kABytes / 2, &tmA, bar, m0 + 64, w.p0 + d0);
@@ -420,11 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         const uint32_t sb = st + kABytes;
-                        const int boxes = (nb + 63) / 64;
-                        if (arrives) mbar_arrive_expect_tx(arrive_bar, (DW ? boxes * 8192 : loaded * 128) * both);
                         if (DW) {
-                            for (int i = 0; i < boxes; ++i)
-                                load_2d<CG>(sb + i * 8192, &tmB.m[0], bar, n0 + 64 * i, w.p0 + d0);
+                            for (int c = 0; c < nb; c += 64)
+                                load_2d<CG>(sb + c * 128, &tmB.m[0], bar, n0 + c, w.p0 + d0);
                         } else {
                             for (int r = 0; r < nb;) {
                                 const int b = box_of(nb - r);
@@ -460,6 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t bdesc0 = BMN ? smem_desc(s0 + kABytes, 8192u, 1024u, SWZ_128B)
                                     : smem_desc(s0 + kABytes, 16u, 1024u, SWZ_128B);
         constexpr uint32_t kAStep = AMN ? 128 : 2, kBStep = BMN ? 128 : 2;
+        const uint32_t a_hi = static_cast<uint32_t>(adesc0 >> 32), b_hi = static_cast<uint32_t>(bdesc0 >> 32);
+        const uint32_t issue = lane == 0;
         int s = 0, acc = 0;
         uint32_t ph = 0, aph = 0, zph = 0;
         bool ok = true;
@@ -474,23 +483,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             // whole stages; the loop stays warp-uniform around the one issuing thread, which keeps the
             // descriptors in uniform registers
             const int whole = DW ? w.cnt / kDepth : w.steps;
+            bool ready = whole > 0 && mbar_test_wait(full_bar(s), ph);
             for (int k = 0; k < whole; ++k) {
-                if (!mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
+                if (!ready && !mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (G::kStage >> 4));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc, (k | kk) != 0 ? 1u : 0u,
-                            lane == 0);
-                if (lane == 0) commit<CG>(empty_bar(s));
-                __syncwarp();
+                const uint32_t so = static_cast<uint32_t>(s) * (G::kStage >> 4), empty = empty_bar(s);
                 if (++s == G::kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
+                // the next stage's test is on its way while this stage's MMAs are issued
+                ready = k + 1 < whole && mbar_test_wait(full_bar(s), ph);
+                const uint32_t a_lo = static_cast<uint32_t>(adesc0) + so, b_lo = static_cast<uint32_t>(bdesc0) + so;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma<CG>(d, a_lo + kAStep * kk, a_hi, b_lo + kBStep * kk, b_hi, idesc, (k | kk) != 0 ? 1u : 0u, issue);
+                if (lane == 0) commit<CG>(empty);
+                __syncwarp();
             }
             if (DW && ok && whole < w.steps) {
                 // the tail: MMAs of 16 rows up to the expert's last, what follows it cleared
@@ -507,9 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 if (lane == 0 && ok) {
-                    const uint64_t so = static_cast<uint32_t>(s) * (G::kStage >> 4);
+                    const uint32_t so = static_cast<uint32_t>(s) * (G::kStage >> 4);
+                    const uint32_t a_lo = static_cast<uint32_t>(adesc0) + so, b_lo = static_cast<uint32_t>(bdesc0) + so;
                     for (int kk = 0; kk < sub; ++kk)
-                        mma<CG>(d, adesc0 + so + kAStep * kk, bdesc0 + so + kBStep * kk, idesc,
+                        mma<CG>(d, a_lo + kAStep * kk, a_hi, b_lo + kBStep * kk, b_hi, idesc,
                                 (whole | kk) != 0 ? 1u : 0u, 1u);
                     commit<CG>(empty_bar(s));
                 }
@@ -570,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = lane; c < a.m / 8; c += 32) row[c] = make_uint4(0, 0, 0, 0);
             }
         }
-    } else {
+    } else {  // warps 4 .. 11
         // ------------------------------------------------ epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter, half of the columns
         const uint32_t stage = out0 + (warp - 4) * G::kOut;
