@@ -77,8 +77,11 @@ struct Unit {
 };
 
 // Maps unit numbers to units.  Called by whole warps; unit numbers must not
-// decrease.  Row products: an expert with c rows has ceil(c / 256) row tiles of
-// nearly equal size times m_tiles units; dw has n_tiles x m_tiles units per
+// decrease.  Row products: an expert with c rows has ceil(c / 256) row tiles
+// times m_tiles units, two tiles of equal size or more of 256 and a rest (320
+// rows: 164 us as 160 + 160, 177 us as 256 + 64, which both read the weights at
+// full length; a prompt batch of ragged experts, sustained: 374 us with full
+// tiles, 380 us with equal ones); dw has n_tiles x m_tiles units per
 // expert.  Inside an expert units go in groups of kGroup column tiles, column
 // tiles fastest, so that the units in flight together (76 pairs) form a compact
 // patch of D and share their operands in L2: with column tiles fastest over the
@@ -143,11 +146,12 @@ struct Walk {
         const int i = u - base - (__shfl_sync(0xffffffffu, incl, l) - tiles * a.m_tiles);
         int mt, nt;
         tile_of(i, a.m_tiles, tiles, mt, nt);
-        const int size = ((w.cnt + tiles - 1) / tiles + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        const int even = ((w.cnt + tiles - 1) / tiles + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        const int size = tiles > 2 ? TILE : even;
         w.m0 = mt * 128 * CG;
         w.n0 = nt * size;
-        w.live = max(0, min(size, w.cnt - w.n0));
-        w.nt = size;
+        w.live = min(size, w.cnt - w.n0);
+        w.nt = (w.live + 16 * CG - 1) / (16 * CG) * (16 * CG);
         w.steps = (a.depth + kDepth - 1) / kDepth;
         return true;
     }
