@@ -25,8 +25,8 @@ using namespace rows;
 // for the CTA that will read it there, so only the first pass has a counting
 // launch.  Inside a tile a warp owns consecutive elements and ranks them with
 // one ballot per digit bit, so the order is that of the input and nothing
-// depends on the order of atomics.  Up to kSmall elements run in one CTA and one
-// launch, where launches would cost more than the work.
+// depends on the order of atomics.  Up to one tile of elements runs in one CTA and
+// one launch (two tiles took it 10.0 us, two launches over two CTAs 7.4 us).
 // The kernels are bound by latency (launches and chains of dependent loads).
 // One cluster of 8 CTAs that ranked with match_any and counted in distributed
 // shared memory took one launch but 56 us for 131072 elements (its 8 SMs' issue
@@ -37,7 +37,7 @@ constexpr int kSortThreads = 512;  // one per bin
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 4;          // per thread and tile
 constexpr int kTile = kSortThreads * kItems;
-constexpr int kSmall = 2 * kTile;
+
 constexpr int kMaxCtas = 128;  // each reads every CTA's counts (256 CTAs for 524288 elements: 30 us in those reads)
 
 struct SortArgs {
@@ -128,80 +128,110 @@ struct Items {
     }
 };
 
+// Ranks of this warp's items among its equal digits, and the digits' counts in
+// its row of s.hist.
+__device__ __forceinline__ void rank_items(const SortArgs& a, int shift, const Items& it, int32_t (&rank)[kItems],
+                                           SortShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << a.bits;
+    const uint32_t before = (1u << lane) - 1u;
+    for (int b = lane; b < bins; b += 32) s.hist[warp][b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+        const bool live = it.key[j] >= 0;
+        const int digit = (it.key[j] >> shift) & (bins - 1);
+        uint32_t peers = __ballot_sync(0xffffffffu, live);  // lanes with the same digit
+#pragma unroll
+        for (int b = 0; b < kDigitBits; ++b) {
+            if (b < a.bits) {
+                const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1);
+                peers &= (digit >> b) & 1 ? set : ~set;
+            }
+        }
+        rank[j] = __popc(peers & before);
+        if (live) rank[j] += s.hist[warp][digit];
+        __syncwarp();
+        if (live && (peers & before) == 0) s.hist[warp][digit] += __popc(peers);
+        __syncwarp();
+    }
+}
+
+// This thread's digit: its counts in the warps' rows become the elements before
+// each warp's; returns their sum.
+__device__ __forceinline__ int32_t scan_warps(SortShared& s, int32_t start) {
+    int32_t c[kSortWarps], run = start;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = s.hist[w][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        s.hist[w][threadIdx.x] = run;
+        run += c[w];
+    }
+    return run - start;
+}
+
+// Writes a tile's items at first(digit) + hist + rank.
+__device__ __forceinline__ void write_items(const SortArgs& a, int pass, const Items& it, const int32_t (&rank)[kItems],
+                                            int32_t* next_table, const SortShared& s, bool add_first) {
+    const int warp = threadIdx.x >> 5, bins = 1 << a.bits, shift = pass * a.bits;
+    const bool last = pass + 1 == a.passes;
+    const int tiles = a.chunk / kTile;
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+        const int32_t key = it.key[j], f = it.idx[j];
+        if (key < 0) continue;
+        const int digit = (key >> shift) & (bins - 1);
+        const int32_t p = s.hist[warp][digit] + rank[j] + (add_first ? s.first[digit] : 0);
+        if (last) {
+            a.order[p] = f;
+            a.pos[f] = key < a.n_keys ? p : -1;
+        } else {
+            ((pass & 1) ? a.idx1 : a.idx0)[p] = f;
+        }
+        int32_t* keys = last ? a.keys : (pass & 1) ? a.keys1 : a.keys0;
+        if (keys) keys[p] = key;
+        if (next_table) {
+            const int32_t tile = p / kTile, cta = tiles == 1 ? tile : tile / tiles;
+            atomicAdd(next_table + cta * bins + ((key >> (shift + a.bits)) & (bins - 1)), 1);
+        }
+    }
+}
+
 // Writes elements [i0, i1) at their places, a tile at a time; `it` holds the
-// first tile.
+// first tile and s.first the places of the first elements.
 __device__ __forceinline__ void place_elements(const SortArgs& a, int pass, int32_t i0, int32_t i1, Items& it,
                                                int32_t* next_table, SortShared& s) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int bins = 1 << a.bits, shift = pass * a.bits;
-    const bool last = pass + 1 == a.passes;
-    const uint32_t before = (1u << lane) - 1u;
+    const int bins = 1 << a.bits;
     for (int64_t tile = i0; tile < i1; tile += kTile) {
-        for (int b = lane; b < bins; b += 32) s.hist[warp][b] = 0;
-        __syncwarp();
         int32_t rank[kItems];
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-            const bool live = it.key[j] >= 0;
-            const int digit = (it.key[j] >> shift) & (bins - 1);
-            uint32_t peers = __ballot_sync(0xffffffffu, live);  // lanes with the same digit
-#pragma unroll
-            for (int b = 0; b < kDigitBits; ++b) {
-                if (b < a.bits) {
-                    const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1);
-                    peers &= (digit >> b) & 1 ? set : ~set;
-                }
-            }
-            rank[j] = __popc(peers & before);
-            if (live) rank[j] += s.hist[warp][digit];
-            __syncwarp();
-            if (live && (peers & before) == 0) s.hist[warp][digit] += __popc(peers);
-            __syncwarp();
-        }
+        rank_items(a, pass * a.bits, it, rank, s);
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < bins) {
-            int32_t run = s.first[threadIdx.x];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int32_t c = s.hist[w][threadIdx.x];
-                s.hist[w][threadIdx.x] = run;
-                run += c;
-            }
-            s.first[threadIdx.x] = run;
+            const int32_t start = s.first[threadIdx.x];
+            s.first[threadIdx.x] = start + scan_warps(s, start);
         }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-            const int32_t key = it.key[j], f = it.idx[j];
-            if (key < 0) continue;
-            const int32_t p = s.hist[warp][(key >> shift) & (bins - 1)] + rank[j];
-            if (last) {
-                a.order[p] = f;
-                a.pos[f] = key < a.n_keys ? p : -1;
-            } else {
-                ((pass & 1) ? a.idx1 : a.idx0)[p] = f;
-            }
-            int32_t* keys = last ? a.keys : (pass & 1) ? a.keys1 : a.keys0;
-            if (keys) keys[p] = key;
-            if (next_table) atomicAdd(next_table + p / a.chunk * bins + ((key >> (shift + a.bits)) & (bins - 1)), 1);
-        }
+        write_items(a, pass, it, rank, next_table, s, false);
         if (tile + kTile < i1) it.load(a, pass, tile + kTile, i1);
         __syncthreads();
     }
 }
 
-// All passes in one CTA.
+// All passes over one tile in one CTA; the digits' counts come with the ranks.
 __global__ void __launch_bounds__(kSortThreads) route_small_kernel(const SortArgs a) {
     __shared__ SortShared s;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     for (int pass = 0; pass < a.passes; ++pass) {
         Items it;
+        int32_t rank[kItems];
         it.load(a, pass, 0, a.n);
-        count_digits(a, pass, 0, a.n, s);
-        const int32_t all = s.first[threadIdx.x];
+        rank_items(a, pass * a.bits, it, rank, s);
+        __syncthreads();
+        const int32_t all = static_cast<int>(threadIdx.x) < (1 << a.bits) ? scan_warps(s, 0) : 0;
         first_places(a, all, 0, a.passes == 1, s);
-        place_elements(a, pass, 0, a.n, it, nullptr, s);
+        write_items(a, pass, it, rank, nullptr, s, true);
+        __syncthreads();
     }
 }
 
@@ -442,12 +472,7 @@ SortPlan sort_plan(int64_t n, int64_t n_keys) {
     while (n_keys >> total) ++total;
     p.passes = (total + kDigitBits - 1) / kDigitBits;
     p.bits = (total + p.passes - 1) / p.passes;
-    if (n <= kSmall) {
-        p.ctas = 1;
-        p.chunk = kSmall;
-        return p;
-    }
-    const int64_t tiles = (n + kTile - 1) / kTile;
+    const int64_t tiles = n ? (n + kTile - 1) / kTile : 1;
     const int64_t per = (tiles + kMaxCtas - 1) / kMaxCtas;
     p.chunk = static_cast<int>(per * kTile);
     p.ctas = static_cast<int>((tiles + per - 1) / per);
