@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(kOffsetThreads)
 }
 
 // ---------------------------------------------------------------- rows
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;       // products and gradient (256: 332 us where 128 take 324, 16384 x 4 x 3584 fp16)
+constexpr int kDispatchThreads = 512;  // copies (256: 179 us, 512: 177 us, 16384 x 8 x 4096 bf16)
 constexpr int kBatch = 4;  // rows of a token in flight per thread
 
 struct RowArgs {
@@ -345,7 +346,7 @@ __device__ __forceinline__ void zero_tail(const RowArgs& a, T* out) {
 
 // One CTA per token: its row is read once and written at its k places.
 template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const RowArgs a) {
     using X = Vec<T, V>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -557,7 +558,7 @@ spmm_status launch_dispatch(const spmm_route_t* R, const void* x, int64_t ldx, v
     const int es = row_elem_bytes(dtype);
     const bool v = rows16(x, ldx, H, es) && rows16(xs, ldxs, H, es);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
+    const int threads = row_threads(H, v ? 16 / es : 1, kDispatchThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
     cudaError_t e;
     SPMM_ROWS_TYPED(e, dtype, v, dispatch_kernel, grid, threads, s, a);

@@ -57,6 +57,8 @@ template <typename T, int V>
 struct Vec {
     using Raw = uint4;
     static __device__ __forceinline__ Raw load(const T* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+    // data read once: leaves the caches first
+    static __device__ __forceinline__ Raw load_cs(const T* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
     static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
     static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { __stcs(reinterpret_cast<uint4*>(p), r); }
     static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
@@ -89,6 +91,7 @@ template <typename T>
 struct Vec<T, 1> {
     using Raw = T;
     static __device__ __forceinline__ Raw load(const T* p) { return __ldg(p); }
+    static __device__ __forceinline__ Raw load_cs(const T* p) { return __ldg(p); }
     static __device__ __forceinline__ void store(T* p, const Raw& r) { *p = r; }
     static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { *p = r; }
     static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
