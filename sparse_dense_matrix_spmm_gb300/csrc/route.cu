@@ -18,19 +18,23 @@ namespace {
 using namespace rows;
 
 // ---------------------------------------------------------------- sort
-// Least-significant-digit radix sort, up to 9 bits per pass.  The digits of
-// every CTA's stretch of the input are counted, then each CTA adds up the counts
-// before its own (smaller digits, then earlier CTAs) and writes its elements in
-// input order at their digits' places.  Placing an element counts its next digit
-// for the CTA that will read it there, so only the first pass has a counting
-// launch.  Inside a tile a warp owns consecutive elements and ranks them with
-// one ballot per digit bit, so the order is that of the input and nothing
-// depends on the order of atomics.  Up to one tile of elements runs in one CTA and
-// one launch (two tiles took it 10.0 us, two launches over two CTAs 7.4 us).
-// The kernels are bound by latency (launches and chains of dependent loads).
-// One cluster of 8 CTAs that ranked with match_any and counted in distributed
-// shared memory took one launch but 56 us for 131072 elements (its 8 SMs' issue
-// slots), and in one CTA 10.3 us for 2048 against 6.8 us here.
+// Least-significant-digit radix sort, up to 9 bits per pass, in tiles of 2048
+// elements.  Inside a tile a warp owns consecutive elements and ranks them with
+// one ballot per digit bit; a digit's place is the sum of the smaller digits, of
+// the earlier tiles' and of the earlier warps' counts.  So the order is that of
+// the input and nothing depends on the order of atomics.  By size:
+//   1 tile         one CTA, one launch
+//   2 .. 8 tiles   one cluster, one launch: the CTAs read each other's counts
+//                  through distributed shared memory
+//   more           one launch per pass over up to kMaxCtas CTAs, and one that
+//                  counts for the first pass; placing an element counts its next
+//                  digit for the CTA that will read it there
+// The kernels are bound by latency (launches, barriers, chains of dependent
+// loads); measured in a graph with 8 choices per token and 128 keys: 16 tokens
+// 3.5 us, 256 tokens 4.7 us, 1024 tokens 6.1 us (7.4 us as two launches), 16384
+// tokens 12.8 us; 32768 ids over 131072 keys (two passes and the offsets) 22 us.
+// One cluster over everything, with ranks from match_any, took 56 us for 16384
+// tokens (8 SMs' issue slots); 16 CTAs per cluster gained nothing over 8.
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kSortThreads = 512;  // one per bin
@@ -38,6 +42,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 4;          // per thread and tile
 constexpr int kTile = kSortThreads * kItems;
 
+constexpr int kMaxCluster = 8;  // the portable limit
 constexpr int kMaxCtas = 128;  // each reads every CTA's counts (256 CTAs for 524288 elements: 30 us in those reads)
 
 struct SortArgs {
@@ -232,6 +237,45 @@ __global__ void __launch_bounds__(kSortThreads) route_small_kernel(const SortArg
         first_places(a, all, 0, a.passes == 1, s);
         write_items(a, pass, it, rank, nullptr, s, true);
         __syncthreads();
+    }
+}
+
+__device__ __forceinline__ int32_t ld_cluster(const int32_t* p, uint32_t rank) {
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::map_shared(ptx::smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+// All passes over up to kMaxCluster tiles in one cluster, a tile per CTA: the
+// CTAs read each other's counts through distributed shared memory.
+__global__ void __launch_bounds__(kSortThreads) route_cluster_kernel(const SortArgs a) {
+    __shared__ SortShared s;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int cta = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
+    const int32_t i0 = cta * kTile, i1 = min(a.n, i0 + kTile);
+    for (int pass = 0; pass < a.passes; ++pass) {
+        Items it;
+        int32_t rank[kItems];
+        it.load(a, pass, i0, i1);
+        rank_items(a, pass * a.bits, it, rank, s);
+        __syncthreads();
+        const bool used = static_cast<int>(threadIdx.x) < (1 << a.bits);
+        s.first[threadIdx.x] = used ? scan_warps(s, 0) : 0;
+        ptx::cluster_sync_all();
+        int32_t all = 0, below = 0;
+        if (used) {
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {
+                const int32_t v = c < ctas ? ld_cluster(&s.first[threadIdx.x], c) : 0;
+                all += v;
+                if (c < cta) below += v;
+            }
+        }
+        ptx::cluster_sync_all();  // every CTA has read the counts
+        first_places(a, all, below, a.passes == 1 && cta == 0, s);
+        write_items(a, pass, it, rank, nullptr, s, true);
+        ptx::cluster_sync_all();  // this pass's results are written
     }
 }
 
@@ -485,7 +529,7 @@ size_t route_workspace_bytes(int64_t T, int32_t k, int64_t n_keys) {
     const int64_t n = T * k;
     const SortPlan p = sort_plan(n, n_keys);
     return (p.passes > 1 ? static_cast<size_t>(n) * 16 : 0) +
-           (p.ctas > 1 ? static_cast<size_t>(p.ctas) * sizeof(int32_t) * p.passes << p.bits : 0);
+           (p.ctas > kMaxCluster ? static_cast<size_t>(p.ctas) * sizeof(int32_t) * p.passes << p.bits : 0);
 }
 
 spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, const spmm_route_t* R, void* ws,
@@ -523,6 +567,8 @@ spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, c
     cudaError_t e = cudaSuccess;
     if (p.ctas == 1) {
         e = launch_chained(route_small_kernel, 1, kSortThreads, 0, 1, s, a);
+    } else if (p.ctas <= kMaxCluster) {
+        e = launch_chained(route_cluster_kernel, p.ctas, kSortThreads, 0, p.ctas, s, a);
     } else {
         e = launch_chained(route_count_kernel, p.ctas, kSortThreads, 0, 1, s, a);
         for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass)
