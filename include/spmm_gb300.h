@@ -544,7 +544,7 @@ SPMM_API spmm_status spmm_embed_grad(const spmm_route_t *R, const void *dy, int6
  * offsets[e] .. offsets[e + 1] - 1 belong to expert e).  W[e] is N x K, row pitch
  * ldw, expert pitch lde elements.  bf16 or fp16.  K, N and every pitch multiples
  * of 8 and every pointer 16-byte aligned (TMA), else SPMM_ERR_SHAPE; at most
- * 65535 experts.
+ * 65535 experts, N and K below 2^30, T k below 2^31 - 512.
  *   spmm_experts     ys[p]  = W[e] xs[p]            ys  T k x N, xs T k x K
  *   spmm_experts_dx  dxs[p] = W[e]^T dys[p]
  *   spmm_experts_dw  dW[e]  = sum_p dys[p] xs[p]^T  (zeros for an unused expert)

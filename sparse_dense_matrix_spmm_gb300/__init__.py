@@ -528,7 +528,7 @@ _ROW_DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.f
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class Route:
     """T x k ids sorted by value: order (flat indices, dropped ones last), pos
     (place of each flat index, -1 if dropped), offsets (first place per key) and,
@@ -609,8 +609,8 @@ def _weights(t: torch.Tensor, what: str, E: int, N: int, K: int, dtype, device):
 def _route_w(R: Route, w: torch.Tensor, device) -> int:
     if w.device != device or w.dtype is not torch.float32:
         raise TypeError(f"w must be float32 on {device}")
-    if w.numel() != R.n_rows or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous {R.T} x {R.k} tensor")
+    if w.shape != R.pos.shape or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous tensor of the ids' shape {tuple(R.pos.shape)}")
     return w.data_ptr()
 
 

@@ -632,7 +632,9 @@ spmm_status check_experts(const spmm_route_t* R, int64_t la, int64_t da, int64_t
     if (st != SPMM_OK) return st;
     if (dtype != SPMM_BF16 && dtype != SPMM_F16) return SPMM_ERR_DTYPE;
     if (N <= 0 || K <= 0 || N % 8 || K % 8) return SPMM_ERR_SHAPE;
-    if (N >= kDimLimit || K >= kDimLimit || R->n_keys > 65535) return SPMM_ERR_UNSUPPORTED;
+    // tile arithmetic is 32-bit: sizes stay a tile below 2^31
+    if (N >= kDimLimit / 2 || K >= kDimLimit / 2 || R->T * R->k >= kDimLimit - 512 || R->n_keys > 65535)
+        return SPMM_ERR_UNSUPPORTED;
     if (bad_pitch(la, da) || bad_pitch(lb, db) || bad_pitch(ldw, K)) return SPMM_ERR_SHAPE;
     if (la % 8 || lb % 8 || ldw % 8 || lde % 8) return SPMM_ERR_SHAPE;
     // experts must not overlap: lde >= (N - 1) ldw + K, without forming the product

@@ -14,6 +14,7 @@ CASES = [
     ([15, 16, 17, 0, 31, 33], 3, 128, 64), ([63, 64, 65, 1], 0, 72, 200), ([127, 128, 129], 2, 256, 128),
     ([255, 3, 257, 300], 1, 264, 328), ([600, 0, 0, 37], 0, 520, 1000), ([5, 2, 0, 7, 1, 3, 6, 4] * 4, 9, 384, 512),
     ([1030], 0, 1536, 520), ([5, 2, 0, 7], 2, 200, 584), ([0, 16], 0, 40, 2056), ([0] * 40 + [1, 3], 0, 24, 64),
+    ([300] + [0] * 30 + [2] * 9, 1, 264, 200),
 ]
 
 

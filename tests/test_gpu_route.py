@@ -73,6 +73,7 @@ def test_route_extremes(n_keys):
     assert spmm.last_device_error() == spmm._lib.DEVERR_INDEX
     wide = torch.from_numpy(_ids(321, 7, n_keys, 2, 0.1)).cuda()
     _same_route(spmm.spmm_build_route(wide[:, 2:5], n_keys), wide[:, 2:5].cpu().numpy(), n_keys)
+    _same_route(spmm.spmm_build_route(wide[:, 3], n_keys), wide[:, 3].cpu().numpy(), n_keys)
     flat = wide[:, 0].contiguous()
     _same_route(spmm.spmm_build_route(flat, n_keys), flat.cpu().numpy(), n_keys)
 
@@ -232,6 +233,8 @@ def test_refusals():
         spmm.spmm_combine(R, ys, w.to(torch.bfloat16))
     with pytest.raises(ValueError):
         spmm.spmm_combine(R, ys, w[:, :1])
+    with pytest.raises(ValueError):
+        spmm.spmm_combine(R, ys, w.t().contiguous())                   # k x T
     with pytest.raises(ValueError):
         spmm.spmm_combine(R, ys, out=x[:9])
     with pytest.raises(TypeError):

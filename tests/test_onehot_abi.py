@@ -95,6 +95,8 @@ def test_experts(L):
         assert call(_route(), 24, 64, 16, 64, lde, 32, 64, 0, 16, 64, None) == SHAPE       # alignment
         assert call(_route(), 16, 64, None, 64, lde, 32, 64, 0, 16, 64, None) == NULL
         assert call(_route(E=70000), 16, 64, 16, 64, lde, 32, 64, 0, 16, 64, None) == UNSUPPORTED
+        assert call(_route(T=(1 << 31) - 100, k=1), 16, 64, 16, 64, lde, 32, 64, 0, 16, 64, None) == UNSUPPORTED
+        assert call(_route(), 16, 1 << 30, 16, 1 << 30, 1 << 36, 32, 1 << 30, 0, 16, 1 << 30, None) == UNSUPPORTED
         assert call(_route(T=0), None, 64, None, 64, lde, 32, 64, 0, None, 64, None) == 0
     assert w(_route(), 16, 32, 16, 64, 32, 64, 0, 16, 60, lde, None) == SHAPE
     assert w(_route(), 16, 32, 16, 64, 32, 64, 0, None, 64, lde, None) == NULL
