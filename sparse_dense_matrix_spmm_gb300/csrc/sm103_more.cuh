@@ -16,6 +16,19 @@ namespace ptx {
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Two fp32 products and sums in one instruction, each rounded as fmaf rounds.
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_f32(float x, float y) {
+    return static_cast<uint64_t>(__float_as_uint(x)) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
+}
+__device__ __forceinline__ float2 unpair_f32(uint64_t v) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
 // 16 TMEM lanes x 32 32-bit columns as four 16 x 8 blocks: in block b a thread
 // holds row lane / 4, columns 2 (lane % 4) and the next (r[4b], r[4b + 1]) and
 // the same of row lane / 4 + 8 (r[4b + 2], r[4b + 3]).
