@@ -27,7 +27,6 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass, field
-from functools import cached_property
 from typing import Optional
 
 import torch
@@ -528,32 +527,22 @@ _ROW_DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.f
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-@dataclass(frozen=True, eq=False)
 class Route:
     """T x k ids sorted by value: order (flat indices, dropped ones last), pos
     (place of each flat index, -1 if dropped), offsets (first place per key) and,
     for k = 1, keys (the sorted ids, n_keys if dropped).  All int32 on the device;
-    pos has the ids' shape."""
-    T: int
-    k: int
-    n_keys: int
-    order: torch.Tensor
-    pos: torch.Tensor
-    offsets: torch.Tensor
-    keys: Optional[torch.Tensor] = None
+    pos has the ids' shape.  A route does not change after it is built."""
 
-    @property
-    def n_rows(self) -> int:
-        return self.T * self.k
+    def __init__(self, T: int, k: int, n_keys: int, order: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor,
+                 keys: Optional[torch.Tensor] = None):
+        self.T, self.k, self.n_keys, self.n_rows = T, k, n_keys, T * k
+        self.order, self.pos, self.offsets, self.keys = order, pos, offsets, keys
+        self.device, self.shape = order.device, pos.shape
+        self._ref = C.byref(_lib.RouteT(T, k, n_keys, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
+                                        None if keys is None else keys.data_ptr()))
 
     def c(self) -> _lib.RouteT:
-        return _lib.RouteT(self.T, self.k, self.n_keys, _ptr(self.order), _ptr(self.pos), _ptr(self.offsets),
-                           _ptr(self.keys))
-
-    @cached_property
-    def _ref(self):
-        """The C struct, marshalled once: a route does not change after it is built."""
-        return C.byref(self.c())
+        return self._ref._obj
 
 
 # At decoding sizes the kernels take 2-4 us, so the wrappers below spend as little
@@ -609,8 +598,8 @@ def _weights(t: torch.Tensor, what: str, E: int, N: int, K: int, dtype, device):
 def _route_w(R: Route, w: torch.Tensor, device) -> int:
     if w.device != device or w.dtype is not torch.float32:
         raise TypeError(f"w must be float32 on {device}")
-    if w.shape != R.pos.shape or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous tensor of the ids' shape {tuple(R.pos.shape)}")
+    if w.shape != R.shape or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous tensor of the ids' shape {tuple(R.shape)}")
     return w.data_ptr()
 
 
@@ -656,7 +645,7 @@ def spmm_build_route(ids: torch.Tensor, n_keys: int, workspace: Optional[torch.T
 
 def spmm_dispatch(R: Route, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """xs[p] = x[order[p] // k] for the kept places, zero rows after them."""
-    H, dev, dt, rows = x.shape[-1], R.order.device, x.dtype, R.n_rows
+    H, dev, dt, rows = x.shape[-1], R.device, x.dtype, R.n_rows
     code, ldx = _row_code(dt), _rows(x, "x", R.T, H, dt, dev)
     if out is None:
         out, ldo = _empty(x, (rows, H), dt, stream), H
@@ -669,7 +658,7 @@ def spmm_dispatch(R: Route, x: torch.Tensor, out: Optional[torch.Tensor] = None,
 def spmm_combine(R: Route, ys: torch.Tensor, w: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     """y[t] = sum_j w[t, j] ys[pos[t, j]] over the kept choices (w fp32; None: weights of 1)."""
-    H, dev, dt = ys.shape[-1], R.order.device, ys.dtype
+    H, dev, dt = ys.shape[-1], R.device, ys.dtype
     code, ldys = _row_code(dt), _rows(ys, "ys", R.n_rows, H, dt, dev)
     w_ptr = None if w is None else _route_w(R, w, dev)
     if out is None:
@@ -689,7 +678,7 @@ def spmm_combine_grad(R: Route, dy: torch.Tensor, ys: torch.Tensor, w: torch.Ten
                       out: Optional[torch.Tensor] = None, stream=None):
     """Gradients of spmm_combine: (dys, dw) with dys[pos[t, j]] = w[t, j] dy[t] (zero
     rows past the kept places) and dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32, of w's shape."""
-    H, dev, dt, rows = dy.shape[-1], R.order.device, dy.dtype, R.n_rows
+    H, dev, dt, rows = dy.shape[-1], R.device, dy.dtype, R.n_rows
     code, lddy, ldys = _row_code(dt), _rows(dy, "dy", R.T, H, dt, dev), _rows(ys, "ys", rows, H, dt, dev)
     w_ptr = _route_w(R, w, dev)
     if out is None:
@@ -734,7 +723,7 @@ def spmm_embed_grad(R: Route, dy: torch.Tensor, scale: float = 1.0, out: Optiona
     """Gradient of spmm_embed for the table, from the route of the ids (k = 1, n_keys
     = V): scale * the sum of dy over each row's tokens.  Every row is written, or
     with accumulate the sums are added to out.  out is dy's type (default) or fp32."""
-    H, dev, dt = dy.shape[-1], R.order.device, dy.dtype
+    H, dev, dt = dy.shape[-1], R.device, dy.dtype
     code, lddy = _row_code(dt), _rows(dy, "dy", R.T, H, dt, dev)
     if out is None:
         if accumulate:
@@ -752,7 +741,7 @@ def spmm_experts(R: Route, xs: torch.Tensor, W: torch.Tensor, out: Optional[torc
                  stream=None) -> torch.Tensor:
     """ys[p] = W[e] xs[p] for the rows p of expert e (W is E x N x K, R.n_keys = E);
     zero rows past the kept places.  bf16 or fp16."""
-    dev, dt, rows = R.order.device, xs.dtype, R.n_rows
+    dev, dt, rows = R.device, xs.dtype, R.n_rows
     N, K = W.shape[-2], W.shape[-1]
     code, ldx = _row_code(dt), _rows(xs, "xs", rows, K, dt, dev)
     ldw, lde = _weights(W, "W", R.n_keys, N, K, dt, dev)
@@ -768,7 +757,7 @@ def spmm_experts(R: Route, xs: torch.Tensor, W: torch.Tensor, out: Optional[torc
 def spmm_experts_dx(R: Route, dys: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """dxs[p] = W[e]^T dys[p] for the rows p of expert e; zero rows past the kept places."""
-    dev, dt, rows = R.order.device, dys.dtype, R.n_rows
+    dev, dt, rows = R.device, dys.dtype, R.n_rows
     N, K = W.shape[-2], W.shape[-1]
     code, ldy = _row_code(dt), _rows(dys, "dys", rows, N, dt, dev)
     ldw, lde = _weights(W, "W", R.n_keys, N, K, dt, dev)
@@ -784,7 +773,7 @@ def spmm_experts_dx(R: Route, dys: torch.Tensor, W: torch.Tensor, out: Optional[
 def spmm_experts_dw(R: Route, dys: torch.Tensor, xs: torch.Tensor, out: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """dW[e] = sum of dys[p] xs[p]^T over the rows p of expert e (E x N x K; zeros for an unused expert)."""
-    dev, dt, rows, E = R.order.device, dys.dtype, R.n_rows, R.n_keys
+    dev, dt, rows, E = R.device, dys.dtype, R.n_rows, R.n_keys
     N, K = dys.shape[-1], xs.shape[-1]
     code, ldy, ldx = _row_code(dt), _rows(dys, "dys", rows, N, dt, dev), _rows(xs, "xs", rows, K, dt, dev)
     if out is None:
