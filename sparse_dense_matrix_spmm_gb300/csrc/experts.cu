@@ -4,15 +4,23 @@
 //   forward   ys[p]  = W[e] xs[p]                 D = W   . xs^T   (N x rows)
 //   dx        dxs[p] = W[e]^T dys[p]              D = W^T . dys^T  (K x rows)
 //   dw        dW[e]  = sum_p dys[p] xs[p]^T       D = dys^T . xs   (N x K)
-// One persistent warp-specialised tcgen05 kernel runs all three.  For the row
-// products the weights are the MMA's M operand (128 features) and an expert's
-// rows its N operand, because N may be any multiple of 16: an expert with one
-// row costs one MMA of N = 16 and one with 1000 rows four of N = 256, and no
-// tile of rows is padded to 128.  Rows past the expert's last one fall into
-// columns of D that are not stored.  For dw the rows are the depth: the tail of
-// the last 64-row block belongs to other experts and is overwritten with zeros
-// in shared memory before the MMA reads it (their values may be infinite, so
-// multiplying by zero would not do).
+// One persistent warp-specialised tcgen05 kernel runs all three, on CTA pairs
+// (M = 256) where D has more than 128 rows.  For the row products the weights are
+// the MMA's M operand and an expert's rows its N operand, because N may be any
+// multiple of 16 (32 for a pair): an expert with one row costs an MMA of N = 32
+// per 256 features and one with 1000 rows four of N = 256, and no tile of rows is
+// padded to 128.  Rows past the expert's last one fall into columns of D that are
+// not stored.  For dw the rows are the depth: the tail of the last 64-row block
+// belongs to other experts and is overwritten with zeros in shared memory before
+// the MMA reads it (their values may be infinite, so multiplying by zero would
+// not do).
+// Why pairs: a 128 x 256 tile of one CTA loads 48 KB per 64 of depth (520 clk of
+// MMA), 92 B/clk, and L2 gives an SM about 70; a pair's CTA loads 32 KB.  One
+// CTA 1160 TFLOP/s, a pair 1320 on a ragged prompt batch (32768 rows, 2048 x
+// 4096), 1450 with the steps below.  What bounds it now: with 1024 rows per
+// expert the power limit (352 us sustained where cuBLAS's batched product takes
+// 341 us), with few rows reading the weights from HBM (6.8-7.6 TB/s), between
+// them the producers' and the issuing thread's instructions per step.
 // The sums are fp32 in TMEM, rounded once to the operands' type.
 //
 // Roles per CTA: warps 0, 1, 12 and 13 load A and B (TMA, 128-byte swizzle, one
@@ -31,16 +39,19 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, 128 columns each
+constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half of the columns each
 constexpr int kMoreProducers = 4 + kEpiWarps;  // first warp of the second pair of producers
 constexpr int kThreads = 32 * (kMoreProducers + 2);
-constexpr int kDepth = 64;       // contraction per stage: 128 bytes, one swizzle row
+constexpr int kDepth = 64;  // contraction per stage: 128 bytes, one swizzle row
 constexpr int kABytes = 128 * 128;
 constexpr int kSmemMax = 232448;  // 227 KB, the most a CTA can have
-constexpr int kFewRows = 16;     // rows per expert up to which row tiles are 64 instead of 256
-constexpr int kDwFewRows = 4;    // rows per expert up to which dw runs on CUDA cores
-constexpr int kVecMost = 16;     // rows in all up to which the forward product runs on CUDA cores
-constexpr int kUnits = 4;        // work units announced ahead
+constexpr int kUnits = 4;         // work units announced ahead
+// Variants by size, all on averages that the host knows.
+// Row tiles of 64 instead of 256 up to this many rows per expert: nine stages fit
+// instead of six (64 tokens x 8 of 128 experts, 1536 x 4096: 226 us against 240).
+constexpr int kFewRows = 16;
+constexpr int kVecMost = 16;   // rows in all up to which the forward product runs on CUDA cores
+constexpr int kDwFewRows = 4;  // rows per expert up to which dw runs on CUDA cores
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -56,13 +67,13 @@ struct ExpertArgs {
 };
 
 // Tensor maps of B.  Row products load an expert's rows in boxes of 128, 64, 32
-// and 16 rows (box_rows); dw uses the first map for its 64 x 64 boxes.
+// and 16 rows (box_of); dw uses the first map for its 64 x 64 boxes.
 struct BMaps {
     CUtensorMap m[4];
 };
 // The next box for `rest` rows (a multiple of 16): at most two boxes and 16
 // unused rows per 128.  Boxes of exactly the rows needed (64 and 16) took 207 us
-// where this takes 188 us (448 rows per expert): every box costs about as
+// where this takes 171 us (448 rows per expert): every box costs about as
 // much as 32 rows.
 __host__ __device__ constexpr int box_of(int rest) { return rest > 96 ? 0 : rest > 48 ? 1 : rest > 16 ? 2 : 3; }
 __host__ __device__ constexpr int boxed_rows(int nb) {
@@ -186,8 +197,7 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
 // expert, in 16-byte pieces.
 template <typename T>
 __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMap* tmOut, const Unit& w, uint32_t t,
-                                           int c0, int c1, int row0, int lane, uint32_t buffers,
-                                           int& odd) {
+                                           int c0, int c1, int row0, int lane, uint32_t buffers, int& odd) {
     T* out = static_cast<T*>(a.out) + static_cast<int64_t>(w.p0 + w.n0) * a.ldo;
     const int unit = lane & 3, feature = row0 + 8 * unit;
     for (int c = c0; c < c1; c += 32, odd ^= 1) {
