@@ -391,21 +391,19 @@ __device__ __forceinline__ void zero_tail(const RowArgs& a, T* out) {
 // One CTA per token: its row is read once and written at its k places.
 template <typename T, int V>
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const RowArgs a) {
-    using X = Vec<T, V>;
+    using X = Cols<T, V, 2>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const T* x = static_cast<const T*>(a.a) + blockIdx.x * a.lda;
     T* out = static_cast<T*>(a.out);
     const int32_t* pos = a.pos + static_cast<int64_t>(blockIdx.x) * a.k;
-    for (int64_t c = threadIdx.x * V; c < a.H; c += 2 * blockDim.x * V) {
-        const int64_t c1 = c + blockDim.x * V;
-        const bool two = c1 < a.H;
-        const typename X::Raw v0 = X::load(x + c), v1 = two ? X::load(x + c1) : X::zero();
+    const int step = blockDim.x * V;
+    for (int64_t c = threadIdx.x * V; c < a.H; c += X::U * step) {
+        typename X::Raw r[X::U];
+        X::load(r, x, c, a.H, step);
         for (int j = 0; j < a.k; ++j) {
             const int64_t p = __ldg(pos + j);
-            if (p < 0) continue;
-            X::store_cs(out + p * a.ldo + c, v0);
-            if (two) X::store_cs(out + p * a.ldo + c1, v1);
+            if (p >= 0) X::store_cs(out + p * a.ldo, r, c, a.H, step);
         }
     }
     zero_tail<T, V>(a, out);
@@ -415,35 +413,41 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const RowArg
 // and rounded once.  Four rows are in flight per thread.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
-    using X = Vec<T, V>;
+    using X = Cols<T, V>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const T* ys = static_cast<const T*>(a.a);
     T* y = static_cast<T*>(a.out) + blockIdx.x * a.ldo;
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.k;
-    for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-        float acc[V] = {};
+    const int step = blockDim.x * V;
+    for (int64_t c = threadIdx.x * V; c < a.H; c += X::U * step) {
+        float acc[X::N] = {};
         for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-            typename X::Raw r[kBatch];
+            typename X::Raw r[kBatch][X::U];
             float w[kBatch];
             bool live[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const int64_t p = j0 + j < a.k ? __ldg(a.pos + f0 + j0 + j) : -1;
                 live[j] = p >= 0;
-                r[j] = live[j] ? X::load(ys + p * a.lda + c) : X::zero();
+                if (live[j])
+                    X::load(r[j], ys + p * a.lda, c, a.H, step);
+                else
+                    X::clear(r[j]);
                 w[j] = a.w && live[j] ? __ldg(a.w + f0 + j0 + j) : 1.f;
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (!live[j]) continue;  // not 0 * w: a weight may be infinite
-                float v[V];
+                float v[X::N];
                 X::unpack(r[j], v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[i], acc[i]);
+                for (int i = 0; i < X::N; ++i) acc[i] = fmaf(w[j], v[i], acc[i]);
             }
         }
-        X::store(y + c, X::pack(acc));
+        typename X::Raw o[X::U];
+        X::pack(o, acc);
+        X::store(y, o, c, a.H, step);
     }
 }
 
@@ -451,7 +455,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
 // with ys, each summed in fp32 per thread, then over the CTA in a fixed order.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs a) {
-    using X = Vec<T, V>;
+    // single 16-bit values one per row: four hold 91 registers, 166 us against 148
+    // at H = 4095 below
+    using X = Cols<T, V, 1, V * sizeof(T) == 2 ? 1 : 4>;
     __shared__ float part[kBatch][kRowThreads / 32];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -460,6 +466,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs
     T* dys = static_cast<T*>(a.out);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.k;
+    const int step = blockDim.x * V;
     for (int j0 = 0; j0 < a.k; j0 += kBatch) {
         int64_t p[kBatch];
         float w[kBatch], dot[kBatch];
@@ -469,23 +476,31 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs
             w[j] = p[j] >= 0 ? __ldg(a.w + f0 + j0 + j) : 0.f;
             dot[j] = 0.f;
         }
-        for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-            typename X::Raw r[kBatch];
+        for (int64_t c = threadIdx.x * V; c < a.H; c += X::U * step) {
+            typename X::Raw r[kBatch][X::U], q[X::U];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) r[j] = p[j] >= 0 ? X::load(ys + p[j] * a.ldb + c) : X::zero();
-            float d[V];
-            X::unpack(X::load(dy + c), d);
+            for (int j = 0; j < kBatch; ++j) {
+                if (p[j] >= 0)
+                    X::load(r[j], ys + p[j] * a.ldb, c, a.H, step);
+                else
+                    X::clear(r[j]);
+            }
+            X::load(q, dy, c, a.H, step);
+            float d[X::N];
+            X::unpack(q, d);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (p[j] < 0) continue;
-                float v[V];
+                float v[X::N];
                 X::unpack(r[j], v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+                for (int i = 0; i < X::N; ++i) {
                     dot[j] = fmaf(d[i], v[i], dot[j]);
                     v[i] = w[j] * d[i];
                 }
-                X::store_cs(dys + p[j] * a.ldo + c, X::pack(v));
+                typename X::Raw o[X::U];
+                X::pack(o, v);
+                X::store_cs(dys + p[j] * a.ldo, o, c, a.H, step);
             }
         }
 #pragma unroll
@@ -602,9 +617,10 @@ spmm_status launch_dispatch(const spmm_route_t* R, const void* x, int64_t ldx, v
     a.out = xs;
     a.ldo = ldxs;
     const int es = row_elem_bytes(dtype);
-    const bool v = rows16(x, ldx, H, es) && rows16(xs, ldxs, H, es);
+    const Operand o[] = {{x, ldx, es}, {xs, ldxs, es}};
+    const int v = row_width(o, H);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1, kDispatchThreads);
+    const int threads = row_threads(H, 16 / es, kDispatchThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
     cudaError_t e;
     SPMM_ROWS_TYPED(e, dtype, v, dispatch_kernel, grid, threads, s, a);
@@ -621,9 +637,10 @@ spmm_status launch_combine(const spmm_route_t* R, const void* ys, int64_t ldys, 
     a.out = y;
     a.ldo = ldy;
     const int es = row_elem_bytes(dtype);
-    const bool v = rows16(ys, ldys, H, es) && rows16(y, ldy, H, es);
+    const Operand o[] = {{ys, ldys, es}, {y, ldy, es}};
+    const int v = row_width(o, H);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
+    const int threads = row_threads(H, 16 / es, kRowThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
     cudaError_t e;
     SPMM_ROWS_TYPED(e, dtype, v, combine_kernel, grid, threads, s, a);
@@ -644,9 +661,10 @@ spmm_status launch_combine_grad(const spmm_route_t* R, const void* dy, int64_t l
     a.ldo = lddys;
     a.dw = dw;
     const int es = row_elem_bytes(dtype);
-    const bool v = rows16(dy, lddy, H, es) && rows16(ys, ldys, H, es) && rows16(dys, lddys, H, es);
+    const Operand o[] = {{dy, lddy, es}, {ys, ldys, es}, {dys, lddys, es}};
+    const int v = row_width(o, H);
     const unsigned grid = static_cast<unsigned>(R->T);
-    const int threads = row_threads(H, v ? 16 / es : 1, kRowThreads);
+    const int threads = row_threads(H, 16 / es, kRowThreads);
     trace_begin(SPMM_KERNEL_ROWS, s);
     cudaError_t e;
     SPMM_ROWS_TYPED(e, dtype, v, combine_grad_kernel, grid, threads, s, a);

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 
 namespace spmm {
 namespace rows {
@@ -51,24 +53,83 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// V consecutive elements of type T: V = 16 / sizeof(T) moves 16 bytes at once
-// (the address must be 16-byte aligned), V = 1 one element.
+// Words that move at once.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<2> {
+    using type = uint16_t;
+};
+template <>
+struct Word<4> {
+    using type = uint32_t;
+};
+template <>
+struct Word<8> {
+    using type = uint2;
+};
+template <>
+struct Word<16> {
+    using type = uint4;
+};
+
+// V consecutive elements of type T, V sizeof(T) = 2, 4, 8 or 16 bytes moved at
+// once (32 bytes, eight fp32 next to eight 16-bit values, in two halves).  The
+// address must be a multiple of those bytes (of 16 for 32).
 template <typename T, int V>
 struct Vec {
-    using Raw = uint4;
-    static __device__ __forceinline__ Raw load(const T* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-    // data read once: leaves the caches first
-    static __device__ __forceinline__ Raw load_cs(const T* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
-    static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
-    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { __stcs(reinterpret_cast<uint4*>(p), r); }
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[V]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    static constexpr int kBytes = V * static_cast<int>(sizeof(T)), kWords = (kBytes + 15) / 16;
+    using W = typename Word<(kBytes < 16 ? kBytes : 16)>::type;
+    struct Two {
+        W w[2];
+    };
+    using Raw = std::conditional_t<kWords == 1, W, Two>;
+    static __device__ __forceinline__ W* words(Raw& r) { return reinterpret_cast<W*>(&r); }
+    static __device__ __forceinline__ const W* words(const Raw& r) { return reinterpret_cast<const W*>(&r); }
+    static __device__ __forceinline__ Raw load(const T* p) {
+        Raw r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                f[i] = __uint_as_float(w[i]);
-            } else {
+        for (int i = 0; i < kWords; ++i) words(r)[i] = __ldg(reinterpret_cast<const W*>(p) + i);
+        return r;
+    }
+    // data read once: leaves the caches first
+    static __device__ __forceinline__ Raw load_cs(const T* p) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) words(r)[i] = __ldcs(reinterpret_cast<const W*>(p) + i);
+        return r;
+    }
+    static __device__ __forceinline__ Raw load_plain(const T* p) {  // data this kernel also writes
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) words(r)[i] = reinterpret_cast<const W*>(p)[i];
+        return r;
+    }
+    static __device__ __forceinline__ void store(T* p, const Raw& r) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) reinterpret_cast<W*>(p)[i] = words(r)[i];
+    }
+    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<W*>(p) + i, words(r)[i]);
+    }
+    static __device__ __forceinline__ Raw zero() {
+        Raw r;
+        memset(&r, 0, sizeof(r));
+        return r;
+    }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[V]) {
+        if constexpr (sizeof(T) == 4) {
+            memcpy(f, &r, sizeof(f));
+        } else if constexpr (V == 1) {
+            T v;
+            memcpy(&v, &r, sizeof(v));
+            f[0] = to_f32<T>(v);
+        } else {
+            uint32_t w[V / 2];
+            memcpy(w, &r, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
                 const float2 p = Pair<T>::unpack(w[i]);
                 f[2 * i] = p.x;
                 f[2 * i + 1] = p.y;
@@ -76,105 +137,130 @@ struct Vec {
         }
     }
     static __device__ __forceinline__ Raw pack(const float (&f)[V]) {
-        uint32_t w[4];
+        Raw r;
+        if constexpr (sizeof(T) == 4) {
+            memcpy(&r, f, sizeof(f));
+        } else if constexpr (V == 1) {
+            const T v = from_f32<T>(f[0]);
+            memcpy(&r, &v, sizeof(v));
+        } else {
+            uint32_t w[V / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4)
-                w[i] = __float_as_uint(f[i]);
-            else
-                w[i] = Pair<T>::pack(f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < V / 2; ++i) w[i] = Pair<T>::pack(f[2 * i], f[2 * i + 1]);
+            memcpy(&r, w, sizeof(w));
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return r;
     }
-};
-template <typename T>
-struct Vec<T, 1> {
-    using Raw = T;
-    static __device__ __forceinline__ Raw load(const T* p) { return __ldg(p); }
-    static __device__ __forceinline__ Raw load_cs(const T* p) { return __ldg(p); }
-    static __device__ __forceinline__ void store(T* p, const Raw& r) { *p = r; }
-    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { *p = r; }
-    static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_f32<T>(r); }
-    static __device__ __forceinline__ Raw pack(const float (&f)[1]) { return from_f32<T>(f[0]); }
 };
 
-// Four 16-bit values next to four fp32 ones: 8 bytes at once.
-template <typename T>
-struct Vec4x16 {
-    using Raw = uint2;
-    static __device__ __forceinline__ void store_cs(T* p, const Raw& r) { __stcs(reinterpret_cast<uint2*>(p), r); }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[4]) {
-        const float2 a = Pair<T>::unpack(r.x), b = Pair<T>::unpack(r.y);
-        f[0] = a.x;
-        f[1] = a.y;
-        f[2] = b.x;
-        f[3] = b.y;
-    }
-    static __device__ __forceinline__ Raw pack(const float (&f)[4]) {
-        return make_uint2(Pair<T>::pack(f[0], f[1]), Pair<T>::pack(f[2], f[3]));
-    }
-};
-template <>
-struct Vec<__half, 4> : Vec4x16<__half> {};
-template <>
-struct Vec<__nv_bfloat16, 4> : Vec4x16<__nv_bfloat16> {};
-
-// Eight fp32 values next to eight 16-bit ones: 32 bytes as two 16-byte moves.
-template <>
-struct Vec<float, 8> {
-    struct Raw {
-        uint4 lo, hi;
-    };
-    static __device__ __forceinline__ Raw load(const float* p) {
-        return {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1)};
-    }
-    static __device__ __forceinline__ void store(float* p, const Raw& r) {
-        reinterpret_cast<uint4*>(p)[0] = r.lo;
-        reinterpret_cast<uint4*>(p)[1] = r.hi;
-    }
-    static __device__ __forceinline__ void store_cs(float* p, const Raw& r) {
-        __stcs(reinterpret_cast<uint4*>(p), r.lo);
-        __stcs(reinterpret_cast<uint4*>(p) + 1, r.hi);
-    }
-    static __device__ __forceinline__ Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
-        const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+// A thread's columns of a row: U vectors of V elements, `step` columns apart: at
+// full width WIDE, in narrower moves up to NARROW of them, so that they too have
+// many bytes in flight (8192 x 4 x 4095 bf16: dispatch 107 us with one at a time,
+// 83 us with four, 92 us with eight).  Column c + u step of vector u counts if
+// it lies below H.
+template <typename T, int V, int WIDE = 1, int NARROW = 4>
+struct Cols {
+    static constexpr int kVecs = 16 / (V * static_cast<int>(sizeof(T)));
+    static constexpr int U = kVecs == 1 ? WIDE : kVecs < NARROW ? kVecs : NARROW, N = U * V;
+    using X = Vec<T, V>;
+    using Raw = typename X::Raw;
+    static __device__ __forceinline__ void load(Raw (&r)[U], const T* row, int64_t c, int64_t H, int step) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+        for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load(row + c + u * step) : X::zero();
     }
-    static __device__ __forceinline__ Raw pack(const float (&f)[8]) {
-        uint32_t w[8];
+    static __device__ __forceinline__ void load_cs(Raw (&r)[U], const T* row, int64_t c, int64_t H, int step) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
-        return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+        for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load_cs(row + c + u * step) : X::zero();
+    }
+    static __device__ __forceinline__ void clear(Raw (&r)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = X::zero();
+    }
+    static __device__ __forceinline__ void store(T* row, const Raw (&r)[U], int64_t c, int64_t H, int step) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * step < H) X::store(row + c + u * step, r[u]);
+    }
+    static __device__ __forceinline__ void store_cs(T* row, const Raw (&r)[U], int64_t c, int64_t H, int step) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * step < H) X::store_cs(row + c + u * step, r[u]);
+    }
+    static __device__ __forceinline__ void unpack(const Raw (&r)[U], float (&f)[N]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[V];
+            X::unpack(r[u], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[u * V + i] = v[i];
+        }
+    }
+    static __device__ __forceinline__ void pack(Raw (&r)[U], const float (&f)[N]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = f[u * V + i];
+            r[u] = X::pack(v);
+        }
     }
 };
 
 }  // namespace rows
 
-// Rows move in 16-byte pieces when the base, the pitch and the row length are
-// all multiples of 16 bytes, else one element at a time.
-inline bool rows16(const void* p, int64_t ld, int64_t H, int es) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es) % 16 == 0 && (H * es) % 16 == 0;
+// Whether rows of H elements of `es` bytes move V elements at a time.
+inline bool rows_move(const void* p, int64_t ld, int64_t H, int es, int V) {
+    const int bytes = V * es < 16 ? V * es : 16;
+    return reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(bytes) == 0 && (ld * es) % bytes == 0 && H % V == 0;
+}
+
+// Elements per move that the base, pitch and row length of every operand allow,
+// 16 bytes at most.  What a width costs, 8192 tokens x 4 in bf16, microseconds:
+//   row length      4096 (16 B)  4100 (8 B)  4098 (4 B)  4095 (2 B)
+//   dispatch          52           54          64          83
+//   combine           51           55          64         117
+//   its gradient      92           97         109         148
+//   embed, 16384      41           44          49          63
+// Moving the three odd lengths element by element took 79, 152, 152 and 85.
+struct Operand {
+    const void* p;
+    int64_t ld;
+    int es;
+};
+template <int N>
+int row_width(const Operand (&o)[N], int64_t H) {
+    for (int v = 16 / o[0].es; v > 1; v /= 2) {
+        bool ok = true;
+        for (const Operand& x : o) ok = ok && rows_move(x.p, x.ld, H, x.es, v);
+        if (ok) return v;
+    }
+    return 1;
+}
+
+// Threads of a CTA that moves rows of H elements, `per` of them each.
+inline int row_threads(int64_t H, int per, int most) {
+    const int64_t n = ((H + per - 1) / per + 31) / 32 * 32;
+    return static_cast<int>(n < most ? n : most);
 }
 
 }  // namespace spmm
 
-// Threads of a CTA that moves rows of H elements, V at a time.
-inline int row_threads(int64_t H, int V, int most) {
-    const int64_t n = ((H + V - 1) / V + 31) / 32 * 32;
-    return static_cast<int>(n < most ? n : most);
-}
-
-// Launch KERNEL<T, V> for a row type and vector width chosen at run time.
-#define SPMM_ROWS_TYPED(status, dtype, vec, KERNEL, grid, threads, s, args)                                      \
-    do {                                                                                                         \
-        if ((dtype) == SPMM_F32)                                                                                 \
-            status = launch_chained(vec ? KERNEL<float, 4> : KERNEL<float, 1>, grid, threads, 0, 1, s, args);    \
-        else if ((dtype) == SPMM_F16)                                                                            \
-            status = launch_chained(vec ? KERNEL<__half, 8> : KERNEL<__half, 1>, grid, threads, 0, 1, s, args);  \
-        else                                                                                                     \
-            status = launch_chained(vec ? KERNEL<__nv_bfloat16, 8> : KERNEL<__nv_bfloat16, 1>, grid, threads, 0, \
-                                    1, s, args);                                                                 \
+// Launch KERNEL<T, V> for a row type and vector width (elements) chosen at run time.
+#define SPMM_ROWS_TYPED(status, dtype, v, KERNEL, grid, threads, s, args)                                          \
+    do {                                                                                                           \
+        if ((dtype) == SPMM_F32)                                                                                   \
+            status = launch_chained((v) == 4 ? KERNEL<float, 4> : (v) == 2 ? KERNEL<float, 2> : KERNEL<float, 1>,  \
+                                    grid, threads, 0, 1, s, args);                                                 \
+        else if ((dtype) == SPMM_F16)                                                                              \
+            status = launch_chained((v) == 8   ? KERNEL<__half, 8>                                                 \
+                                    : (v) == 4 ? KERNEL<__half, 4>                                                 \
+                                    : (v) == 2 ? KERNEL<__half, 2>                                                 \
+                                               : KERNEL<__half, 1>,                                                \
+                                    grid, threads, 0, 1, s, args);                                                 \
+        else                                                                                                       \
+            status = launch_chained((v) == 8   ? KERNEL<__nv_bfloat16, 8>                                          \
+                                    : (v) == 4 ? KERNEL<__nv_bfloat16, 4>                                          \
+                                    : (v) == 2 ? KERNEL<__nv_bfloat16, 2>                                          \
+                                               : KERNEL<__nv_bfloat16, 1>,                                         \
+                                    grid, threads, 0, 1, s, args);                                                 \
     } while (0)
