@@ -25,14 +25,18 @@ using namespace rows;
 // the input and nothing depends on the order of atomics.  By size:
 //   1 tile         one CTA, one launch
 //   2 .. 8 tiles   one cluster, one launch: the CTAs read each other's counts
-//                  through distributed shared memory
+//                  and hand the elements from pass to pass through distributed
+//                  shared memory (one tile: through its own)
 //   more           one launch per pass over up to kMaxCtas CTAs, and one that
 //                  counts for the first pass; placing an element counts its next
 //                  digit for the CTA that will read it there
 // The kernels are bound by latency (launches, barriers, chains of dependent
 // loads); measured in a graph with 8 choices per token and 128 keys: 16 tokens
-// 3.5 us, 256 tokens 4.7 us, 1024 tokens 6.1 us (7.4 us as two launches), 16384
+// 3.5 us, 256 tokens 4.7 us, 1024 tokens 5.6 us (7.4 us as two launches), 16384
 // tokens 12.8 us; 32768 ids over 131072 keys (two passes and the offsets) 22 us.
+// Elements handed on in shared memory against a round trip through L2: 2048 ids
+// over 50000 keys 11.8 us against 13.7 us, 8192 ids 16.3 us against 17.9 us, 2049
+// ids over 300000 keys (three passes) 16.3 us against 21.9 us.
 // One cluster over everything, with ranks from match_any, took 56 us for 16384
 // tokens (8 SMs' issue slots); 16 CTAs per cluster gained nothing over 8.
 constexpr int kDigitBits = 9;
@@ -71,8 +75,8 @@ __device__ __forceinline__ int32_t load_key(const SortArgs& a, int32_t f) {
     return a.n_keys;
 }
 
-// Input of a pass: the ids, or the result of the pass before (written by other
-// SMs or earlier in this kernel, so read past L1).
+// Input of a pass of more than a cluster: the ids, or the result of the pass
+// before (written by other SMs, so read past L1).
 __device__ __forceinline__ int32_t pass_key(const SortArgs& a, int pass, int32_t i) {
     return pass ? __ldcg(((pass & 1) ? a.keys0 : a.keys1) + i) : load_key(a, i);
 }
@@ -119,6 +123,14 @@ __device__ __forceinline__ void first_places(const SortArgs& a, int32_t all, int
     __syncthreads();
 }
 
+// The elements of a CTA's tile on their way from one pass to the next, for
+// inputs of one cluster at most (so an index fits 16 bits).
+struct Exchange {
+    int32_t key[kTile];
+    uint16_t idx[kTile];
+};
+static_assert(kMaxCluster * kTile <= 65536, "indexes of a cluster's elements fit 16 bits");
+
 // A thread's elements of a tile: consecutive ones per warp.  Key -1 past the end.
 struct Items {
     int32_t key[kItems], idx[kItems];
@@ -129,6 +141,14 @@ struct Items {
             const int32_t at = static_cast<int32_t>(i);
             key[j] = i < i1 ? pass_key(a, pass, at) : -1;
             idx[j] = i < i1 && pass ? __ldcg(((pass & 1) ? a.idx0 : a.idx1) + at) : at;
+        }
+    }
+    __device__ __forceinline__ void load(const Exchange& x, int32_t n) {  // n elements of the tile
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const int i = (threadIdx.x >> 5) * (32 * kItems) + j * 32 + (threadIdx.x & 31);
+            key[j] = i < n ? x.key[i] : -1;
+            idx[j] = i < n ? x.idx[i] : 0;
         }
     }
 };
@@ -173,6 +193,32 @@ __device__ __forceinline__ int32_t scan_warps(SortShared& s, int32_t start) {
         run += c[w];
     }
     return run - start;
+}
+
+// Sends items to the places of an intermediate pass, in the tile of CTA
+// p / kTile of the cluster (CLUSTER) or in this CTA's.
+template <bool CLUSTER>
+__device__ __forceinline__ void send_items(const SortArgs& a, int shift, const Items& it, const int32_t (&rank)[kItems],
+                                           Exchange& x, const SortShared& s) {
+    const int warp = threadIdx.x >> 5, bins = 1 << a.bits;
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+        if (it.key[j] < 0) continue;
+        const int digit = (it.key[j] >> shift) & (bins - 1);
+        const int32_t p = s.hist[warp][digit] + rank[j] + s.first[digit], at = p % kTile;
+        if (CLUSTER) {
+            const uint32_t cta = p / kTile;
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::map_shared(ptx::smem_u32(&x.key[at]), cta)),
+                         "r"(it.key[j])
+                         : "memory");
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(ptx::map_shared(ptx::smem_u32(&x.idx[at]), cta)),
+                         "h"(static_cast<uint16_t>(it.idx[j]))
+                         : "memory");
+        } else {
+            x.key[at] = it.key[j];
+            x.idx[at] = static_cast<uint16_t>(it.idx[j]);
+        }
+    }
 }
 
 // Writes a tile's items at first(digit) + hist + rank.
@@ -225,17 +271,24 @@ __device__ __forceinline__ void place_elements(const SortArgs& a, int pass, int3
 // All passes over one tile in one CTA; the digits' counts come with the ranks.
 __global__ void __launch_bounds__(kSortThreads) route_small_kernel(const SortArgs a) {
     __shared__ SortShared s;
+    __shared__ Exchange x;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     for (int pass = 0; pass < a.passes; ++pass) {
         Items it;
         int32_t rank[kItems];
-        it.load(a, pass, 0, a.n);
+        if (pass == 0)
+            it.load(a, 0, 0, a.n);
+        else
+            it.load(x, a.n);
         rank_items(a, pass * a.bits, it, rank, s);
         __syncthreads();
         const int32_t all = static_cast<int>(threadIdx.x) < (1 << a.bits) ? scan_warps(s, 0) : 0;
         first_places(a, all, 0, a.passes == 1, s);
-        write_items(a, pass, it, rank, nullptr, s, true);
+        if (pass + 1 < a.passes)
+            send_items<false>(a, pass * a.bits, it, rank, x, s);
+        else
+            write_items(a, pass, it, rank, nullptr, s, true);
         __syncthreads();
     }
 }
@@ -246,10 +299,10 @@ __device__ __forceinline__ int32_t ld_cluster(const int32_t* p, uint32_t rank) {
     return v;
 }
 
-// All passes over up to kMaxCluster tiles in one cluster, a tile per CTA: the
-// CTAs read each other's counts through distributed shared memory.
+// All passes over up to kMaxCluster tiles in one cluster, a tile per CTA.
 __global__ void __launch_bounds__(kSortThreads) route_cluster_kernel(const SortArgs a) {
     __shared__ SortShared s;
+    __shared__ Exchange x;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int cta = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
@@ -257,7 +310,10 @@ __global__ void __launch_bounds__(kSortThreads) route_cluster_kernel(const SortA
     for (int pass = 0; pass < a.passes; ++pass) {
         Items it;
         int32_t rank[kItems];
-        it.load(a, pass, i0, i1);
+        if (pass == 0)
+            it.load(a, 0, i0, i1);
+        else
+            it.load(x, i1 - i0);
         rank_items(a, pass * a.bits, it, rank, s);
         __syncthreads();
         const bool used = static_cast<int>(threadIdx.x) < (1 << a.bits);
@@ -274,7 +330,11 @@ __global__ void __launch_bounds__(kSortThreads) route_cluster_kernel(const SortA
         }
         ptx::cluster_sync_all();  // every CTA has read the counts
         first_places(a, all, below, a.passes == 1 && cta == 0, s);
-        write_items(a, pass, it, rank, nullptr, s, true);
+        if (pass + 1 == a.passes) {
+            write_items(a, pass, it, rank, nullptr, s, true);
+            break;
+        }
+        send_items<true>(a, pass * a.bits, it, rank, x, s);
         ptx::cluster_sync_all();  // this pass's results are written
     }
 }
