@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
     ptx::grid_dep_wait();
     const int64_t t = blockIdx.x;
     const int64_t id =
-        a.wide ? __ldg(static_cast<const int64_t*>(a.ids) + t) : __ldg(static_cast<const int32_t*>(a.ids) + t);
+        a.wide ? static_cast<const int64_t*>(a.ids)[t] : static_cast<const int32_t*>(a.ids)[t];
     const bool live = id >= 0 && id < a.V;
     if (id >= a.V && threadIdx.x == 0) atomicOr(a.err, SPMM_DEVERR_INDEX);
     const T* row = static_cast<const T*>(a.table) + (live ? id : 0) * a.ldt;
@@ -89,7 +89,7 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int
     using O = Vec<TO, V>;
     TO* out = static_cast<TO*>(a.out) + v * a.ldo + c;
     float f[V] = {};
-    if (a.accumulate) O::unpack(O::load_plain(out), f);
+    if (a.accumulate) O::unpack(O::load(out), f);
 #pragma unroll
     for (int k = 0; k < V; ++k) f[k] = fmaf(a.scale, acc[k], f[k]);
     O::store_cs(out, O::pack(f));
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
         const int64_t v0 = (block - a.chunks * pieces) * kZeroRows;
         int32_t start[kZeroRows + 1];
 #pragma unroll
-        for (int i = 0; i <= kZeroRows; ++i) start[i] = __ldg(a.offsets + (v0 + i < a.V ? v0 + i : a.V));
+        for (int i = 0; i <= kZeroRows; ++i) start[i] = a.offsets[v0 + i < a.V ? v0 + i : a.V];
 #pragma unroll
         for (int i = 0; i < kZeroRows; ++i) {
             if (v0 + i >= a.V || start[i] != start[i + 1]) continue;
@@ -121,14 +121,14 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
         return;
     }
     const int64_t chunk = block / pieces, p0 = chunk * kChunk;
-    const int64_t kept = __ldg(a.offsets + a.V);
+    const int64_t kept = a.offsets[a.V];
     if (p0 >= kept) return;
     const int n = static_cast<int>(kept - p0 < kChunk ? kept - p0 : kChunk);
     for (int i = threadIdx.x; i < kChunk + 2; i += blockDim.x) {
         const int64_t p = p0 + i - 1;
         const bool in = p >= 0 && p < kept;
-        key[i] = in ? __ldg(a.keys + p) : -1;
-        if (i >= 1 && i <= kChunk) token[i - 1] = in ? __ldg(a.order + p) : 0;
+        key[i] = in ? a.keys[p] : -1;
+        if (i >= 1 && i <= kChunk) token[i - 1] = in ? a.order[p] : 0;
     }
     __syncthreads();
     const int64_t c = ((block - chunk * pieces) * blockDim.x + threadIdx.x) * V;
@@ -204,10 +204,10 @@ __global__ void __launch_bounds__(kRowThreads) embed_join_kernel(const EmbedGrad
         const int64_t p = (first + threadIdx.x) * kChunk;
         int32_t v = -1, end = 0;
         if (p < a.T) {
-            const int32_t here = __ldg(a.keys + p), before = __ldg(a.keys + p - 1);
-            if (here == before && here < a.V && __ldg(a.offsets + here) >= p - kChunk) {
+            const int32_t here = a.keys[p], before = a.keys[p - 1];
+            if (here == before && here < a.V && a.offsets[here] >= p - kChunk) {
                 v = here;
-                end = __ldg(a.offsets + here + 1);
+                end = a.offsets[here + 1];
             }
         }
         row[threadIdx.x] = v;

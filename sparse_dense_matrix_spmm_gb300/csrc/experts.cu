@@ -117,8 +117,8 @@ struct Walk {
     }
     __device__ void window() {
         const int e = e0 + lane;
-        start = e < a.E ? __ldg(a.offsets + e) : 0;
-        cnt = e < a.E ? __ldg(a.offsets + e + 1) - start : 0;
+        start = e < a.E ? a.offsets[e] : 0;
+        cnt = e < a.E ? a.offsets[e + 1] - start : 0;
         incl = (cnt + TILE - 1) / TILE * a.m_tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -133,8 +133,8 @@ struct Walk {
             w.e = u / per;
             int mt, nt;
             tile_of(u - w.e * per, a.m_tiles, a.n_tiles, mt, nt);
-            w.p0 = __ldg(a.offsets + w.e);
-            w.cnt = __ldg(a.offsets + w.e + 1) - w.p0;
+            w.p0 = a.offsets[w.e];
+            w.cnt = a.offsets[w.e + 1] - w.p0;
             w.m0 = mt * 128 * CG;
             w.n0 = nt * TILE;
             w.live = min(TILE, a.n - w.n0);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!DW) {
-            for (int64_t p = __ldg(a.offsets + a.E) + static_cast<int64_t>(blockIdx.x); p < a.R; p += gridDim.x) {
+            for (int64_t p = a.offsets[a.E] + static_cast<int64_t>(blockIdx.x); p < a.R; p += gridDim.x) {
                 uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + p * a.ldo);
                 for (int c = lane; c < a.m / 8; c += 32) row[c] = make_uint4(0, 0, 0, 0);
             }
@@ -685,8 +685,8 @@ __device__ __forceinline__ void dot_rows(const VecArgs& a, const T* w0, const T*
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
             const int k = k0 + 256 * i;
-            r[0][i] = k < a.K ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : V::zero();
-            r[1][i] = k < a.K ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : V::zero();
+            r[0][i] = k < a.K ? ptx::ld_global_cs(reinterpret_cast<const uint4*>(w0 + k)) : V::zero();
+            r[1][i] = k < a.K ? ptx::ld_global_cs(reinterpret_cast<const uint4*>(w1 + k)) : V::zero();
         }
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
@@ -733,19 +733,19 @@ __global__ void __launch_bounds__(kVecWarps * 32, 4) experts_vec_kernel(const Ve
     if (n >= a.N) return;
     T* out = static_cast<T*>(a.out) + p * a.ldo + n;
     const bool two = n + 1 < a.N;
-    if (p >= __ldg(a.offsets + a.E)) {
+    if (p >= a.offsets[a.E]) {
         if (lane < 2 && (lane == 0 || two)) out[lane] = rows::from_f32<T>(0.f);
         return;
     }
     int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, at = lo + step * lane;
-        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldg(a.offsets + at) <= p);
+        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= p);
         lo += step * (31 - __clz(le));
         hi = min(hi, lo + step);
     }
-    if ((p - __ldg(a.offsets + lo)) % kVecRows) return;
-    const int rows = min(kVecRows, __ldg(a.offsets + lo + 1) - p);
+    if ((p - a.offsets[lo]) % kVecRows) return;
+    const int rows = min(kVecRows, a.offsets[lo + 1] - p);
     const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
     const T* w0 = static_cast<const T*>(a.W) + lo * a.lde + n * a.ldw;
     const T* w1 = two ? w0 + a.ldw : w0;
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kDwThreads, 4) experts_dw_vec_kernel(const DwA
     grid_dep_launch();
     grid_dep_wait();
     const int64_t e = blockIdx.y, n0 = static_cast<int64_t>(blockIdx.x) * kDwRows;
-    const int32_t p0 = __ldg(a.offsets + e), cnt = __ldg(a.offsets + e + 1) - p0;
+    const int32_t p0 = a.offsets[e], cnt = a.offsets[e + 1] - p0;
     const T* dys = static_cast<const T*>(a.dys) + p0 * a.ldd + n0;
     const T* xs = static_cast<const T*>(a.xs) + p0 * a.ldx;
     T* out = static_cast<T*>(a.dW) + e * a.lde + n0 * a.ldw;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kDwThreads, 4) experts_dw_vec_kernel(const DwA
                 __syncthreads();
                 if (static_cast<int>(threadIdx.x) < nc * kDwRows) {  // N % 8 == 0: every row exists
                     const int c = threadIdx.x / kDwRows, r = threadIdx.x % kDwRows;
-                    const float v = rows::to_f32<T>(__ldg(dys + (c0 + c) * a.ldd + r));
+                    const float v = rows::to_f32<T>(dys[(c0 + c) * a.ldd + r]);
                     d[c][r] = pair_f32(v, v);
                 }
                 __syncthreads();

@@ -69,7 +69,7 @@ __device__ __forceinline__ int32_t load_key(const SortArgs& a, int32_t f) {
         at = t * a.ldi + (f - t * a.k);
     }
     const int64_t v =
-        a.wide ? __ldg(static_cast<const int64_t*>(a.ids) + at) : __ldg(static_cast<const int32_t*>(a.ids) + at);
+        a.wide ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
     if (v >= 0 && v < a.n_keys) return static_cast<int32_t>(v);
     if (v >= 0) atomicOr(a.err, SPMM_DEVERR_INDEX);
     return a.n_keys;
@@ -78,7 +78,7 @@ __device__ __forceinline__ int32_t load_key(const SortArgs& a, int32_t f) {
 // Input of a pass of more than a cluster: the ids, or the result of the pass
 // before (written by other SMs, so read past L1).
 __device__ __forceinline__ int32_t pass_key(const SortArgs& a, int pass, int32_t i) {
-    return pass ? __ldcg(((pass & 1) ? a.keys0 : a.keys1) + i) : load_key(a, i);
+    return pass ? ptx::ld_global_cg(((pass & 1) ? a.keys0 : a.keys1) + i) : load_key(a, i);
 }
 
 __device__ __forceinline__ int32_t warp_scan(int32_t v, int lane) {  // inclusive
@@ -140,7 +140,7 @@ struct Items {
             const int64_t i = tile + (threadIdx.x >> 5) * (32 * kItems) + j * 32 + (threadIdx.x & 31);
             const int32_t at = static_cast<int32_t>(i);
             key[j] = i < i1 ? pass_key(a, pass, at) : -1;
-            idx[j] = i < i1 && pass ? __ldcg(((pass & 1) ? a.idx0 : a.idx1) + at) : at;
+            idx[j] = i < i1 && pass ? ptx::ld_global_cg(((pass & 1) ? a.idx0 : a.idx1) + at) : at;
         }
     }
     __device__ __forceinline__ void load(const Exchange& x, int32_t n) {  // n elements of the tile
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const SortArg
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int c = c0 + i + cta < ctas ? c0 + i + cta : c0 + i + cta - ctas;
-                v[i] = c0 + i < ctas ? __ldcg(table + c * bins + threadIdx.x) : 0;
+                v[i] = c0 + i < ctas ? ptx::ld_global_cg(table + c * bins + threadIdx.x) : 0;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -402,20 +402,20 @@ __global__ void __launch_bounds__(kOffsetThreads)
     int64_t lo = 0, hi = n;  // the answer for e0 lies in [lo, hi]
     while (lo < hi) {
         const int64_t step = (hi - lo + kOffsetThreads - 1) / kOffsetThreads, at = lo + threadIdx.x * step;
-        const int64_t below = __syncthreads_count(at < hi && __ldcg(sorted + at) < e0);
+        const int64_t below = __syncthreads_count(at < hi && ptx::ld_global_cg(sorted + at) < e0);
         hi = min(hi, lo + below * step);
         if (below) lo += (below - 1) * step + 1;
     }
     if (e > n_keys) return;
     int64_t step = 1;
-    while (lo + step <= n && __ldg(sorted + lo + step - 1) < e) {
+    while (lo + step <= n && sorted[lo + step - 1] < e) {
         lo += step;
         step *= 2;
     }
     hi = min(int64_t(n), lo + step - 1);
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (__ldg(sorted + mid) < e)
+        if (sorted[mid] < e)
             lo = mid + 1;
         else
             hi = mid;
@@ -443,7 +443,7 @@ struct RowArgs {
 // Rows past the last kept place are written as zeros, spread over the grid.
 template <typename T, int V>
 __device__ __forceinline__ void zero_tail(const RowArgs& a, T* out) {
-    for (int64_t p = __ldg(a.offsets + a.n_keys) + static_cast<int64_t>(blockIdx.x); p < a.T * a.k; p += gridDim.x)
+    for (int64_t p = a.offsets[a.n_keys] + static_cast<int64_t>(blockIdx.x); p < a.T * a.k; p += gridDim.x)
         for (int64_t c = threadIdx.x * V; c < a.H; c += blockDim.x * V)
             Vec<T, V>::store_cs(out + p * a.ldo + c, Vec<T, V>::zero());
 }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const RowArg
         typename X::Raw r[X::U];
         X::load(r, x, c, a.H, step);
         for (int j = 0; j < a.k; ++j) {
-            const int64_t p = __ldg(pos + j);
+            const int64_t p = pos[j];
             if (p >= 0) X::store_cs(out + p * a.ldo, r, c, a.H, step);
         }
     }
@@ -488,13 +488,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
             bool live[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int64_t p = j0 + j < a.k ? __ldg(a.pos + f0 + j0 + j) : -1;
+                const int64_t p = j0 + j < a.k ? a.pos[f0 + j0 + j] : -1;
                 live[j] = p >= 0;
                 if (live[j])
                     X::load(r[j], ys + p * a.lda, c, a.H, step);
                 else
                     X::clear(r[j]);
-                w[j] = a.w && live[j] ? __ldg(a.w + f0 + j0 + j) : 1.f;
+                w[j] = a.w && live[j] ? a.w[f0 + j0 + j] : 1.f;
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs
         float w[kBatch], dot[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            p[j] = j0 + j < a.k ? __ldg(a.pos + f0 + j0 + j) : -1;
-            w[j] = p[j] >= 0 ? __ldg(a.w + f0 + j0 + j) : 0.f;
+            p[j] = j0 + j < a.k ? a.pos[f0 + j0 + j] : -1;
+            w[j] = p[j] >= 0 ? a.w[f0 + j0 + j] : 0.f;
             dot[j] = 0.f;
         }
         for (int64_t c = threadIdx.x * V; c < a.H; c += X::U * step) {

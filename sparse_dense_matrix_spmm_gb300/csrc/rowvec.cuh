@@ -8,6 +8,8 @@
 #include <cstring>
 #include <type_traits>
 
+#include "sm103_more.cuh"
+
 namespace spmm {
 namespace rows {
 
@@ -89,20 +91,14 @@ struct Vec {
     static __device__ __forceinline__ Raw load(const T* p) {
         Raw r;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) words(r)[i] = __ldg(reinterpret_cast<const W*>(p) + i);
+        for (int i = 0; i < kWords; ++i) words(r)[i] = reinterpret_cast<const W*>(p)[i];
         return r;
     }
     // data read once: leaves the caches first
     static __device__ __forceinline__ Raw load_cs(const T* p) {
         Raw r;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) words(r)[i] = __ldcs(reinterpret_cast<const W*>(p) + i);
-        return r;
-    }
-    static __device__ __forceinline__ Raw load_plain(const T* p) {  // data this kernel also writes
-        Raw r;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) words(r)[i] = reinterpret_cast<const W*>(p)[i];
+        for (int i = 0; i < kWords; ++i) words(r)[i] = ptx::ld_global_cs(reinterpret_cast<const W*>(p) + i);
         return r;
     }
     static __device__ __forceinline__ void store(T* p, const Raw& r) {

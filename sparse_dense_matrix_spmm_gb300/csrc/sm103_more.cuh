@@ -13,8 +13,44 @@ namespace ptx {
 // once every earlier kernel has finished and its writes are visible; nothing of
 // theirs may be read or overwritten before it.  grid_dep_launch lets the next
 // kernel's CTAs be scheduled.
+// A chained kernel is resident while its predecessor still writes, so it must not
+// read what that may have written (any operand) by non-coherent loads: those are
+// for memory that is read-only for the kernel's lifetime, and the compiler may
+// move them over the wait.  It reads by ordinary loads, which the wait's memory
+// clobber keeps behind it, or by ld_global_cg / ld_global_cs below, which are
+// volatile and so stay behind it too.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Past L1.
+__device__ __forceinline__ int32_t ld_global_cg(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+// Data read once: leaves the caches first.
+__device__ __forceinline__ uint16_t ld_global_cs(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_global_cs(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_global_cs(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_global_cs(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
 // Two fp32 products and sums in one instruction, each rounded as fmaf rounds.
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
