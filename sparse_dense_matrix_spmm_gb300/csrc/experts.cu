@@ -204,6 +204,7 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
         const uint32_t stage = buffers + odd * 2048;
         const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
         uint32_t lo[16], hi[16];
+        __syncwarp();  // TMEM loads are .aligned; the warp comes from a spinning wait or one thread's store
         tmem_ld_16x32(t + c, lo);
         tmem_ld_16x32(t + (16u << 16) + c, hi);
         tmem_ld_wait();
@@ -244,6 +245,7 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap*
     for (int c = c0; c < c1; c += 64, odd ^= 1) {
         const uint32_t stage = buffers + odd * 4096;
         uint32_t v[4][16];
+        __syncwarp();  // as in store_rows
         if (w.steps == 0) {
 #pragma unroll
             for (int h = 0; h < 4; ++h)

@@ -29,3 +29,37 @@ def test_cluster_barrier_brings_its_warps_together():
     body = _body(_code("sm103_more.cuh"), r"void cluster_sync_all\(\)")
     assert ".aligned" in body
     assert body.index("__syncwarp()") < body.index("asm")
+
+
+# What may leave a warp's threads apart, what brings them together, what needs them together.
+_APART = r"if \(lane|mbar_wait\w*\(|mbar_try_wait\("
+_TOGETHER = r"__syncwarp\(\)|__syncthreads\(\)|__shfl\w*_sync\(|__ballot_sync\(|__all_sync\(|cluster_sync_all\(\)|sync_all<"
+_NEEDS = r"tmem_ld\w*\(|stmatrix_\w+\("
+
+
+def _unsafe(body, apart):
+    """The first collective call that a warp may reach apart, walking the text in order."""
+    for m in re.finditer(f"(?P<apart>{_APART})|(?P<together>{_TOGETHER})|(?P<needs>{_NEEDS})", body):
+        if m.group("together"):
+            apart = False
+        elif m.group("apart"):
+            apart = True
+        elif apart:
+            return m.group(0)
+    return None
+
+
+def test_the_walk_itself():
+    assert _unsafe("mbar_wait(x); tmem_ld16(t);", False) == "tmem_ld16("
+    assert _unsafe("mbar_wait(x); __syncwarp(); tmem_ld16(t);", False) is None
+    assert _unsafe("tmem_ld16(t); if (lane == 0) {}", False) is None
+
+
+def test_experts_read_tmem_together():
+    """The epilogue's loops are entered from a wait that each thread spins in, and go round after one thread's store."""
+    code = _code("experts.cu")
+    for head in (r"void store_rows\(", r"void store_dw\("):
+        body = _body(code, head)
+        loop = body[body.index("for (int c = c0"):]
+        assert re.search(_NEEDS, loop)
+        assert _unsafe(loop + loop, True) is None, head
