@@ -556,7 +556,16 @@ def _row_code(dtype) -> int:
 
 
 def _handle(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    """The raw handle of the call's stream.  The library launches on the current device, so operands or a
+    stream of another one are refused."""
+    current = torch._C._cuda_getDevice()
+    if device.index != current:
+        raise ValueError(f"operands are on {device}, but the current device is cuda:{current} (torch.cuda.set_device)")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(current)
+    if stream.device_index != current:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, but the current device is cuda:{current}")
+    return stream.cuda_stream
 
 
 def _empty(like: torch.Tensor, shape, dtype, stream):
