@@ -531,15 +531,25 @@ class Route:
     """T x k ids sorted by value: order (flat indices, dropped ones last), pos
     (place of each flat index, -1 if dropped), offsets (first place per key) and,
     for k = 1, keys (the sorted ids, n_keys if dropped).  All int32 on the device;
-    pos has the ids' shape.  A route does not change after it is built."""
+    pos has the ids' shape.  A route does not change after it is built: its C
+    struct holds the tensors' addresses, so assigning to a field raises.  Copies
+    and pickles build a struct of their own."""
 
     def __init__(self, T: int, k: int, n_keys: int, order: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor,
                  keys: Optional[torch.Tensor] = None):
-        self.T, self.k, self.n_keys, self.n_rows = T, k, n_keys, T * k
-        self.order, self.pos, self.offsets, self.keys = order, pos, offsets, keys
-        self.device, self.shape = order.device, pos.shape
-        self._ref = C.byref(_lib.RouteT(T, k, n_keys, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
-                                        None if keys is None else keys.data_ptr()))
+        ref = C.byref(_lib.RouteT(T, k, n_keys, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
+                                  None if keys is None else keys.data_ptr()))
+        self.__dict__.update(T=T, k=k, n_keys=n_keys, n_rows=T * k, order=order, pos=pos, offsets=offsets, keys=keys,
+                             device=order.device, shape=pos.shape, _ref=ref)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"cannot assign to {name}: a route does not change after it is built")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"cannot delete {name}: a route does not change after it is built")
+
+    def __reduce__(self):
+        return Route, (self.T, self.k, self.n_keys, self.order, self.pos, self.offsets, self.keys)
 
     def c(self) -> _lib.RouteT:
         return self._ref._obj

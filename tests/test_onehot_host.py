@@ -1,5 +1,7 @@
 """What the one-hot wrappers do on the host, without a GPU."""
+import copy
 import inspect
+import pickle
 from types import SimpleNamespace
 
 import pytest
@@ -27,3 +29,42 @@ def test_every_wrapper_asks_for_the_handle():
     for f in (spmm.spmm_build_route, spmm.spmm_dispatch, spmm.spmm_combine, spmm.spmm_combine_grad, spmm.spmm_embed,
               spmm.spmm_embed_grad, spmm.spmm_experts, spmm.spmm_experts_dx, spmm.spmm_experts_dw):
         assert "_handle(stream, " in inspect.getsource(f), f.__name__
+
+
+def _route(keys=True):
+    i32 = torch.int32
+    return spmm.Route(5, 1, 3, torch.arange(5, dtype=i32), torch.arange(5, dtype=i32),
+                      torch.tensor([0, 2, 3, 5], dtype=i32), torch.zeros(5, dtype=i32) if keys else None)
+
+
+def _holds_its_own(R):
+    c = R.c()
+    assert (c.T, c.k, c.n_keys) == (R.T, R.k, R.n_keys) and R.n_rows == R.T * R.k
+    assert c.order == R.order.data_ptr() and c.pos == R.pos.data_ptr() and c.offsets == R.offsets.data_ptr()
+    assert c.keys == (None if R.keys is None else R.keys.data_ptr())
+
+
+@pytest.mark.parametrize("name", ["T", "k", "n_keys", "n_rows", "order", "pos", "offsets", "keys", "device", "shape"])
+def test_route_fields_cannot_be_replaced(name):
+    """The C struct holds the tensors' addresses: a replaced tensor would leave the kernels on freed memory."""
+    R = _route()
+    _holds_its_own(R)
+    before = getattr(R, name)
+    with pytest.raises(AttributeError, match="does not change"):
+        setattr(R, name, before)
+    with pytest.raises(AttributeError, match="does not change"):
+        delattr(R, name)
+    assert getattr(R, name) is before
+    _holds_its_own(R)
+
+
+@pytest.mark.parametrize("keys", [True, False])
+def test_routes_are_copied_with_structs_of_their_own(keys):
+    R = _route(keys)
+    shallow, deep, thawed = copy.copy(R), copy.deepcopy(R), pickle.loads(pickle.dumps(R))
+    for S in (shallow, deep, thawed):
+        _holds_its_own(S)
+        assert torch.equal(S.order, R.order) and torch.equal(S.pos, R.pos) and torch.equal(S.offsets, R.offsets)
+        assert S.shape == R.shape and S.device == R.device
+    assert shallow.pos is R.pos
+    assert deep.pos.data_ptr() != R.pos.data_ptr() and thawed.pos.data_ptr() != R.pos.data_ptr()
