@@ -46,6 +46,16 @@ constexpr int kDepth = 64;  // contraction per stage: 128 bytes, one swizzle row
 constexpr int kABytes = 128 * 128;
 constexpr int kSmemMax = 232448;  // 227 KB, the most a CTA can have
 constexpr int kUnits = 4;         // work units announced ahead
+// A wait may span a unit, and at the end the units announced ahead of it, and a
+// unit has as many steps as its depth has blocks of 64 (dw: the rows of an
+// expert).  So the limit of a wait grows with the most steps that a unit can have:
+// 2 us for each, where a step takes 0.3 us and, with every SM streaming from HBM,
+// 0.7.  (At 2 s flat, dw of 8 x 8 over 400 million rows, 0.33 us a step, gave up.)
+constexpr uint64_t kStepLimitNs = 2000;
+constexpr uint64_t wait_limit_ns(int64_t most_depth) {
+    const uint64_t steps = (static_cast<uint64_t>(most_depth) + kDepth - 1) / kDepth;
+    return kWaitTimeoutNs + steps * (kUnits + 1) * kStepLimitNs;
+}
 // Variants by size, all on averages that the host knows.
 // Row tiles of 64 instead of 256 up to this many rows per expert: nine stages fit
 // instead of six (64 tokens x 8 of 128 experts, 1536 x 4096: 226 us against 240).
@@ -899,7 +909,7 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
     a.ldo = ldo;
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
-    a.timeout_ns = kWaitTimeoutNs;
+    a.timeout_ns = wait_limit_ns(a.depth);
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     const int tile = pair && n <= E * kFewRows ? 64 : 256;
@@ -951,7 +961,7 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     a.lde = lde;
     a.bf16 = dtype == SPMM_BF16;
     a.err = dev->err;
-    a.timeout_ns = kWaitTimeoutNs;
+    a.timeout_ns = wait_limit_ns(n);
     const bool pair = a.m > 128;
     a.m_tiles = pair ? (a.m + 255) / 256 : (a.m + 127) / 128;
     a.n_tiles = (a.n + 255) / 256;
