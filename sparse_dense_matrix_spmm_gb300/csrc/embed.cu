@@ -43,7 +43,7 @@ struct EmbedArgs {
 // One CTA per token.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
-    using X = Cols<T, V, 2, 1>;  // narrow moves one at a time, 20 to 25% faster than four
+    using X = Cols<T, V, 2, 2>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int64_t t = blockIdx.x;
@@ -138,8 +138,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
     float acc[V] = {};
     for (int i0 = 0; i0 < n; i0 += kFlight) {
         typename X::Raw r[kFlight];
+        if (i0 + kFlight <= n) {  // loads without a test each: 4095 columns 139 us, with 144
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) r[i] = i0 + i < n ? X::load_cs(dy + token[i0 + i] * a.ldy) : X::zero();
+            for (int i = 0; i < kFlight; ++i) r[i] = X::load_cs(dy + token[i0 + i] * a.ldy);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) r[i] = i0 + i < n ? X::load_cs(dy + token[i0 + i] * a.ldy) : X::zero();
+        }
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
             if (i0 + i >= n) break;

@@ -480,25 +480,35 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
     T* y = static_cast<T*>(a.out) + blockIdx.x * a.ldo;
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.k;
     const int step = blockDim.x * V;
+    int64_t p[kBatch];  // places of the batch's rows, and their weights
+    float w[kBatch];
+    const auto choices = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            p[j] = j0 + j < a.k ? a.pos[f0 + j0 + j] : -1;
+            w[j] = a.w && p[j] >= 0 ? a.w[f0 + j0 + j] : 1.f;
+        }
+    };
+    // up to four choices are read once where the moves are narrow and the columns take
+    // many rounds (4095: 76 us, read every round 81); at full width the registers
+    // cost more than the reads (4096: 53 us, read every round 51)
+    constexpr bool kOnce = X::U > 1;
+    if (kOnce) choices(0);
     for (int64_t c = threadIdx.x * V; c < a.H; c += X::U * step) {
         float acc[X::N] = {};
         for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+            if (!kOnce || a.k > kBatch) choices(j0);
             typename X::Raw r[kBatch][X::U];
-            float w[kBatch];
-            bool live[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int64_t p = j0 + j < a.k ? a.pos[f0 + j0 + j] : -1;
-                live[j] = p >= 0;
-                if (live[j])
-                    X::load(r[j], ys + p * a.lda, c, a.H, step);
+                if (p[j] >= 0)
+                    X::load(r[j], ys + p[j] * a.lda, c, a.H, step);
                 else
                     X::clear(r[j]);
-                w[j] = a.w && live[j] ? a.w[f0 + j0 + j] : 1.f;
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                if (!live[j]) continue;  // not 0 * w: a weight may be infinite
+                if (p[j] < 0) continue;  // not 0 * w: a weight may be infinite
                 float v[X::N];
                 X::unpack(r[j], v);
 #pragma unroll
@@ -515,9 +525,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
 // with ys, each summed in fp32 per thread, then over the CTA in a fixed order.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowArgs a) {
-    // single 16-bit values one per row: four hold 91 registers, 166 us against 148
-    // at H = 4095 below
-    using X = Cols<T, V, 1, V * sizeof(T) == 2 ? 1 : 4>;
+    using X = Cols<T, V>;
     __shared__ float part[kBatch][kRowThreads / 32];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();

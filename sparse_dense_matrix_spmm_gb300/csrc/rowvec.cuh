@@ -150,19 +150,27 @@ struct Vec {
 };
 
 // A thread's columns of a row: U vectors of V elements, `step` columns apart: at
-// full width WIDE, in narrower moves up to NARROW of them, so that they too have
-// many bytes in flight (8192 x 4 x 4095 bf16: dispatch 107 us with one at a time,
-// 83 us with four, 92 us with eight).  Column c + u step of vector u counts if
-// it lies below H.
-template <typename T, int V, int WIDE = 1, int NARROW = 4>
+// full width WIDE, in narrower moves as many as make 16 bytes, four at most, times
+// DEPTH, so that they too have many bytes in flight.  They are loaded before
+// anything is stored (the compiler may not move an ordinary load over a store) and
+// without a test each where all of them count.  8192 x 4 x 4095 bf16, dispatch: 107
+// us with one at a time, 77 us with four; 16384 tokens, embed: 124 us with one, 65
+// us with four, 57 us with eight.  Column c + u step of vector u counts if it lies
+// below H.
+template <typename T, int V, int WIDE = 1, int DEPTH = 1>
 struct Cols {
     static constexpr int kVecs = 16 / (V * static_cast<int>(sizeof(T)));
-    static constexpr int U = kVecs == 1 ? WIDE : kVecs < NARROW ? kVecs : NARROW, N = U * V;
+    static constexpr int U = kVecs == 1 ? WIDE : (kVecs < 4 ? kVecs : 4) * DEPTH, N = U * V;
     using X = Vec<T, V>;
     using Raw = typename X::Raw;
     static __device__ __forceinline__ void load(Raw (&r)[U], const T* row, int64_t c, int64_t H, int step) {
+        if (c + (U - 1) * step < H) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load(row + c + u * step) : X::zero();
+            for (int u = 0; u < U; ++u) r[u] = X::load(row + c + u * step);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load(row + c + u * step) : X::zero();
+        }
     }
     static __device__ __forceinline__ void load_cs(Raw (&r)[U], const T* row, int64_t c, int64_t H, int step) {
 #pragma unroll
@@ -213,11 +221,10 @@ inline bool rows_move(const void* p, int64_t ld, int64_t H, int es, int V) {
 // Elements per move that the base, pitch and row length of every operand allow,
 // 16 bytes at most.  What a width costs, 8192 tokens x 4 in bf16, microseconds:
 //   row length      4096 (16 B)  4100 (8 B)  4098 (4 B)  4095 (2 B)
-//   dispatch          52           54          64          83
-//   combine           51           55          64         117
-//   its gradient      92           97         109         148
-//   embed, 16384      41           44          49          63
-// Moving the three odd lengths element by element took 79, 152, 152 and 85.
+//   dispatch          52           54          64          77
+//   combine           51           55          58          76
+//   its gradient      92           97         105         137
+//   embed, 16384      41           43          45          57
 struct Operand {
     const void* p;
     int64_t ld;
