@@ -699,11 +699,11 @@ spmm_status spmm_combine_grad(const spmm_route_t* R, const void* dy, int64_t ldd
     spmm_status st = check_route(R, false);
     if (st != SPMM_OK) return st;
     if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
-    if (H <= 0 || bad_pitch(lddy, H) || bad_pitch(ldys, H) || bad_pitch(lddys, H)) return SPMM_ERR_SHAPE;
+    if (H < 0 || bad_pitch(lddy, H) || bad_pitch(ldys, H) || bad_pitch(lddys, H)) return SPMM_ERR_SHAPE;
     if (H >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
     if (R->T == 0) return SPMM_OK;
     if ((st = check_route(R, true)) != SPMM_OK) return st;
-    if (!dy || !ys || !w || !dys || !dw) return SPMM_ERR_NULL;
+    if (!w || !dw || (H > 0 && (!dy || !ys || !dys))) return SPMM_ERR_NULL;  // H = 0: dw is all zeros
     if (misaligned(dy, dtype) || misaligned(ys, dtype) || misaligned(dys, dtype) || misaligned(w, SPMM_F32) ||
         misaligned(dw, SPMM_F32))
         return SPMM_ERR_SHAPE;

@@ -240,9 +240,9 @@ int row_width(const Operand (&o)[N], int64_t H) {
     return 1;
 }
 
-// Threads of a CTA that moves rows of H elements, `per` of them each.
+// Threads of a CTA that moves rows of H elements, `per` of them each; at least a warp.
 inline int row_threads(int64_t H, int per, int most) {
-    const int64_t n = ((H + per - 1) / per + 31) / 32 * 32;
+    const int64_t n = H ? ((H + per - 1) / per + 31) / 32 * 32 : 32;
     return static_cast<int>(n < most ? n : most);
 }
 

@@ -1,0 +1,27 @@
+"""Forms of the row operators that need a case of their own, against plain definitions."""
+import numpy as np
+import pytest
+
+from tests.gpu_util import need_gpu
+from tests.onehot_util import DT
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_without_columns(dtype):
+    """H = 0: nothing to move, and the weights' gradient is a sum of nothing."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    T, k = 5, 3
+    ids = np.random.default_rng(1).integers(-1, 4, (T, k))
+    R = spmm.spmm_build_route(torch.from_numpy(ids).cuda(), 4)
+    x, ys = torch.empty((T, 0), dtype=DT[dtype], device="cuda"), torch.empty((T * k, 0), dtype=DT[dtype], device="cuda")
+    w = torch.ones((T, k), device="cuda")
+    assert spmm.spmm_dispatch(R, x).shape == (T * k, 0)
+    assert spmm.spmm_combine(R, ys, w).shape == (T, 0)
+    junk = torch.full((T, k), 9.0, device="cuda")  # what dw's memory may hold before
+    del junk
+    dys, dw = spmm.spmm_combine_grad(R, x, ys, w)
+    assert dys.shape == (T * k, 0) and dw.shape == (T, k) and not dw.any()
+    assert spmm.last_device_error() == 0

@@ -1,5 +1,6 @@
 """What the one-hot wrappers do on the host, without a GPU."""
 import copy
+import ctypes
 import inspect
 import pickle
 from types import SimpleNamespace
@@ -68,3 +69,17 @@ def test_routes_are_copied_with_structs_of_their_own(keys):
         assert S.shape == R.shape and S.device == R.device
     assert shallow.pos is R.pos
     assert deep.pos.data_ptr() != R.pos.data_ptr() and thawed.pos.data_ptr() != R.pos.data_ptr()
+
+
+def test_combine_grad_of_rows_without_columns_is_accepted():
+    """As spmm_dispatch and spmm_combine accept them.  Without tokens nothing is launched."""
+    from sparse_dense_matrix_spmm_gb300 import build
+    build.build()
+    L = spmm._lib.load()
+    R = ctypes.byref(spmm._lib.RouteT(0, 2, 4, 16, 16, 16, 16))
+    assert L.spmm_combine_grad(R, None, 0, None, 0, 16, None, 0, 16, 0, 0, None) == 0
+    assert L.spmm_combine_grad(R, None, 0, None, 0, 16, None, 0, 16, -1, 0, None) == 2
+    R = ctypes.byref(spmm._lib.RouteT(3, 2, 4, 16, 16, 16, 16))
+    assert L.spmm_combine_grad(R, None, 0, None, 0, None, None, 0, 16, 0, 0, None) == 1   # w
+    assert L.spmm_combine_grad(R, None, 0, None, 0, 16, None, 0, None, 0, 0, None) == 1   # dw
+    assert L.spmm_combine_grad(R, None, 8, 16, 8, 16, 16, 8, 16, 8, 0, None) == 1         # dy, with columns
