@@ -257,15 +257,23 @@ cudaError_t embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
     const int64_t zeros = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
     const int64_t blocks = a.chunks * pieces + zeros;
     if (blocks == 0) return cudaSuccess;
-    if (blocks >= (int64_t(1) << 31) || pieces >= 65536) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_chained(embed_grad_kernel<T, V, TO>, static_cast<unsigned>(blocks), threads, 0, 1, s, a,
-                                         static_cast<int>(pieces));
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorNotSupported;
+    cudaError_t e = launch_chained(embed_grad_kernel<T, V, TO>, static_cast<unsigned>(blocks), threads, 0, 1, s, a,
+                                   static_cast<int>(pieces));
     if (e != cudaSuccess || a.chunks < 2) return e;
     constexpr int VJ = V > 4 ? 4 : V;  // 16 bytes of a partial sum
-    const dim3 grid(static_cast<unsigned>((a.chunks - 1 + kBoundaries - 1) / kBoundaries),
-                    static_cast<unsigned>((a.H + kRowThreads * VJ - 1) / (kRowThreads * VJ)));
-    if (grid.y >= 65536) return cudaErrorInvalidConfiguration;
-    return launch_chained(embed_join_kernel<VJ, TO>, grid, kRowThreads, 0, 1, s, a);
+    constexpr int64_t kAcross = 65535, kSpan = kRowThreads * VJ;  // a grid's rows; columns of a piece
+    for (int64_t c = 0; c < a.H && e == cudaSuccess; c += kAcross * kSpan) {
+        EmbedGradArgs b = a;
+        b.H = a.H - c;
+        b.out = static_cast<TO*>(a.out) + c;
+        b.partial = a.partial + c;
+        if (b.H > kAcross * kSpan) b.H = kAcross * kSpan;
+        const dim3 grid(static_cast<unsigned>((a.chunks - 1 + kBoundaries - 1) / kBoundaries),
+                        static_cast<unsigned>((b.H + kSpan - 1) / kSpan));
+        e = launch_chained(embed_join_kernel<VJ, TO>, grid, kRowThreads, 0, 1, s, b);
+    }
+    return e;
 }
 
 template <typename T, int V>
@@ -336,7 +344,7 @@ spmm_status launch_embed_grad(const spmm_route_t* R, const void* dy, int64_t ldy
     else
         e = embed_grad_16<__nv_bfloat16>(a, v, f32, s);
     trace_end(SPMM_KERNEL_ROWS, s);
-    return cuda_status(e);
+    return e == cudaErrorNotSupported ? SPMM_ERR_UNSUPPORTED : cuda_status(e);  // a grid of 2^31 CTAs or more
 }
 
 }  // namespace spmm

@@ -25,3 +25,23 @@ def test_rows_without_columns(dtype):
     dys, dw = spmm.spmm_combine_grad(R, x, ys, w)
     assert dys.shape == (T * k, 0) and dw.shape == (T, k) and not dw.any()
     assert spmm.last_device_error() == 0
+
+
+@pytest.mark.parametrize("H", [256 * 65536 + 1, 256 * 65536 * 4 + 8])
+def test_table_gradient_of_very_long_rows(H):
+    """More pieces of the columns than a grid has rows, for a run that crosses a chunk of tokens."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    torch.cuda.empty_cache()
+    T = 70
+    ids = torch.ones(T, dtype=torch.int64, device="cuda")
+    ids[5] = 0
+    dy = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    for t in range(T):  # small integers: the sums are exact in fp32
+        dy[t] = torch.randint(-2, 3, (H,), device="cuda", dtype=torch.int8)
+    got = spmm.spmm_embed_grad(spmm.spmm_build_route(ids, 2), dy, out=torch.empty((2, H), device="cuda"))
+    want = torch.zeros(H, device="cuda")
+    for t in range(T):
+        if t != 5:
+            want += dy[t]
+    assert torch.equal(got[1], want) and torch.equal(got[0], dy[5].float())
