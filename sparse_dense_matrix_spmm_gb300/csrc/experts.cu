@@ -687,11 +687,11 @@ constexpr int kVecWarps = 8, kVecRows = 4, kVecFeatures = 2 * kVecWarps;
 
 // Two weight rows with C rows of xs.
 template <typename T, int C>
-__device__ __forceinline__ void dot_rows(const VecArgs& a, const T* w0, const T* w1, const T* x, T* out, bool two,
-                                         int lane) {
+__device__ __forceinline__ void dot_rows(const VecArgs& a, const T* w0, const T* w1, const T* x, T* out, int lane) {
     using V = rows::Vec<T, 8>;
     float acc[2][C] = {};
-    constexpr int kFlight = 2;  // per weight row; 4 spilled at four CTAs per SM
+    // per weight row; at four CTAs per SM (64 registers) 48-52 bytes of spills are loaded, with 4 128-140
+    constexpr int kFlight = 2;
     for (int k0 = lane * 8; k0 < a.K; k0 += 256 * kFlight) {
         uint4 r[2][kFlight];
 #pragma unroll
@@ -728,7 +728,7 @@ __device__ __forceinline__ void dot_rows(const VecArgs& a, const T* w0, const T*
         }
         if (lane == 0) {
             out[c * a.ldo] = rows::from_f32<T>(acc[0][c]);
-            if (two) out[c * a.ldo + 1] = rows::from_f32<T>(acc[1][c]);
+            out[c * a.ldo + 1] = rows::from_f32<T>(acc[1][c]);
         }
     }
 }
@@ -742,11 +742,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 4) experts_vec_kernel(const Ve
     grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int p = blockIdx.y, n = (blockIdx.x * kVecWarps + warp) * 2;
-    if (n >= a.N) return;
+    if (n >= a.N) return;  // N is even: n + 1 is a feature too
     T* out = static_cast<T*>(a.out) + p * a.ldo + n;
-    const bool two = n + 1 < a.N;
     if (p >= a.offsets[a.E]) {
-        if (lane < 2 && (lane == 0 || two)) out[lane] = rows::from_f32<T>(0.f);
+        if (lane < 2) out[lane] = rows::from_f32<T>(0.f);
         return;
     }
     int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
@@ -760,15 +759,15 @@ __global__ void __launch_bounds__(kVecWarps * 32, 4) experts_vec_kernel(const Ve
     const int rows = min(kVecRows, a.offsets[lo + 1] - p);
     const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
     const T* w0 = static_cast<const T*>(a.W) + lo * a.lde + n * a.ldw;
-    const T* w1 = two ? w0 + a.ldw : w0;
+    const T* w1 = w0 + a.ldw;
     if (rows == 1)
-        dot_rows<T, 1>(a, w0, w1, x, out, two, lane);
+        dot_rows<T, 1>(a, w0, w1, x, out, lane);
     else if (rows == 2)
-        dot_rows<T, 2>(a, w0, w1, x, out, two, lane);
+        dot_rows<T, 2>(a, w0, w1, x, out, lane);
     else if (rows == 3)
-        dot_rows<T, 3>(a, w0, w1, x, out, two, lane);
+        dot_rows<T, 3>(a, w0, w1, x, out, lane);
     else
-        dot_rows<T, 4>(a, w0, w1, x, out, two, lane);
+        dot_rows<T, 4>(a, w0, w1, x, out, lane);
 }
 
 // dw of few rows per expert is a write: E N K values from a handful of rows. The

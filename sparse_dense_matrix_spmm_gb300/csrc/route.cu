@@ -429,7 +429,7 @@ constexpr int kDispatchThreads = 512;  // copies (256: 179 us, 512: 177 us, 1638
 constexpr int kBatch = 4;  // rows of a token in flight per thread
 
 struct RowArgs {
-    const int32_t *order, *pos, *offsets;
+    const int32_t *pos, *offsets;
     int64_t T, H, n_keys;
     int32_t k;
     const void *a, *b;  // operands (dispatch: x; combine: ys; gradient: dy, ys)
@@ -667,7 +667,6 @@ spmm_status launch_build_route(const void* ids, int32_t id_bytes, int64_t ldi, c
 
 static RowArgs row_args(const spmm_route_t* R, int64_t H) {
     RowArgs a{};
-    a.order = R->order;
     a.pos = R->pos;
     a.offsets = R->offsets;
     a.T = R->T;

@@ -172,10 +172,6 @@ struct Cols {
             for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load(row + c + u * step) : X::zero();
         }
     }
-    static __device__ __forceinline__ void load_cs(Raw (&r)[U], const T* row, int64_t c, int64_t H, int step) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = c + u * step < H ? X::load_cs(row + c + u * step) : X::zero();
-    }
     static __device__ __forceinline__ void clear(Raw (&r)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) r[u] = X::zero();
