@@ -35,3 +35,12 @@ def test_clusters_with_few_keys(n, n_keys):
     need_gpu()
     _check(_ids(n, 1, n_keys, n + n_keys, 0.1), n_keys)
     _check(_ids(n // 3, 3, n_keys, n - n_keys, 0.02), n_keys)
+
+
+@pytest.mark.parametrize("T,k,n_keys,drop", [(300001, 1, 5000, 0.0), (300001, 1, 200000, 0.1), (150001, 2, 200000, 0.0),
+                                             (300001, 1, 300000, 0.3), (100003, 7, 1000, 0.01)])
+def test_many_elements_over_many_keys(T, k, n_keys, drop):
+    """More than 262144 elements in two or three passes: a CTA takes several tiles, and the counts of the
+    next pass go to the CTA that will read the element there."""
+    need_gpu()
+    _check(_ids(T, k, n_keys, T + n_keys, drop), n_keys)

@@ -45,3 +45,32 @@ def test_table_gradient_of_very_long_rows(H):
         if t != 5:
             want += dy[t]
     assert torch.equal(got[1], want) and torch.equal(got[0], dy[5].float())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("H", [64, 7])
+def test_weights_that_are_not_finite(dtype, H):
+    """An infinite or NaN weight of a dropped choice does not count, of a kept one it reaches its token only."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    ids = np.array([[0, 2, -1], [1, 0, 2], [-1, -1, -1], [2, -1, 0], [1, 2, 0], [0, 1, -1]])
+    T, k = ids.shape
+    R = spmm.spmm_build_route(torch.from_numpy(ids).cuda(), 3)
+    ys = torch.ones((T * k, H), dtype=DT[dtype], device="cuda")
+    dy = torch.ones((T, H), dtype=DT[dtype], device="cuda")
+    w = torch.full((T, k), 0.5, device="cuda")
+    clean = [spmm.spmm_combine(R, ys, w), *spmm.spmm_combine_grad(R, dy, ys, w)]
+    for value in (float("inf"), float("nan")):
+        v = w.clone()
+        v[torch.from_numpy(ids < 0).cuda()] = value
+        for a, b in zip(clean, [spmm.spmm_combine(R, ys, v), *spmm.spmm_combine_grad(R, dy, ys, v)]):
+            assert torch.equal(a, b)
+        v = w.clone()
+        v[4, 1] = value
+        y, (dys, dw) = spmm.spmm_combine(R, ys, v), spmm.spmm_combine_grad(R, dy, ys, v)
+        at = int(R.pos[4, 1])
+        assert not y[4].isfinite().any() and not dys[at].isfinite().any()
+        others = [t for t in range(T) if t != 4]
+        assert torch.equal(y[others], clean[0][others]) and torch.equal(dw, clean[2])
+        rows = [p for p in range(T * k) if p != at]
+        assert torch.equal(dys[rows], clean[1][rows])
