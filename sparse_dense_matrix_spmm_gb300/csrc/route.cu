@@ -32,11 +32,12 @@ using namespace rows;
 //                  digit for the CTA that will read it there
 // The kernels are bound by latency (launches, barriers, chains of dependent
 // loads); measured in a graph with 8 choices per token and 128 keys: 16 tokens
-// 3.5 us, 256 tokens 4.7 us, 1024 tokens 5.6 us (7.4 us as two launches), 16384
-// tokens 12.8 us; 32768 ids over 131072 keys (two passes and the offsets) 22 us.
-// Elements handed on in shared memory against a round trip through L2: 2048 ids
-// over 50000 keys 11.8 us against 13.7 us, 8192 ids 16.3 us against 17.9 us, 2049
-// ids over 300000 keys (three passes) 16.3 us against 21.9 us.
+// 3.6 us, 256 tokens 4.8 us, 1024 tokens 5.5 us (7.4 us as two launches), 16384
+// tokens 11.4 us (11.8 us with loads past L1); 32768 ids over 131072 keys (two
+// passes and the offsets) 21.7 us.  Elements handed on in shared memory against a
+// round trip through L2: 2048 ids over 50000 keys 11.7 us against 13.7 us, 8192
+// ids 15.8 us against 17.9 us, 2049 ids over 300000 keys (three passes) 15.8 us
+// against 21.9 us.
 // One cluster over everything, with ranks from match_any, took 56 us for 16384
 // tokens (8 SMs' issue slots); 16 CTAs per cluster gained nothing over 8.
 constexpr int kDigitBits = 9;
@@ -75,10 +76,10 @@ __device__ __forceinline__ int32_t load_key(const SortArgs& a, int32_t f) {
     return a.n_keys;
 }
 
-// Input of a pass of more than a cluster: the ids, or the result of the pass
-// before (written by other SMs, so read past L1).
+// Input of a pass of more than a cluster: the ids, or the result of the launch
+// before.
 __device__ __forceinline__ int32_t pass_key(const SortArgs& a, int pass, int32_t i) {
-    return pass ? ptx::ld_global_cg(((pass & 1) ? a.keys0 : a.keys1) + i) : load_key(a, i);
+    return pass ? ((pass & 1) ? a.keys0 : a.keys1)[i] : load_key(a, i);
 }
 
 __device__ __forceinline__ int32_t warp_scan(int32_t v, int lane) {  // inclusive
@@ -140,7 +141,7 @@ struct Items {
             const int64_t i = tile + (threadIdx.x >> 5) * (32 * kItems) + j * 32 + (threadIdx.x & 31);
             const int32_t at = static_cast<int32_t>(i);
             key[j] = i < i1 ? pass_key(a, pass, at) : -1;
-            idx[j] = i < i1 && pass ? ptx::ld_global_cg(((pass & 1) ? a.idx0 : a.idx1) + at) : at;
+            idx[j] = i < i1 && pass ? ((pass & 1) ? a.idx0 : a.idx1)[at] : at;
         }
     }
     __device__ __forceinline__ void load(const Exchange& x, int32_t n) {  // n elements of the tile
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const SortArg
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int c = c0 + i + cta < ctas ? c0 + i + cta : c0 + i + cta - ctas;
-                v[i] = c0 + i < ctas ? ptx::ld_global_cg(table + c * bins + threadIdx.x) : 0;
+                v[i] = c0 + i < ctas ? table[c * bins + threadIdx.x] : 0;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kOffsetThreads)
     int64_t lo = 0, hi = n;  // the answer for e0 lies in [lo, hi]
     while (lo < hi) {
         const int64_t step = (hi - lo + kOffsetThreads - 1) / kOffsetThreads, at = lo + threadIdx.x * step;
-        const int64_t below = __syncthreads_count(at < hi && ptx::ld_global_cg(sorted + at) < e0);
+        const int64_t below = __syncthreads_count(at < hi && sorted[at] < e0);
         hi = min(hi, lo + below * step);
         if (below) lo += (below - 1) * step + 1;
     }

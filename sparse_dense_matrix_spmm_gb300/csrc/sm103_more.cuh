@@ -17,17 +17,11 @@ namespace ptx {
 // read what that may have written (any operand) by non-coherent loads: those are
 // for memory that is read-only for the kernel's lifetime, and the compiler may
 // move them over the wait.  It reads by ordinary loads, which the wait's memory
-// clobber keeps behind it, or by ld_global_cg / ld_global_cs below, which are
-// volatile and so stay behind it too.
+// clobber keeps behind it, or by ld_global_cs below, which is volatile and so
+// stays behind it too.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Past L1.
-__device__ __forceinline__ int32_t ld_global_cg(const int32_t* p) {
-    int32_t v;
-    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
-}
 // Data read once: leaves the caches first.
 __device__ __forceinline__ uint16_t ld_global_cs(const uint16_t* p) {
     uint16_t v;
