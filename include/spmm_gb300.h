@@ -32,7 +32,8 @@
  *     asynchronous on `stream`; builders that must report sizes or
  *     data-dependent format errors synchronise `stream` (stated per call).
  *   - Kernels never wait without bound: a pipeline wait that exceeds its limit
- *     (about 2 s) records SPMM_DEVERR_TIMEOUT in a sticky per-device error word
+ *     (about 2 s; the experts' products, whose waits span a whole tile, 2 s and
+ *     10 us per 64 of their depth) records SPMM_DEVERR_TIMEOUT in a sticky per-device error word
  *     and the kernel returns; spmm_last_device_error() reads and clears it.
  *   - Alignment: B, C, format value arrays and 2:4 metadata must be 16-byte
  *     aligned, and ldb must make a row 16-byte aligned (TMA requirement).
@@ -490,9 +491,10 @@ SPMM_API spmm_status spmm_bcsr_permuted(const spmm_bcsr_t *A, const int32_t *per
  * Products with one-hot sparse matrices, the sparse operands of a mixture of
  * experts and of an embedding table.  Rows are bf16, fp16 or fp32 (the experts'
  * products: bf16 or fp16), row-major with a pitch in elements of at least the row
- * length; sums are fp32 and rounded once (to nearest even).  Row pointers need
- * only their element's alignment except where stated; rows whose base, pitch and
- * length are multiples of 16 bytes move in 16-byte pieces.  Every call is
+ * length; sums are fp32 and rounded once (to nearest even).  Results must not
+ * overlap operands.  Row pointers need only their element's alignment except where
+ * stated; rows move in the widest pieces of 16, 8, 4 or 2 bytes that divide the
+ * base, pitch and length of every operand.  Every call is
  * asynchronous on `stream` and gives the same bits on every run.  A shape with
  * nothing to write returns SPMM_OK without launching.  A dimension of 2^31 or
  * more, or T k >= 2^31, -> SPMM_ERR_UNSUPPORTED (row offsets are 64-bit). */
@@ -518,7 +520,8 @@ SPMM_API spmm_status spmm_dispatch(const spmm_route_t *R, const void *x, int64_t
 SPMM_API spmm_status spmm_combine(const spmm_route_t *R, const void *ys, int64_t ldys, const float *w, void *y,
                                   int64_t ldy, int64_t H, int32_t dtype, spmm_stream_t stream);
 /* Gradients of spmm_combine: dys[pos[t][j]] = w[t][j] dy[t] (zero rows past the
- * kept places) and dw[t][j] = <dy[t], ys[pos[t][j]]> (0 for a dropped choice). */
+ * kept places) and dw[t][j] = <dy[t], ys[pos[t][j]]> (0 for a dropped choice, and
+ * for H = 0). */
 SPMM_API spmm_status spmm_combine_grad(const spmm_route_t *R, const void *dy, int64_t lddy, const void *ys,
                                        int64_t ldys, const float *w, void *dys, int64_t lddys, float *dw, int64_t H,
                                        int32_t dtype, spmm_stream_t stream);
@@ -542,9 +545,9 @@ SPMM_API spmm_status spmm_embed_grad(const spmm_route_t *R, const void *dy, int6
 
 /* The experts' products on rows sorted by expert (R->n_keys experts, places
  * offsets[e] .. offsets[e + 1] - 1 belong to expert e).  W[e] is N x K, row pitch
- * ldw, expert pitch lde elements.  bf16 or fp16.  K, N and every pitch multiples
- * of 8 and every pointer 16-byte aligned (TMA), else SPMM_ERR_SHAPE; at most
- * 65535 experts, N and K below 2^30, T k below 2^31 - 512.
+ * ldw, expert pitch lde elements.  bf16 or fp16.  K and N positive, they and every
+ * pitch multiples of 8 and every pointer 16-byte aligned (TMA), else
+ * SPMM_ERR_SHAPE; at most 65535 experts, N and K below 2^30, T k below 2^31 - 512.
  *   spmm_experts     ys[p]  = W[e] xs[p]            ys  T k x N, xs T k x K
  *   spmm_experts_dx  dxs[p] = W[e]^T dys[p]
  *   spmm_experts_dw  dW[e]  = sum_p dys[p] xs[p]^T  (zeros for an unused expert)

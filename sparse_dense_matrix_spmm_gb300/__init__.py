@@ -22,6 +22,11 @@ builders spmm_prune_24 / spmm_prune_tvw.  One-hot operators (tokens by expert or
 by vocabulary row): spmm_build_route, spmm_dispatch, spmm_combine and their
 gradients, spmm_embed and spmm_embed_grad, and the experts' products
 spmm_experts / spmm_experts_dx / spmm_experts_dw between them.
+
+Calls are not recorded by autograd: a result has no history even where an operand
+requires grad.  A backward pass calls the gradient operators itself, by hand
+(examples/moe_layer.py) or in a torch.autograd.Function of the caller's.  Results
+must not overlap operands, and operands live on the current device.
 """
 from __future__ import annotations
 
