@@ -628,6 +628,8 @@ def _route_w(R: Route, w: torch.Tensor, device) -> int:
 
 
 def spmm_build_route_workspace_size(T: int, k: int, n_keys: int) -> int:
+    if k >= 1 << 31:  # the C entry takes 32 bits, of which ctypes would keep the lower ones
+        raise SpmmError("spmm_build_route_workspace_size", 8)
     n = C.c_size_t(0)
     _lib.call("spmm_build_route_workspace_size", T, k, n_keys, C.byref(n))
     return n.value

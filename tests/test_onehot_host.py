@@ -83,3 +83,13 @@ def test_combine_grad_of_rows_without_columns_is_accepted():
     assert L.spmm_combine_grad(R, None, 0, None, 0, None, None, 0, 16, 0, 0, None) == 1   # w
     assert L.spmm_combine_grad(R, None, 0, None, 0, 16, None, 0, None, 0, 0, None) == 1   # dw
     assert L.spmm_combine_grad(R, None, 8, 16, 8, 16, 16, 8, 16, 8, 0, None) == 1         # dy, with columns
+
+
+def test_more_choices_than_32_bits_are_refused():
+    """2^32 + 5 choices of one token must not become 5."""
+    for k in (1 << 31, (1 << 32) + 5):
+        with pytest.raises(spmm.SpmmError, match="UNSUPPORTED"):
+            spmm.spmm_build_route_workspace_size(1, k, 4)
+    ids = SimpleNamespace(is_cuda=True, dtype=torch.int32, shape=(1, (1 << 32) + 5), stride=lambda d: 1)
+    with pytest.raises(spmm.SpmmError, match="UNSUPPORTED"):
+        spmm.spmm_build_route(ids, 4)
