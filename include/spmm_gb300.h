@@ -215,6 +215,29 @@ typedef struct {
     int32_t *keys;    /* [T k] or null */
 } spmm_route_t;
 
+/* Rows held in 8 bits: a checkpoint of activations.  Values c .. c + 15 of a row
+ * (c a multiple of 16; the last group may be short) share a power of two 2^e, the
+ * smallest with e in [-126, 121] for which all of them round to integers of at
+ * most 127 in magnitude; x is held as q 2^e, q = x 2^-e rounded half to even (at e =
+ * 121, next to the largest fp32, cut off at 127).  The error is at most 2^(e - 1), and
+ * q 2^e is exact in bf16 and fp32 (fp16 rounds it where it leaves fp16's range).
+ *   q[rows][ldq]      the integers
+ *   scale[rows][lds]  e + 127 per group; 255: the group held an infinity or a NaN
+ *                     (q = 0) and reads back as NaN
+ * A group of zeros has e = -126 and q = 0. */
+typedef struct {
+    int64_t rows, cols;
+    int8_t *q;
+    int64_t ldq; /* >= cols */
+    uint8_t *scale;
+    int64_t lds; /* >= (cols + 15) / 16 */
+} spmm_rows8_t;
+
+/* Activations of a gated block, silu(x) = x / (1 + e^-x), gelu(x) = x Phi(x) with
+ * the normal distribution function Phi, and its tanh form x (1 + tanh(sqrt(2 / pi)
+ * (x + 0.044715 x^3))) / 2. */
+typedef enum { SPMM_ACT_SILU = 0, SPMM_ACT_GELU = 1, SPMM_ACT_GELU_TANH = 2 } spmm_act;
+
 /* ---------------------------------------------------------------- utilities */
 
 SPMM_API const char *spmm_status_string(spmm_status s);
@@ -241,7 +264,10 @@ SPMM_API spmm_status spmm_selftest_timeout(uint64_t timeout_ns, spmm_stream_t st
 #define SPMM_KERNEL_SDDMM 7   /* sampled dense-dense product                       */
 #define SPMM_KERNEL_ROUTE 8   /* sort of tokens by key (route builder)             */
 #define SPMM_KERNEL_ROWS 9    /* rows moved or summed through a route or by id     */
-#define SPMM_KERNEL_EXPERTS 10 /* the experts' products                            */
+#define SPMM_KERNEL_EXPERTS 10 /* the experts' products, plain and gated           */
+#define SPMM_KERNEL_TOPK 11    /* router: choice of experts and its gradient       */
+#define SPMM_KERNEL_ROWS8 12   /* rows to 8 bits and back                          */
+#define SPMM_KERNEL_GATED_GRAD 13 /* gradient of the gated activation              */
 /* Turns tracing on (clearing earlier records) or off. */
 SPMM_API spmm_status spmm_trace_enable(int32_t on);
 /* Synchronises the traced events and reports launches and total milliseconds
@@ -562,6 +588,66 @@ SPMM_API spmm_status spmm_experts_dx(const spmm_route_t *R, const void *dys, int
 SPMM_API spmm_status spmm_experts_dw(const spmm_route_t *R, const void *dys, int64_t ldy, const void *xs, int64_t ldx,
                                      int64_t N, int64_t K, int32_t dtype, void *dW, int64_t ldw, int64_t lde,
                                      spmm_stream_t stream);
+
+/* ---------------------------------------------------------------- gated experts
+ * What a mixture-of-experts layer needs around the products above: the choice of
+ * experts, the gated feed-forward block, checkpoints in 8 bits.  The conventions of
+ * the one-hot operators hold (pitches in elements, no overlap of results and
+ * operands, asynchronous, the same bits on every run, limits of 2^31). */
+
+/* The router: for each token t the k largest of its E logits (row pitch ldl; bf16,
+ * fp16 or fp32), in descending order, equal ones by ascending index.  ids[T][k]
+ * (id_bytes 4 or 8 each) are their indices, w[T][k] fp32 their weights: with renorm = 1 the softmax
+ * over the chosen logits, with renorm = 0 their entries of the softmax over all E.
+ * A logit of -infinity is never chosen: a token with fewer than k others gets id -1
+ * (a dropped choice of spmm_build_route) and weight 0 in its last places.  NaN ranks
+ * above every number and makes the token's weights NaN, as +infinity does.
+ * 1 <= k <= E (else SPMM_ERR_SHAPE); k <= 32 and E <= 1024, else
+ * SPMM_ERR_UNSUPPORTED. */
+SPMM_API spmm_status spmm_topk(const void *logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
+                               int32_t renorm, void *ids, int32_t id_bytes, float *w, spmm_stream_t stream);
+/* Gradient of spmm_topk's weights for the logits, from its ids and w and the
+ * gradient dw[T][k] (fp32) of w: dlogits[t][e] = sum over j with ids[t][j] = e of
+ * w_j dw_j, less p_e sum_i w_i dw_i, where p_e is the softmax over the chosen (renorm
+ * = 1: the w_j, zero elsewhere, and logits may be null) or over all E.  Every entry is
+ * written; a negative id is a dropped choice, whose w and dw are not read; an id >= E is dropped too and
+ * sets SPMM_DEVERR_INDEX.  dlogits has the logits' type. */
+SPMM_API spmm_status spmm_topk_grad(const void *logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
+                                    int32_t renorm, const void *ids, int32_t id_bytes, const float *w,
+                                    const float *dw, void *dlogits, int64_t ldd, spmm_stream_t stream);
+
+/* Rows to 8 bits (spmm_rows8_t; P's sizes and pitches are inputs, its arrays the
+ * caller's) and back.  x and out are P->rows x P->cols of bf16, fp16 or fp32. */
+SPMM_API spmm_status spmm_pack_rows(const void *x, int64_t ldx, int32_t dtype, const spmm_rows8_t *P,
+                                    spmm_stream_t stream);
+SPMM_API spmm_status spmm_unpack_rows(const spmm_rows8_t *P, void *out, int64_t ldo, int32_t dtype,
+                                      spmm_stream_t stream);
+
+/* The experts' gated feed-forward block on rows sorted by expert: W[e] is 2 N x K,
+ * its first N rows the gate's weights and its last N the up projection's, and for
+ * the rows p of expert e
+ *   [g u] = W[e] xs[p] (fp32 sums),   h[p] = act(g) u,
+ * rounded once.  A training step keeps [g u] for the way back: rounded to the rows'
+ * type in gu (T k x 2 N, row pitch ldgu; null: not kept), or in 8 bits straight
+ * from the sums in *packed (rows = T k, cols = 2 N; null: not kept); not both. Rows
+ * past the kept places are written as zeros (scale 1).  Types, alignment and limits
+ * as for spmm_experts with 2 N features; N % 16 == 0; packed->q 16-byte aligned with ldq %
+ * 16 == 0. */
+SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, int64_t ldx, const void *W,
+                                        int64_t ldw, int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act,
+                                        void *h, int64_t ldh, void *gu, int64_t ldgu, const spmm_rows8_t *packed,
+                                        spmm_stream_t stream);
+/* Gradient of the activation and the product, from the kept [g u] (gu, or packed;
+ * exactly one of them) and the gradient dh of h:
+ *   dgu[p] = [dh u act'(g), dh act(g)]  (T k x 2 N),
+ * and, where h is not null, h[p] = act(g) u again (T k x N), which the gradient of the projection after
+ * it needs.  Rows past the kept places are written as zeros and never read.  bf16 or
+ * fp16; N % 16 == 0, pitches multiples of 8 (packed->ldq of 16) and pointers 16-byte
+ * aligned.  The gradients of the rows and of the weights are spmm_experts_dx and spmm_experts_dw of
+ * dgu with 2 N features. */
+SPMM_API spmm_status spmm_gated_grad(const spmm_route_t *R, const void *dh, int64_t lddh, const void *gu, int64_t ldgu,
+                                     const spmm_rows8_t *packed, int64_t N, int32_t dtype, int32_t act, void *dgu,
+                                     int64_t lddgu, void *h, int64_t ldh, spmm_stream_t stream);
 
 #ifdef __cplusplus
 }

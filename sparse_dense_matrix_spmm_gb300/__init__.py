@@ -14,6 +14,7 @@ Format containers hold device tensors:
   CSR(M, K, nnz, dtype, row_ptr, col, val)
   WCSR(...)  (see include/spmm_gb300.h for the field meanings)
   Route(T, k, n_keys, order, pos, offsets)   (one-hot rows sorted by key)
+  Rows8(rows, cols, dtype, q, scale)   (rows held in 8 bits)
 
 Beyond C = A B for those formats: spmm_slide ((2n-2):2n as overlapping 2:4
 windows), spmm_bcsr_permuted (BCSR after a Reverse Cuthill-McKee order from
@@ -21,7 +22,11 @@ rcm_order), spmm_sddmm (A B sampled at a CSR pattern) and the pruning
 builders spmm_prune_24 / spmm_prune_tvw.  One-hot operators (tokens by expert or
 by vocabulary row): spmm_build_route, spmm_dispatch, spmm_combine and their
 gradients, spmm_embed and spmm_embed_grad, and the experts' products
-spmm_experts / spmm_experts_dx / spmm_experts_dw between them.
+spmm_experts / spmm_experts_dx / spmm_experts_dw between them.  Around those, for
+a gated mixture of experts: the router spmm_topk, the gated feed-forward block
+spmm_experts_gated, activation checkpoints in 8 bits (spmm_pack_rows,
+spmm_unpack_rows, save="packed"), and the gradients spmm_topk_grad,
+spmm_gated_grad and spmm_experts_gated_grad.
 
 Calls are not recorded by autograd: a result has no history even where an operand
 requires grad.  A backward pass calls the gradient operators itself, by hand
@@ -48,6 +53,8 @@ __all__ = ["BCSR", "Mat24", "Slide", "TVW", "CSR", "WCSR", "SpmmError", "spmm_bc
            "Route", "spmm_build_route", "spmm_build_route_workspace_size", "spmm_dispatch", "spmm_dispatch_grad",
            "spmm_combine", "spmm_combine_grad", "spmm_embed", "spmm_embed_grad", "spmm_embed_grad_workspace_size",
            "spmm_experts", "spmm_experts_dx", "spmm_experts_dw", "spmm_experts_grad",
+           "Rows8", "spmm_topk", "spmm_topk_grad", "spmm_pack_rows", "spmm_unpack_rows",
+           "spmm_experts_gated", "spmm_gated_grad", "spmm_experts_gated_grad",
            "last_device_error", "selftest_timeout", "library_path", "trace_enable", "trace_read"]
 
 _DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.int8: _lib.SPMM_I8,
@@ -813,3 +820,184 @@ def spmm_experts_dw(R: Route, dys: torch.Tensor, xs: torch.Tensor, out: Optional
 def spmm_experts_grad(R: Route, dys: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, stream=None):
     """Both gradients of spmm_experts: (dxs, dW)."""
     return spmm_experts_dx(R, dys, W, stream=stream), spmm_experts_dw(R, dys, xs, stream=stream)
+
+
+# ------------------------------------------------------------------ gated experts
+_ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH}
+
+
+@dataclass
+class Rows8:
+    """rows x cols values of dtype held in 8 bits: 16 consecutive values of a row share
+    a power of two, value = q 2^(scale - 127) (scale 255: NaN).  q is int8, rows x
+    cols, scale uint8, rows x ceil(cols / 16); both may be views of wider rows."""
+    rows: int
+    cols: int
+    dtype: torch.dtype
+    q: torch.Tensor
+    scale: torch.Tensor
+
+    def c(self) -> _lib.Rows8T:
+        groups = -(-self.cols // 16)
+        for t, what, dt, n in ((self.q, "q", torch.int8, self.cols), (self.scale, "scale", torch.uint8, groups)):
+            if not t.is_cuda or t.device != self.q.device:
+                raise ValueError("q and scale must be on one CUDA device (this library has no CPU path)")
+            if t.dtype is not dt or t.shape != (self.rows, n):
+                raise ValueError(f"{what} must be {self.rows} x {n} of {dt}")
+            if n > 1 and self.rows > 0 and t.stride(1) != 1:
+                raise ValueError(f"{what} must have contiguous rows")
+        wide = self.rows > 1
+        return _lib.Rows8T(self.rows, self.cols, self.q.data_ptr(), self.q.stride(0) if wide else -(-self.cols // 16) * 16,
+                           self.scale.data_ptr(), self.scale.stride(0) if wide else groups)
+
+
+def _rows8(like: torch.Tensor, rows: int, cols: int, dtype, stream) -> Rows8:
+    """Unwritten 8-bit rows; the pitch of q is a multiple of 16, so that every row moves in wide pieces."""
+    q = _empty(like, (rows, -(-cols // 16) * 16), torch.int8, stream)[:, :cols]
+    return Rows8(rows, cols, dtype, q, _empty(like, (rows, -(-cols // 16)), torch.uint8, stream))
+
+
+def _act(act: str) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, not {act!r}")
+    return code
+
+
+def spmm_topk(logits: torch.Tensor, k: int, renorm: bool = True, id_dtype=torch.int64, stream=None):
+    """The router: (ids, w) of each token's k largest logits (T x E; bf16, fp16 or
+    fp32), largest first, equal ones by ascending index.  w (fp32) is the softmax over
+    the chosen logits, or with renorm=False their entries of the softmax over all E.
+    -inf is never chosen: id -1 (dropped by spmm_build_route) and weight 0 take its
+    place.  NaN ranks first and makes the token's weights NaN.  k <= 32, E <= 1024."""
+    _check_dev(logits)
+    T, E = logits.shape
+    dev = logits.device
+    code, ldl = _row_code(logits.dtype), _rows(logits, "logits", T, E, logits.dtype, dev)
+    id_bytes = _ID_BYTES.get(id_dtype)
+    if id_bytes is None:
+        raise TypeError(f"ids must be int32 or int64, not {id_dtype}")
+    if not 0 < k <= E:
+        raise ValueError(f"k must be between 1 and {E}, not {k}")
+    ids, w = _empty(logits, (T, k), id_dtype, stream), _empty(logits, (T, k), torch.float32, stream)
+    _lib.call("spmm_topk", logits.data_ptr(), T, E, ldl, code, k, 1 if renorm else 0, ids.data_ptr(), id_bytes, w.data_ptr(),
+              _handle(stream, dev))
+    return ids, w
+
+
+def spmm_topk_grad(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, dw: torch.Tensor, renorm: bool = True,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of spmm_topk's weights for the logits (T x E of their type; every entry
+    written), from its ids and w and the gradient dw of w.  A negative id is a dropped
+    choice; an id >= E as well and sets SPMM_DEVERR_INDEX."""
+    _check_dev(logits)
+    T, E = logits.shape
+    dev = logits.device
+    code, ldl = _row_code(logits.dtype), _rows(logits, "logits", T, E, logits.dtype, dev)
+    id_bytes = _ID_BYTES.get(ids.dtype)
+    if id_bytes is None:
+        raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
+    if ids.dim() != 2 or ids.shape[0] != T or ids.device != dev or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous {T} x k tensor on {dev}")
+    for t, what in ((w, "w"), (dw, "dw")):
+        if t.device != dev or t.dtype is not torch.float32:
+            raise TypeError(f"{what} must be float32 on {dev}")
+        if t.shape != ids.shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous tensor of the ids' shape {tuple(ids.shape)}")
+    k = ids.shape[1]
+    if not 0 < k <= E:
+        raise ValueError(f"k must be between 1 and {E}, not {k}")
+    if out is None:
+        out, ldo = _empty(logits, (T, E), logits.dtype, stream), E
+    else:
+        ldo = _rows(out, "out", T, E, logits.dtype, dev)
+    _lib.call("spmm_topk_grad", logits.data_ptr(), T, E, ldl, code, k, 1 if renorm else 0, ids.data_ptr(), id_bytes,
+              w.data_ptr(), dw.data_ptr(), out.data_ptr(), ldo, _handle(stream, dev))
+    return out
+
+
+def spmm_pack_rows(x: torch.Tensor, out: Optional[Rows8] = None, stream=None) -> Rows8:
+    """A checkpoint of rows x (bf16, fp16 or fp32) in 8 bits: Rows8, 17/16 bytes a value.
+    A value is off by at most half a unit of its group, 1/255 to 1/127.5 of the
+    group's largest magnitude."""
+    _check_dev(x)
+    rows, cols = x.shape
+    code, ldx = _row_code(x.dtype), _rows(x, "x", rows, cols, x.dtype, x.device)
+    if out is None:
+        out = _rows8(x, rows, cols, x.dtype, stream)
+    elif (out.rows, out.cols, out.dtype, out.q.device) != (rows, cols, x.dtype, x.device):
+        raise ValueError(f"out must hold {rows} x {cols} values of {x.dtype} on {x.device}")
+    _lib.call("spmm_pack_rows", x.data_ptr(), ldx, code, C.byref(out.c()), _handle(stream, x.device))
+    return out
+
+
+def spmm_unpack_rows(P: Rows8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The rows that P holds, of P.dtype (or of out's type)."""
+    dev = P.q.device
+    p = P.c()
+    if out is None:
+        out, ldo = _empty(P.q, (P.rows, P.cols), P.dtype, stream), P.cols
+    else:
+        ldo = _rows(out, "out", P.rows, P.cols, out.dtype, dev)
+    _lib.call("spmm_unpack_rows", C.byref(p), out.data_ptr(), ldo, _row_code(out.dtype), _handle(stream, dev))
+    return out
+
+
+def spmm_experts_gated(R: Route, xs: torch.Tensor, W: torch.Tensor, act: str = "silu", save: Optional[str] = None,
+                       out: Optional[torch.Tensor] = None, stream=None):
+    """h[p] = act(g) u with [g u] = W[e] xs[p] for the rows p of expert e: W is E x 2N x
+    K, the gate's N rows before the up projection's; act is silu, gelu or gelu_tanh;
+    zero rows past the kept places.  bf16 or fp16, N a multiple of 16.  A training step
+    keeps [g u] (T k x 2N) for spmm_experts_gated_grad: save="rows" returns (h, gu) with gu of xs's
+    type, save="packed" (h, Rows8) with gu in 8 bits."""
+    dev, dt, rows = R.device, xs.dtype, R.n_rows
+    N, K = W.shape[-2] // 2, W.shape[-1]
+    code, ldx, actc = _row_code(dt), _rows(xs, "xs", rows, K, dt, dev), _act(act)
+    ldw, lde = _weights(W, "W", R.n_keys, 2 * N, K, dt, dev)
+    if save not in (None, "rows", "packed"):
+        raise ValueError(f"save must be None, 'rows' or 'packed', not {save!r}")
+    if out is None:
+        out, ldo = _empty(xs, (rows, N), dt, stream), N
+    else:
+        ldo = _rows(out, "out", rows, N, dt, dev)
+    gu = _empty(xs, (rows, 2 * N), dt, stream) if save == "rows" else None
+    packed = _rows8(xs, rows, 2 * N, dt, stream) if save == "packed" else None
+    _lib.call("spmm_experts_gated", R._ref, xs.data_ptr(), ldx, W.data_ptr(), ldw, lde, N, K, code, actc, out.data_ptr(), ldo,
+              None if gu is None else gu.data_ptr(), 2 * N, None if packed is None else C.byref(packed.c()),
+              _handle(stream, dev))
+    return out if save is None else (out, gu if packed is None else packed)
+
+
+def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: bool = False,
+                    out: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of h = act(g) u for [g u], from the kept gu (rows or Rows8) and the
+    gradient dh: dgu (T k x 2N), zero rows past the kept places.  with_h returns (dgu, h):
+    h again, which the gradient of the projection after it needs."""
+    dev, dt, rows = R.device, dh.dtype, R.n_rows
+    N = dh.shape[-1]
+    code, ldd, actc = _row_code(dt), _rows(dh, "dh", rows, N, dt, dev), _act(act)
+    if isinstance(gu, Rows8):
+        if (gu.rows, gu.cols, gu.q.device) != (rows, 2 * N, dev):
+            raise ValueError(f"gu must hold {rows} x {2 * N} values on {dev}")
+        gu_ptr, ldgu, packed = None, 2 * N, C.byref(gu.c())
+    else:
+        ldgu = _rows(gu, "gu", rows, 2 * N, dt, dev)
+        gu_ptr, packed = gu.data_ptr(), None
+    if out is None:
+        out, ldo = _empty(dh, (rows, 2 * N), dt, stream), 2 * N
+    else:
+        ldo = _rows(out, "out", rows, 2 * N, dt, dev)
+    h = _empty(dh, (rows, N), dt, stream) if with_h else None
+    _lib.call("spmm_gated_grad", R._ref, dh.data_ptr(), ldd, gu_ptr, ldgu, packed, N, code, actc, out.data_ptr(), ldo,
+              None if h is None else h.data_ptr(), N, _handle(stream, dev))
+    return (out, h) if with_h else out
+
+
+def spmm_experts_gated_grad(R: Route, dh: torch.Tensor, xs, W: torch.Tensor, gu, act: str = "silu", stream=None):
+    """The gradients (dgu, dxs, dW) of spmm_experts_gated from the gradient dh of h: xs
+    (rows or their Rows8 checkpoint) and W as in the forward call, gu what it saved."""
+    dgu = spmm_gated_grad(R, dh, gu, act, stream=stream)
+    dxs = spmm_experts_dx(R, dgu, W, stream=stream)
+    if isinstance(xs, Rows8):
+        xs = spmm_unpack_rows(xs, _empty(dh, (xs.rows, xs.cols), dh.dtype, stream), stream=stream)
+    return dgu, dxs, spmm_experts_dw(R, dgu, xs, stream=stream)

@@ -11,6 +11,8 @@ SPMM_BF16, SPMM_F16, SPMM_I8, SPMM_E4M3, SPMM_E5M2, SPMM_F32 = 0, 1, 2, 3, 4, 5
 DEVERR_TIMEOUT, DEVERR_INDEX, DEVERR_FORMAT = 1, 2, 4
 KERNEL_BCSR, KERNEL_SPARSE, KERNEL_WIDEN, KERNEL_WCSR, KERNEL_PRUNE, KERNEL_PERMUTE, KERNEL_SDDMM = 1, 2, 3, 4, 5, 6, 7
 KERNEL_ROUTE, KERNEL_ROWS, KERNEL_EXPERTS = 8, 9, 10
+KERNEL_TOPK, KERNEL_ROWS8, KERNEL_GATED_GRAD = 11, 12, 13
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
 STATUS = {0: "SPMM_OK", 1: "SPMM_ERR_NULL", 2: "SPMM_ERR_SHAPE", 3: "SPMM_ERR_DTYPE", 4: "SPMM_ERR_FORMAT",
           5: "SPMM_ERR_WORKSPACE", 6: "SPMM_ERR_TIMEOUT", 7: "SPMM_ERR_CUDA", 8: "SPMM_ERR_UNSUPPORTED"}
 
@@ -55,6 +57,10 @@ class TvwT(C.Structure):
 
 class RouteT(C.Structure):
     _fields_ = [("T", I64), ("k", I32), ("n_keys", I64), ("order", P), ("pos", P), ("offsets", P), ("keys", P)]
+
+
+class Rows8T(C.Structure):
+    _fields_ = [("rows", I64), ("cols", I64), ("q", P), ("ldq", I64), ("scale", P), ("lds", I64)]
 
 
 # name -> (restype, argtypes); every function declared in include/spmm_gb300.h
@@ -102,6 +108,13 @@ SIGNATURES = {
     "spmm_experts": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, P, I64, P]),
     "spmm_experts_dx": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, P, I64, P]),
     "spmm_experts_dw": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I32, P, I64, I64, P]),
+    "spmm_topk": (I32, [P, I64, I64, I64, I32, I32, I32, P, I32, P, P]),
+    "spmm_topk_grad": (I32, [P, I64, I64, I64, I32, I32, I32, P, I32, P, P, P, I64, P]),
+    "spmm_pack_rows": (I32, [P, I64, I32, C.POINTER(Rows8T), P]),
+    "spmm_unpack_rows": (I32, [C.POINTER(Rows8T), P, I64, I32, P]),
+    "spmm_experts_gated": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, I32, P, I64, P, I64,
+                                 C.POINTER(Rows8T), P]),
+    "spmm_gated_grad": (I32, [C.POINTER(RouteT), P, I64, P, I64, C.POINTER(Rows8T), I64, I32, I32, P, I64, P, I64, P]),
 }
 
 _lib = None

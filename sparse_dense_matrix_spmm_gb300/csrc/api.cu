@@ -787,4 +787,127 @@ spmm_status spmm_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldy,
     return launch_experts_dw(R, dys, ldy, xs, ldx, N, K, dtype, dW, ldw, lde, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------- gated experts
+
+namespace {
+spmm_status check_rows8(const spmm_rows8_t* P) {
+    if (!P) return SPMM_ERR_NULL;
+    if (P->rows < 0 || P->cols < 0 || bad_pitch(P->ldq, P->cols)) return SPMM_ERR_SHAPE;
+    if (P->rows >= kDimLimit || P->cols >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (bad_pitch(P->lds, (P->cols + 15) / 16)) return SPMM_ERR_SHAPE;
+    return SPMM_OK;
+}
+
+// The 8-bit form of [g u] for the rows of a route.
+spmm_status check_packed(const spmm_rows8_t* P, const spmm_route_t* R, int64_t N) {
+    const spmm_status st = check_rows8(P);
+    if (st != SPMM_OK) return st;
+    if (P->rows != R->T * R->k || P->cols != 2 * N || P->ldq % 16 || !aligned16(P->q)) return SPMM_ERR_SHAPE;
+    if (P->rows > 0 && (!P->q || !P->scale)) return SPMM_ERR_NULL;
+    return SPMM_OK;
+}
+
+bool bad_act(int32_t act) { return act != SPMM_ACT_SILU && act != SPMM_ACT_GELU && act != SPMM_ACT_GELU_TANH; }
+
+spmm_status check_topk(int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k, int32_t renorm, const void* ids,
+                       int32_t id_bytes) {
+    if (!dtype_row(dtype) || (id_bytes != 4 && id_bytes != 8)) return SPMM_ERR_DTYPE;
+    if (T < 0 || E <= 0 || k <= 0 || k > E || (renorm & ~1) || bad_pitch(ldl, E)) return SPMM_ERR_SHAPE;
+    if (T >= kDimLimit || E > 1024 || k > 32 || T * k >= kDimLimit) return SPMM_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(ids) % static_cast<unsigned>(id_bytes)) return SPMM_ERR_SHAPE;
+    return SPMM_OK;
+}
+}  // namespace
+
+spmm_status spmm_topk(const void* logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k, int32_t renorm,
+                      void* ids, int32_t id_bytes, float* w, spmm_stream_t stream) {
+    const spmm_status st = check_topk(T, E, ldl, dtype, k, renorm, ids, id_bytes);
+    if (st != SPMM_OK) return st;
+    if (T == 0) return SPMM_OK;
+    if (!logits || !ids || !w) return SPMM_ERR_NULL;
+    if (misaligned(logits, dtype) || misaligned(w, SPMM_F32)) return SPMM_ERR_SHAPE;
+    return launch_topk(logits, T, E, ldl, dtype, k, renorm, ids, id_bytes, w, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_topk_grad(const void* logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
+                           int32_t renorm, const void* ids, int32_t id_bytes, const float* w, const float* dw,
+                           void* dlogits, int64_t ldd, spmm_stream_t stream) {
+    const spmm_status st = check_topk(T, E, renorm ? E : ldl, dtype, k, renorm, ids, id_bytes);
+    if (st != SPMM_OK) return st;
+    if (bad_pitch(ldd, E)) return SPMM_ERR_SHAPE;
+    if (T == 0) return SPMM_OK;
+    if ((!logits && !renorm) || !ids || !w || !dw || !dlogits) return SPMM_ERR_NULL;
+    if ((!renorm && misaligned(logits, dtype)) || misaligned(w, SPMM_F32) || misaligned(dw, SPMM_F32) ||
+        misaligned(dlogits, dtype))
+        return SPMM_ERR_SHAPE;
+    return launch_topk_grad(logits, T, E, ldl, dtype, k, renorm, ids, id_bytes, w, dw, dlogits, ldd,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_pack_rows(const void* x, int64_t ldx, int32_t dtype, const spmm_rows8_t* P, spmm_stream_t stream) {
+    const spmm_status st = check_rows8(P);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
+    if (bad_pitch(ldx, P->cols)) return SPMM_ERR_SHAPE;
+    if (P->rows == 0 || P->cols == 0) return SPMM_OK;
+    if (!x || !P->q || !P->scale) return SPMM_ERR_NULL;
+    if (misaligned(x, dtype)) return SPMM_ERR_SHAPE;
+    return launch_pack_rows(x, ldx, dtype, P, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_unpack_rows(const spmm_rows8_t* P, void* out, int64_t ldo, int32_t dtype, spmm_stream_t stream) {
+    const spmm_status st = check_rows8(P);
+    if (st != SPMM_OK) return st;
+    if (!dtype_row(dtype)) return SPMM_ERR_DTYPE;
+    if (bad_pitch(ldo, P->cols)) return SPMM_ERR_SHAPE;
+    if (P->rows == 0 || P->cols == 0) return SPMM_OK;
+    if (!out || !P->q || !P->scale) return SPMM_ERR_NULL;
+    if (misaligned(out, dtype)) return SPMM_ERR_SHAPE;
+    return launch_unpack_rows(P, out, ldo, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_experts_gated(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
+                               int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, void* h, int64_t ldh,
+                               void* gu, int64_t ldgu, const spmm_rows8_t* packed, spmm_stream_t stream) {
+    if (N <= 0 || N % 16) return SPMM_ERR_SHAPE;
+    if (N >= kDimLimit / 4) return SPMM_ERR_UNSUPPORTED;
+    spmm_status st = check_experts(R, ldx, K, ldh, N, ldw, lde, 2 * N, K, dtype);
+    if (st != SPMM_OK) return st;
+    if (bad_act(act)) return SPMM_ERR_UNSUPPORTED;
+    if (gu && packed) return SPMM_ERR_UNSUPPORTED;
+    if (gu && (bad_pitch(ldgu, 2 * N) || ldgu % 8)) return SPMM_ERR_SHAPE;
+    if (packed && (st = check_packed(packed, R, N)) != SPMM_OK) return st;
+    if (R->T == 0) return SPMM_OK;
+    if (!R->offsets || !xs || !W || !h) return SPMM_ERR_NULL;
+    if (!aligned16(xs) || !aligned16(W) || !aligned16(h) || !aligned16(gu)) return SPMM_ERR_SHAPE;
+    GatedOut out{h, ldh, gu, ldgu, nullptr, 0, nullptr, 0};
+    if (packed) {
+        out.q = packed->q;
+        out.ldq = packed->ldq;
+        out.scale = packed->scale;
+        out.lds = packed->lds;
+    }
+    return launch_experts_gated_vec(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                            const spmm_rows8_t* packed, int64_t N, int32_t dtype, int32_t act, void* dgu,
+                            int64_t lddgu, void* h, int64_t ldh, spmm_stream_t stream) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (dtype != SPMM_BF16 && dtype != SPMM_F16) return SPMM_ERR_DTYPE;
+    if (N <= 0 || N % 16) return SPMM_ERR_SHAPE;
+    if (N >= kDimLimit / 4 || bad_act(act)) return SPMM_ERR_UNSUPPORTED;
+    if (bad_pitch(lddh, N) || bad_pitch(lddgu, 2 * N) || lddh % 8 || lddgu % 8) return SPMM_ERR_SHAPE;
+    if (h && (bad_pitch(ldh, N) || ldh % 8)) return SPMM_ERR_SHAPE;
+    if (gu && (bad_pitch(ldgu, 2 * N) || ldgu % 8)) return SPMM_ERR_SHAPE;
+    if (packed && (st = check_packed(packed, R, N)) != SPMM_OK) return st;
+    if (R->T == 0) return SPMM_OK;
+    if (!R->offsets || !dh || !dgu || (!gu && !packed)) return SPMM_ERR_NULL;
+    if (gu && packed) return SPMM_ERR_UNSUPPORTED;
+    if (!aligned16(dh) || !aligned16(gu) || !aligned16(dgu) || !aligned16(h)) return SPMM_ERR_SHAPE;
+    return launch_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, h, ldh,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

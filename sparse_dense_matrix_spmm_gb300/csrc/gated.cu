@@ -1,0 +1,280 @@
+// gated.cu -- the experts' gated block on CUDA cores (a token or two), and the
+// gradient of its activation.
+//   forward   [g u] = W[e] xs[p],  h[p] = act(g) u
+//   gradient  dgu[p] = [dh u act'(g), dh act(g)]
+#include "gated.cuh"
+#include "internal.h"
+#include "rowvec.cuh"
+
+namespace spmm {
+namespace {
+
+using namespace rows;
+using namespace gated;
+
+// ---------------------------------------------------------------- forward, very few rows
+// Dot products on CUDA cores: a warp takes one feature, its gate row and its up
+// row, with up to four rows of an expert; 16 warps a group of 16 features.
+constexpr int kVecWarps = 16, kVecRows = 4;
+
+struct VecArgs {
+    const int32_t* offsets;
+    int32_t E, R;
+    const void *xs, *W;
+    int64_t ldx, ldw, lde;
+    int32_t N, K;
+    GatedOut out;
+};
+
+template <typename T, int C>
+__device__ __forceinline__ void dot_rows(const VecArgs& a, const T* wg, const T* wu, const T* x, int lane,
+                                         float (*sums)[kVecRows][kVecWarps], int warp) {
+    using V = Vec<T, 8>;
+    float acc[2][C] = {};
+    constexpr int kFlight = 2;  // loads per weight row before their sums
+    for (int k0 = lane * 8; k0 < a.K; k0 += 256 * kFlight) {
+        uint4 r[2][kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int k = k0 + 256 * i;
+            r[0][i] = k < a.K ? ptx::ld_global_cs(reinterpret_cast<const uint4*>(wg + k)) : V::zero();
+            r[1][i] = k < a.K ? ptx::ld_global_cs(reinterpret_cast<const uint4*>(wu + k)) : V::zero();
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int k = k0 + 256 * i;
+            if (k >= a.K) break;
+            float f0[8], f1[8];
+            V::unpack(r[0][i], f0);
+            V::unpack(r[1][i], f1);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float v[8];
+                V::unpack(V::load(x + c * a.ldx + k), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[0][c] = fmaf(f0[j], v[j], acc[0][c]);
+                    acc[1][c] = fmaf(f1[j], v[j], acc[1][c]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int s = 16; s; s >>= 1) {
+            acc[0][c] += __shfl_xor_sync(0xffffffffu, acc[0][c], s);
+            acc[1][c] += __shfl_xor_sync(0xffffffffu, acc[1][c], s);
+        }
+        if (lane == 0) {
+            sums[0][c][warp] = acc[0][c];
+            sums[1][c][warp] = acc[1][c];
+        }
+    }
+}
+
+// Grid (16 features, sorted place): the CTAs of an expert's first place and of
+// every fourth after it take up to four of its rows, the others leave; places of
+// dropped choices are zeroed.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kVecWarps * 32, 2) gated_vec_kernel(const VecArgs a) {
+    __shared__ float sums[2][kVecRows][kVecWarps];  // gate and up
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n0 = blockIdx.x * kVecWarps;
+    for (int p = blockIdx.y; p < a.R; p += gridDim.y) {
+        int rows = 1;
+        const bool live = p < a.offsets[a.E];
+        if (live) {
+            int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, at = lo + step * lane;
+                const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= p);
+                lo += step * (31 - __clz(le));
+                hi = min(hi, lo + step);
+            }
+            if ((p - a.offsets[lo]) % kVecRows) continue;
+            rows = min(kVecRows, a.offsets[lo + 1] - p);
+            const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
+            const T* wg = static_cast<const T*>(a.W) + lo * a.lde + (n0 + warp) * a.ldw;
+            const T* wu = wg + a.N * a.ldw;
+            if (rows == 1)
+                dot_rows<T, 1>(a, wg, wu, x, lane, sums, warp);
+            else if (rows == 2)
+                dot_rows<T, 2>(a, wg, wu, x, lane, sums, warp);
+            else if (rows == 3)
+                dot_rows<T, 3>(a, wg, wu, x, lane, sums, warp);
+            else
+                dot_rows<T, 4>(a, wg, wu, x, lane, sums, warp);
+        }
+        __syncthreads();
+        if (threadIdx.x < 2 * kVecRows * 16) {  // whole warps: half, row, feature
+            const int f = threadIdx.x & 15, c = threadIdx.x >> 4 & 3, half = threadIdx.x >> 6;
+            const bool in = c < rows;
+            const float v = live && in ? sums[half][c][f] : 0.f;
+            const int64_t row = p + c;
+            const int n = n0 + f;
+            if (half == 0 && in)
+                static_cast<T*>(a.out.h)[row * a.out.ldh + n] = from_f32<T>(live ? act<ACT>(v) * sums[1][c][f] : 0.f);
+            if (a.out.gu && in) static_cast<T*>(a.out.gu)[row * a.out.ldgu + half * a.N + n] = from_f32<T>(v);
+            if (a.out.q) {
+                uint32_t code = magnitude_code(v);
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, d));
+                const uint32_t b = scale_byte(code);
+                const int64_t col = static_cast<int64_t>(half) * a.N + n;
+                if (in) {
+                    a.out.q[row * a.out.ldq + col] = static_cast<int8_t>(quantise(v, b));
+                    if (f == 0) a.out.scale[row * a.out.lds + col / kGroup] = static_cast<uint8_t>(b);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- gradient of the activation
+// Bound by HBM: a thread takes 8 features of a place, reads dh, g and u and writes
+// both gradients (and h).
+constexpr int kGradThreads = 256;
+
+struct GradArgs {
+    const int32_t* offsets;
+    int32_t E;
+    int64_t R;
+    int32_t N;
+    const void* dh;
+    int64_t lddh;
+    const void* gu;
+    int64_t ldgu;
+    const int8_t* q;
+    int64_t ldq;
+    const uint8_t* scale;
+    int64_t lds;
+    void* dgu;
+    int64_t lddgu;
+    void* h;
+    int64_t ldh;
+    int32_t tx;  // threads along a row
+};
+
+// Eight kept values in 8 bits (half a group).
+__device__ __forceinline__ void load8(const int8_t* q, uint32_t byte, float (&f)[8]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q);
+    const float unit = unit_of(byte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(byte_of(i < 4 ? w.x : w.y, i & 3)) * unit;
+}
+
+template <typename T, int ACT, bool PACKED>
+__global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GradArgs a) {
+    using V = Vec<T, 8>;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int x = threadIdx.x % a.tx;
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * (kGradThreads / a.tx) + threadIdx.x / a.tx;
+    if (p >= a.R) return;
+    const bool live = p < a.offsets[a.E];
+    T* dg = static_cast<T*>(a.dgu) + p * a.lddgu;
+    T* du = dg + a.N;
+    T* h = a.h ? static_cast<T*>(a.h) + p * a.ldh : nullptr;
+    for (int c = x * 8; c < a.N; c += a.tx * 8) {
+        float d[8] = {}, f[8] = {}, y[8] = {};
+        if (live) {
+            float g[8], u[8];
+            const typename V::Raw rd = V::load(static_cast<const T*>(a.dh) + p * a.lddh + c);
+            if (PACKED) {
+                const int8_t* q = a.q + p * a.ldq + c;
+                const uint8_t* s = a.scale + p * a.lds + c / kGroup;
+                load8(q, s[0], g);
+                load8(q + a.N, s[a.N / kGroup], u);
+            } else {
+                const T* r = static_cast<const T*>(a.gu) + p * a.ldgu + c;
+                const typename V::Raw rg = V::load(r), ru = V::load(r + a.N);
+                V::unpack(rg, g);
+                V::unpack(ru, u);
+            }
+            V::unpack(rd, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v, dv;
+                act_grad<ACT>(g[i], v, dv);
+                f[i] = d[i] * v;
+                d[i] *= u[i] * dv;
+                y[i] = v * u[i];
+            }
+        }
+        V::store(dg + c, V::pack(d));
+        V::store(du + c, V::pack(f));
+        if (h) V::store(h + c, V::pack(y));
+    }
+}
+
+template <typename T, bool PACKED>
+cudaError_t launch_grad(const GradArgs& a, int32_t act, cudaStream_t s) {
+    const int64_t per = kGradThreads / a.tx;
+    const dim3 grid(static_cast<unsigned>((a.R + per - 1) / per));
+    return launch_rows(act == SPMM_ACT_SILU   ? gated_grad_kernel<T, SPMM_ACT_SILU, PACKED>
+                       : act == SPMM_ACT_GELU ? gated_grad_kernel<T, SPMM_ACT_GELU, PACKED>
+                                              : gated_grad_kernel<T, SPMM_ACT_GELU_TANH, PACKED>,
+                       grid, kGradThreads, s, a);
+}
+
+template <typename T>
+cudaError_t launch_vec(const VecArgs& a, int32_t act, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(a.N / kVecWarps), static_cast<unsigned>(a.R < 65535 ? a.R : 65535));
+    return launch_rows(act == SPMM_ACT_SILU   ? gated_vec_kernel<T, SPMM_ACT_SILU>
+                       : act == SPMM_ACT_GELU ? gated_vec_kernel<T, SPMM_ACT_GELU>
+                                              : gated_vec_kernel<T, SPMM_ACT_GELU_TANH>,
+                       grid, kVecWarps * 32, s, a);
+}
+
+}  // namespace
+
+spmm_status launch_experts_gated_vec(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
+                                     int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
+                                     cudaStream_t s) {
+    const VecArgs a{R->offsets, static_cast<int32_t>(R->n_keys), static_cast<int32_t>(R->T * R->k), xs, W, ldx, ldw, lde,
+                    static_cast<int32_t>(N), static_cast<int32_t>(K), out};
+    trace_begin(SPMM_KERNEL_EXPERTS, s);
+    const cudaError_t e = dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16>(a, act, s) : launch_vec<__half>(a, act, s);
+    trace_end(SPMM_KERNEL_EXPERTS, s);
+    return cuda_status(e);
+}
+
+spmm_status launch_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                              const spmm_rows8_t* packed, int64_t N, int32_t dtype, int32_t act, void* dgu,
+                              int64_t lddgu, void* h, int64_t ldh, cudaStream_t s) {
+    GradArgs a{};
+    a.offsets = R->offsets;
+    a.E = static_cast<int32_t>(R->n_keys);
+    a.R = R->T * R->k;
+    a.N = static_cast<int32_t>(N);
+    a.dh = dh;
+    a.lddh = lddh;
+    a.gu = gu;
+    a.ldgu = ldgu;
+    if (packed) {
+        a.q = packed->q;
+        a.ldq = packed->ldq;
+        a.scale = packed->scale;
+        a.lds = packed->lds;
+    }
+    a.dgu = dgu;
+    a.lddgu = lddgu;
+    a.h = h;
+    a.ldh = ldh;
+    a.tx = 2;
+    while (a.tx < kGradThreads && a.tx * 8 < N) a.tx *= 2;
+    cudaError_t e;
+    trace_begin(SPMM_KERNEL_GATED_GRAD, s);
+    if (dtype == SPMM_BF16)
+        e = packed ? launch_grad<__nv_bfloat16, true>(a, act, s) : launch_grad<__nv_bfloat16, false>(a, act, s);
+    else
+        e = packed ? launch_grad<__half, true>(a, act, s) : launch_grad<__half, false>(a, act, s);
+    trace_end(SPMM_KERNEL_GATED_GRAD, s);
+    return cuda_status(e);
+}
+
+}  // namespace spmm

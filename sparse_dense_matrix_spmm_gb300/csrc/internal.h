@@ -91,6 +91,12 @@ cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, in
     return e;
 }
 
+// launch_chained for kernels of single CTAs without dynamic shared memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_rows(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
+    return launch_chained(kernel, grid, threads, 0, 1, s, static_cast<Args&&>(args)...);
+}
+
 // Kernel launchers implemented in the per-format translation units.  Arguments
 // are already validated by the C-ABI layer.
 // row_perm (device, M entries): C row row_perm[r] receives row r; only for
@@ -173,5 +179,31 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
                                 int64_t ldo, cudaStream_t s);
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
                               int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s);
+
+// The router; rows in 8 bits; the gated block and the gradient of its activation.
+spmm_status launch_topk(const void* logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k, int32_t renorm,
+                        void* ids, int32_t id_bytes, float* w, cudaStream_t s);
+spmm_status launch_topk_grad(const void* logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
+                             int32_t renorm, const void* ids, int32_t id_bytes, const float* w, const float* dw,
+                             void* dlogits, int64_t ldd, cudaStream_t s);
+spmm_status launch_pack_rows(const void* x, int64_t ldx, int32_t dtype, const spmm_rows8_t* P, cudaStream_t s);
+spmm_status launch_unpack_rows(const spmm_rows8_t* P, void* out, int64_t ldo, int32_t dtype, cudaStream_t s);
+// What spmm_experts_gated writes; gu, q: null if not kept.
+struct GatedOut {
+    void* h;
+    int64_t ldh;
+    void* gu;
+    int64_t ldgu;
+    int8_t* q;
+    int64_t ldq;
+    uint8_t* scale;
+    int64_t lds;
+};
+spmm_status launch_experts_gated_vec(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
+                                     int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
+                                     cudaStream_t s);
+spmm_status launch_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                              const spmm_rows8_t* packed, int64_t N, int32_t dtype, int32_t act, void* dgu,
+                              int64_t lddgu, void* h, int64_t ldh, cudaStream_t s);
 
 }  // namespace spmm
