@@ -169,6 +169,19 @@ bool encode_tmap_4d(CUtensorMap* map, CUtensorMapDataType type, const void* base
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_5d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const uint64_t dims[5],
+                    const uint64_t strides_bytes[4], const uint32_t box[5], CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t d[5] = {dims[0], dims[1], dims[2], dims[3], dims[4]};
+    cuuint64_t st[4] = {strides_bytes[0], strides_bytes[1], strides_bytes[2], strides_bytes[3]};
+    cuuint32_t bx[5] = {box[0], box[1], box[2], box[3], box[4]};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    std::memset(map, 0, sizeof(*map));
+    return f(map, type, 5, const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 spmm_status check_24(const spmm_24_t* A, int64_t N) {
     if (!A) return SPMM_ERR_NULL;
@@ -887,7 +900,7 @@ spmm_status spmm_experts_gated(const spmm_route_t* R, const void* xs, int64_t ld
         out.scale = packed->scale;
         out.lds = packed->lds;
     }
-    return launch_experts_gated_vec(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, reinterpret_cast<cudaStream_t>(stream));
+    return launch_experts_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, reinterpret_cast<cudaStream_t>(stream));
 }
 
 spmm_status spmm_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,

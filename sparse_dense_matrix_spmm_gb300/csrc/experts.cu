@@ -22,6 +22,14 @@
 // 341 us), with few rows reading the weights from HBM (6.8-7.6 TB/s), between
 // them the producers' and the issuing thread's instructions per step.
 // The sums are fp32 in TMEM, rounded once to the operands' type.
+//   gated     [g u] = W[e] xs[p], h[p] = act(g) u     (W[e]: N gate rows, N up rows)
+// is the forward product with another order of the weights' rows and another
+// epilogue.  A tile's 128 rows are loaded as 16 gate rows, the 16 up rows of the same
+// features, the next 16 gate rows and so on (one 5-D TMA box), so that TMEM lanes 0-15 of a
+// warp's quarter hold g and lanes 16-31 hold u: the two 16-lane loads of the epilogue
+// leave g and u of one feature and row in the same thread, and neither shuffles nor
+// shared memory stand between the sums and act(g) u.  [g u] itself never leaves the SM
+// unless it is kept, rounded or as 8-bit integers whose groups of 16 are the warp's 16 features.
 //
 // Roles per CTA: warps 0, 1, 12 and 13 load A and B (TMA, 128-byte swizzle, one
 // ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-11
@@ -30,6 +38,7 @@
 // work units, 32 experts' offsets at a time, and announces them to the other
 // warps through a ring of four (a search per role cost every role its latency
 // per unit); at the end it writes the zero rows of dropped choices.
+#include "gated.cuh"
 #include "internal.h"
 #include "rowvec.cuh"
 #include "sm103_more.cuh"
@@ -38,6 +47,10 @@ namespace spmm {
 namespace {
 
 using namespace ptx;
+
+// What a kernel computes: a plain product, or the gated block that keeps nothing, [g
+// u] in the rows' type, or [g u] in 8 bits.
+enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3 };
 
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half of the columns each
 constexpr int kMoreProducers = 4 + kEpiWarps;  // first warp of the second pair of producers
@@ -91,6 +104,30 @@ __host__ __device__ constexpr int boxed_rows(int nb) {
     while (n < nb) n += 128 >> box_of(nb - n);
     return n;
 }
+
+// Further arguments of the gated block: D's rows (ExpertArgs::m) are the 2 N
+// interleaved ones, `features` = N.
+template <int FORM>
+struct Gate {};
+struct GateArgs {
+    int32_t features, act;
+};
+template <>
+struct Gate<kGated> : GateArgs {};
+template <>
+struct Gate<kGatedRows> : GateArgs {
+    CUtensorMap tmKept;  // boxes of 16 columns, 32 rows
+    void* gu;
+    int64_t ldgu;
+};
+template <>
+struct Gate<kGatedPacked> : GateArgs {
+    CUtensorMap tmKept;
+    int8_t* q;
+    int64_t ldq;
+    uint8_t* scale;
+    int64_t lds;
+};
 
 // A work unit: D rows m0.. and columns n0.. (row products: rows p0 + n0 ..) of
 // expert e, `nt` columns computed and `live` of them stored, `steps` stages.
@@ -180,7 +217,8 @@ struct Walk {
 };
 
 // Shared memory: the ring of stages, as deep as fits, two staging buffers per
-// epilogue warp (32 x 32 results of a row product, 32 x 64 of dw), barriers, units.
+// epilogue warp (32 x 32 results of a row product, 32 x 64 of dw; the gated block uses
+// the same bytes as four planes of 32 x 16), barriers, units.
 template <int CG, int TILE, bool DW>
 struct Ring {
     static constexpr int kBBytes = TILE / CG * 128;
@@ -243,6 +281,142 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
         }
         if (lane == 0) bulk_commit();  // an empty group: one per use of a buffer
         __syncwarp();
+    }
+}
+
+// Gated block: TMEM lanes 0-15 of the warp's quarter are g, 16-31 u of the same 16
+// features.  Results leave in planes of 32 rows x 16 features, four of which a warp
+// uses in turn: as a TMA box of 32 live rows (32 bytes a row, 16-byte units swizzled
+// by row / 4), the last rows of a tile in 16-byte pieces.
+constexpr int kPlanes = 4, kPlaneBytes = 1024;
+
+// One plane in 16 bits.  v[4 b] .. v[4 b + 3]: rows 8 b + 2 (lane % 4) and the next of
+// feature lane / 4, and the same of feature lane / 4 + 8.
+template <typename T>
+__device__ __forceinline__ void store_plane(const CUtensorMap* tm, T* out, int64_t ld, int column, bool in, int row,
+                                            int live, const float (&v)[16], int lane, uint32_t planes, int& turn) {
+    const uint32_t plane = planes + turn * kPlaneBytes;
+    turn = (turn + 1) % kPlanes;
+    if (lane == 0) bulk_wait_read<kPlanes - 1>();  // the store before the last three has read this plane
+    __syncwarp();
+    const uint32_t put = plane + ((lane >> 4) * 8 + (lane & 7)) * 32 + (((lane >> 3 & 1) ^ (lane >> 2 & 1)) << 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // rows 16 j .. 16 j + 15
+        const float* f = v + 8 * j;
+        using P = rows::Pair<T>;
+        stmatrix_x4_trans(put + j * 512, P::pack(f[0], f[1]), P::pack(f[2], f[3]), P::pack(f[4], f[5]), P::pack(f[6], f[7]));
+    }
+    if (live >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (in) tma_store_2d(tm, plane, column, row);
+            bulk_commit();
+        }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * i + (lane >> 1), unit = lane & 1;
+        const uint4 p = ld_shared_v4(plane + r * 32 + ((unit ^ (r >> 2 & 1)) << 4));
+        if (in && r < live)
+            __stcs(reinterpret_cast<uint4*>(out + (static_cast<int64_t>(row) + r) * ld + column + 8 * unit), p);
+    }
+    if (lane == 0) bulk_commit();  // an empty group: one per use of a plane
+    __syncwarp();
+}
+
+// One plane in 8 bits, and its 32 scale bytes.  A row's 16 features are in the 8
+// lanes of the same lane % 4, two each.
+__device__ __forceinline__ void store_packed(const Gate<kGatedPacked>& x, int column, bool in, int row, int live,
+                                             const float (&v)[16], int lane, uint32_t planes, int& turn) {
+    using namespace gated;
+    const uint32_t plane = planes + turn * kPlaneBytes;
+    turn = (turn + 1) % kPlanes;
+    if (lane == 0) bulk_wait_read<kPlanes - 1>();
+    uint32_t mine = 0;  // the scale of row 8 (lane / 8) + 2 (lane % 4) + lane / 4 % 2
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        // codes of two rows side by side, 16 bits each
+        uint32_t code = max(magnitude_code(v[4 * b]), magnitude_code(v[4 * b + 2])) |
+                        max(magnitude_code(v[4 * b + 1]), magnitude_code(v[4 * b + 3])) << 16;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) code = __vmaxu2(code, __shfl_xor_sync(0xffffffffu, code, d));
+        const uint32_t s0 = scale_byte(code & 0xFFFFu), s1 = scale_byte(code >> 16);
+        const uint32_t at = plane + (8 * b + 2 * (lane & 3)) * 16 + (lane >> 2);
+        st_shared_u8(at, quantise(v[4 * b], s0));
+        st_shared_u8(at + 8, quantise(v[4 * b + 2], s0));
+        st_shared_u8(at + 16, quantise(v[4 * b + 1], s1));
+        st_shared_u8(at + 24, quantise(v[4 * b + 3], s1));
+        if (lane >> 3 == b) mine = lane & 4 ? s1 : s0;
+    }
+    const int mine_row = 8 * (lane >> 3) + 2 * (lane & 3) + (lane >> 2 & 1);
+    if (in && mine_row < live)
+        x.scale[(static_cast<int64_t>(row) + mine_row) * x.lds + column / gated::kGroup] = static_cast<uint8_t>(mine);
+    if (live >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (in) tma_store_2d(&x.tmKept, plane, column, row);
+            bulk_commit();
+        }
+        return;
+    }
+    __syncwarp();
+    const uint4 p = ld_shared_v4(plane + lane * 16);
+    if (in && lane < live)
+        __stcs(reinterpret_cast<uint4*>(x.q + (static_cast<int64_t>(row) + lane) * x.ldq + column), p);
+    if (lane == 0) bulk_commit();
+    __syncwarp();
+}
+
+template <typename T, int ACT, int FORM>
+__device__ __forceinline__ void store_gated(const ExpertArgs& a, const Gate<FORM>& x, const CUtensorMap* tmOut,
+                                            const Unit& w, uint32_t t, int c0, int c1, int row0, int lane,
+                                            uint32_t planes, int& turn) {
+    const int f0 = row0 / 2;  // the warp's first feature: features come in groups of 16 (N % 16 == 0)
+    const bool in = row0 < a.m;
+    for (int c = c0; c < c1; c += 32) {
+        uint32_t lo[16], hi[16];
+        __syncwarp();  // as in store_rows
+        tmem_ld_16x32(t + c, lo);
+        tmem_ld_16x32(t + (16u << 16) + c, hi);
+        tmem_ld_wait();
+        float g[16], u[16], h[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            g[i] = __uint_as_float(lo[i]);
+            u[i] = __uint_as_float(hi[i]);
+            h[i] = gated::act<ACT>(g[i]) * u[i];
+        }
+        const int row = w.p0 + w.n0 + c, live = c1 - c;
+        store_plane<T>(tmOut, static_cast<T*>(a.out), a.ldo, f0, in, row, live, h, lane, planes, turn);
+        if constexpr (FORM == kGatedRows) {
+            store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, f0, in, row, live, g, lane, planes, turn);
+            store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, x.features + f0, in, row, live, u, lane, planes, turn);
+        }
+        if constexpr (FORM == kGatedPacked) {
+            store_packed(x, f0, in, row, live, g, lane, planes, turn);
+            store_packed(x, x.features + f0, in, row, live, u, lane, planes, turn);
+        }
+    }
+}
+
+// The kept form of rows past the last expert's: zeros. Called by a warp per row.
+template <int FORM>
+__device__ __forceinline__ void clear_kept(const Gate<FORM>& x, int64_t p, int lane) {
+    if constexpr (FORM == kGatedRows) {
+        uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(x.gu) + p * x.ldgu);
+        for (int c = lane; c < x.features / 4; c += 32) row[c] = make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (FORM == kGatedPacked) {
+        uint4* row = reinterpret_cast<uint4*>(x.q + p * x.ldq);
+        for (int c = lane; c < x.features / 8; c += 32) {
+            row[c] = make_uint4(0, 0, 0, 0);
+            x.scale[p * x.lds + c] = 1;
+        }
     }
 }
 
@@ -325,6 +499,14 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint
         tma_load_3d(dst, m, bar, c0, c1, c2);
 }
 template <int CG>
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
+                                        int c4) {
+    if (CG == 2)
+        tma_load_5d_pair(dst, m, bar, c0, c1, c2, c3, c4);
+    else
+        tma_load_5d(dst, m, bar, c0, c1, c2, c3, c4);
+}
+template <int CG>
 __device__ __forceinline__ void sync_all() {
     if (CG == 2)
         cluster_sync_all();
@@ -334,10 +516,11 @@ __device__ __forceinline__ void sync_all() {
 
 // AMN / BMN: the operand's contiguous direction is D's row / column (else the
 // depth).  BMN is dw.
-template <int CG, int TILE, bool AMN, bool BMN>
+template <int CG, int TILE, bool AMN, bool BMN, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
-                   const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a) {
+                   const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a,
+                   const __grid_constant__ Gate<FORM> gate) {
     constexpr bool DW = BMN;
     using G = Ring<CG, TILE, DW>;
     extern __shared__ uint8_t smem_raw[];
@@ -451,6 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (AMN) {
                             load_3d<CG>(st, &tmA, bar, m0, d0, w.e);
                             load_3d<CG>(st + kABytes / 2, &tmA, bar, m0 + 64, d0, w.e);
+                        } else if (FORM != kPlain) {
+                            load_5d<CG>(st, &tmA, bar, d0, 0, 0, m0 / 32, w.e);  // 32 rows of D: 16 gate, 16 up
                         } else {
                             load_3d<CG>(st, &tmA, bar, d0, m0, w.e);
                         }
@@ -607,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!DW) {
             for (int64_t p = a.offsets[a.E] + static_cast<int64_t>(blockIdx.x); p < a.R; p += gridDim.x) {
                 uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + p * a.ldo);
-                for (int c = lane; c < a.m / 8; c += 32) row[c] = make_uint4(0, 0, 0, 0);
+                for (int c = lane; c < (FORM == kPlain ? a.m / 8 : a.m / 16); c += 32) row[c] = make_uint4(0, 0, 0, 0);
+                clear_kept(gate, p, lane);
             }
         }
     } else {  // warps 4 .. 11
@@ -626,7 +812,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // columns past the live ones of this warp's half are computed but not stored
             const int c0 = half * (TILE / 2), c1 = min(w.live, c0 + TILE / 2);
-            if (DW) {
+            if constexpr (FORM != kPlain) {
+                auto store = [&](auto type, auto act) {
+                    using T = decltype(type);
+                    store_gated<T, decltype(act)::value, FORM>(a, gate, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
+                };
+                auto typed = [&](auto act) {
+                    if (a.bf16)
+                        store(__nv_bfloat16(), act);
+                    else
+                        store(__half(), act);
+                };
+                if (gate.act == SPMM_ACT_SILU)
+                    typed(std::integral_constant<int, SPMM_ACT_SILU>());
+                else if (gate.act == SPMM_ACT_GELU)
+                    typed(std::integral_constant<int, SPMM_ACT_GELU>());
+                else
+                    typed(std::integral_constant<int, SPMM_ACT_GELU_TANH>());
+            } else if (DW) {
                 if (a.bf16)
                     store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
                 else
@@ -863,18 +1066,20 @@ bool rows_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t ld, int64_
                           static_cast<uint64_t>(ld) * 2, kDepth, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int CG, int TILE, bool AMN, bool BMN>
+template <int CG, int TILE, bool AMN, bool BMN, int FORM = kPlain>
 spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const CUtensorMap& tmOut, const ExpertArgs& a,
-                   int64_t units, const DeviceInfo* dev, cudaStream_t s) {
+                   int64_t units, const DeviceInfo* dev, cudaStream_t s, const Gate<FORM>& gate = {}) {
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
-    const auto kern = experts_kernel<CG, TILE, AMN, BMN>;
+    const auto kern = experts_kernel<CG, TILE, AMN, BMN, FORM>;
     constexpr int smem = Ring<CG, TILE, BMN>::kSmem;
-    constexpr int slot = kSlotExperts + (TILE < 256 ? 6 : 0) + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0);
+    constexpr int slot = FORM == kPlain
+                             ? kSlotExperts + (TILE < 256 ? 6 : 0) + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0)
+                             : kSlotGated + 3 * (FORM - 1) + (TILE < 256 ? 2 : CG - 1);
     if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, slot)) return SPMM_ERR_CUDA;
     const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
     const cudaError_t e = launch_chained(kern, static_cast<unsigned>(groups * CG), kThreads, smem, CG, s, tmA, tmB,
-                                         tmOut, a);
+                                         tmOut, a, gate);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
 }
@@ -972,6 +1177,75 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
     return pair ? launch<2, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s)
                 : launch<1, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s);
+}
+
+namespace {
+
+template <int FORM>
+spmm_status launch_gated(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw, int64_t lde,
+                         int64_t N, int64_t K, int32_t dtype, void* h, int64_t ldh, const Gate<FORM>& gate,
+                         const DeviceInfo* dev, cudaStream_t s) {
+    const int64_t n = R->T * R->k, E = R->n_keys;
+    ExpertArgs a{};
+    a.offsets = R->offsets;
+    a.E = static_cast<int32_t>(E);
+    a.R = static_cast<int32_t>(n);
+    a.m = static_cast<int32_t>(2 * N);
+    a.depth = static_cast<int32_t>(K);
+    a.out = h;
+    a.ldo = ldh;
+    a.bf16 = dtype == SPMM_BF16;
+    a.err = dev->err;
+    a.timeout_ns = wait_limit_ns(a.depth);
+    const bool pair = a.m > 128;
+    a.m_tiles = pair ? (a.m + 255) / 256 : 1;
+    const int tile = pair && n <= E * kFewRows ? 64 : 256;
+    CUtensorMap tmA, tmOut;
+    BMaps tmB{};
+    // the weights' rows as (16 rows, gate or up, groups of 16)
+    const uint64_t row = static_cast<uint64_t>(ldw) * 2;
+    const uint64_t dims[5] = {static_cast<uint64_t>(K), 16, 2, static_cast<uint64_t>(N / 16), static_cast<uint64_t>(E)};
+    const uint64_t strides[4] = {row, row * static_cast<uint64_t>(N), row * 16, static_cast<uint64_t>(lde) * 2};
+    const uint32_t box[5] = {kDepth, 16, 2, 4, 1};
+    if (!encode_tmap_5d(&tmA, half_type(dtype), W, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return SPMM_ERR_CUDA;
+    const int64_t most = ((n < tile ? n : tile) + 31) / 32 * 32 / (pair ? 2 : 1);
+    for (int i = box_of(static_cast<int>(most)); i < 4; ++i)
+        if (!rows_map(&tmB.m[i], dtype, xs, ldx, n, K, 128u >> i)) return SPMM_ERR_CUDA;
+    if (!encode_tmap_2d(&tmOut, half_type(dtype), h, static_cast<uint64_t>(N), static_cast<uint64_t>(n),
+                        static_cast<uint64_t>(ldh) * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B))
+        return SPMM_ERR_CUDA;
+    const int64_t units = (n / tile + (n < E ? n : E)) * a.m_tiles;
+    if (tile == 64) return launch<2, 64, false, false, FORM>(tmA, tmB, tmOut, a, units, dev, s, gate);
+    if (pair) return launch<2, 256, false, false, FORM>(tmA, tmB, tmOut, a, units, dev, s, gate);
+    return launch<1, 256, false, false, FORM>(tmA, tmB, tmOut, a, units, dev, s, gate);
+}
+
+}  // namespace
+
+spmm_status launch_experts_gated(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
+                                 int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
+                                 cudaStream_t s) {
+    const int64_t n = R->T * R->k;
+    if (n <= kVecMost) return launch_experts_gated_vec(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, s);
+    const DeviceInfo* dev = device_info();
+    if (!dev) return SPMM_ERR_CUDA;
+    const GateArgs g{static_cast<int32_t>(N), act};
+    const uint64_t cols = static_cast<uint64_t>(2 * N), rows = static_cast<uint64_t>(n);
+    if (out.gu) {
+        Gate<kGatedRows> x{g, {}, out.gu, out.ldgu};
+        if (!encode_tmap_2d(&x.tmKept, half_type(dtype), out.gu, cols, rows, static_cast<uint64_t>(out.ldgu) * 2, 16, 32,
+                            CU_TENSOR_MAP_SWIZZLE_32B))
+            return SPMM_ERR_CUDA;
+        return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, x, dev, s);
+    }
+    if (out.q) {
+        Gate<kGatedPacked> x{g, {}, out.q, out.ldq, out.scale, out.lds};
+        if (!encode_tmap_2d(&x.tmKept, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.q, cols, rows, static_cast<uint64_t>(out.ldq), 16,
+                            32, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return SPMM_ERR_CUDA;
+        return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, x, dev, s);
+    }
+    return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, Gate<kGated>{g}, dev, s);
 }
 
 }  // namespace spmm

@@ -19,7 +19,7 @@ constexpr int kVecWarps = 16, kVecRows = 4;
 
 struct VecArgs {
     const int32_t* offsets;
-    int32_t E, R;
+    int32_t E;
     const void *xs, *W;
     int64_t ldx, ldw, lde;
     int32_t N, K;
@@ -82,55 +82,51 @@ __global__ void __launch_bounds__(kVecWarps * 32, 2) gated_vec_kernel(const VecA
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n0 = blockIdx.x * kVecWarps;
-    for (int p = blockIdx.y; p < a.R; p += gridDim.y) {
-        int rows = 1;
-        const bool live = p < a.offsets[a.E];
-        if (live) {
-            int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32, at = lo + step * lane;
-                const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= p);
-                lo += step * (31 - __clz(le));
-                hi = min(hi, lo + step);
-            }
-            if ((p - a.offsets[lo]) % kVecRows) continue;
-            rows = min(kVecRows, a.offsets[lo + 1] - p);
-            const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
-            const T* wg = static_cast<const T*>(a.W) + lo * a.lde + (n0 + warp) * a.ldw;
-            const T* wu = wg + a.N * a.ldw;
-            if (rows == 1)
-                dot_rows<T, 1>(a, wg, wu, x, lane, sums, warp);
-            else if (rows == 2)
-                dot_rows<T, 2>(a, wg, wu, x, lane, sums, warp);
-            else if (rows == 3)
-                dot_rows<T, 3>(a, wg, wu, x, lane, sums, warp);
-            else
-                dot_rows<T, 4>(a, wg, wu, x, lane, sums, warp);
+    const int p = blockIdx.y, n0 = blockIdx.x * kVecWarps;
+    int rows = 1;
+    const bool live = p < a.offsets[a.E];
+    if (live) {
+        int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = lo + step * lane;
+            const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= p);
+            lo += step * (31 - __clz(le));
+            hi = min(hi, lo + step);
         }
-        __syncthreads();
-        if (threadIdx.x < 2 * kVecRows * 16) {  // whole warps: half, row, feature
-            const int f = threadIdx.x & 15, c = threadIdx.x >> 4 & 3, half = threadIdx.x >> 6;
-            const bool in = c < rows;
-            const float v = live && in ? sums[half][c][f] : 0.f;
-            const int64_t row = p + c;
-            const int n = n0 + f;
-            if (half == 0 && in)
-                static_cast<T*>(a.out.h)[row * a.out.ldh + n] = from_f32<T>(live ? act<ACT>(v) * sums[1][c][f] : 0.f);
-            if (a.out.gu && in) static_cast<T*>(a.out.gu)[row * a.out.ldgu + half * a.N + n] = from_f32<T>(v);
-            if (a.out.q) {
-                uint32_t code = magnitude_code(v);
+        if ((p - a.offsets[lo]) % kVecRows) return;
+        rows = min(kVecRows, a.offsets[lo + 1] - p);
+        const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
+        const T* wg = static_cast<const T*>(a.W) + lo * a.lde + (n0 + warp) * a.ldw;
+        const T* wu = wg + a.N * a.ldw;
+        if (rows == 1)
+            dot_rows<T, 1>(a, wg, wu, x, lane, sums, warp);
+        else if (rows == 2)
+            dot_rows<T, 2>(a, wg, wu, x, lane, sums, warp);
+        else if (rows == 3)
+            dot_rows<T, 3>(a, wg, wu, x, lane, sums, warp);
+        else
+            dot_rows<T, 4>(a, wg, wu, x, lane, sums, warp);
+    }
+    __syncthreads();
+    if (threadIdx.x >= 2 * kVecRows * 16) return;  // whole warps: half, row, feature
+    const int f = threadIdx.x & 15, c = threadIdx.x >> 4 & 3, half = threadIdx.x >> 6;
+    const bool in = c < rows;
+    const float v = live && in ? sums[half][c][f] : 0.f;
+    const int64_t row = p + c;
+    const int n = n0 + f;
+    if (half == 0 && in)
+        static_cast<T*>(a.out.h)[row * a.out.ldh + n] = from_f32<T>(live ? act<ACT>(v) * sums[1][c][f] : 0.f);
+    if (a.out.gu && in) static_cast<T*>(a.out.gu)[row * a.out.ldgu + half * a.N + n] = from_f32<T>(v);
+    if (a.out.q) {
+        uint32_t code = magnitude_code(v);
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, d));
-                const uint32_t b = scale_byte(code);
-                const int64_t col = static_cast<int64_t>(half) * a.N + n;
-                if (in) {
-                    a.out.q[row * a.out.ldq + col] = static_cast<int8_t>(quantise(v, b));
-                    if (f == 0) a.out.scale[row * a.out.lds + col / kGroup] = static_cast<uint8_t>(b);
-                }
-            }
+        for (int d = 1; d < 16; d <<= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, d));
+        const uint32_t b = scale_byte(code);
+        const int64_t col = static_cast<int64_t>(half) * a.N + n;
+        if (in) {
+            a.out.q[row * a.out.ldq + col] = static_cast<int8_t>(quantise(v, b));
+            if (f == 0) a.out.scale[row * a.out.lds + col / kGroup] = static_cast<uint8_t>(b);
         }
-        __syncthreads();
     }
 }
 
@@ -222,8 +218,8 @@ cudaError_t launch_grad(const GradArgs& a, int32_t act, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_vec(const VecArgs& a, int32_t act, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.N / kVecWarps), static_cast<unsigned>(a.R < 65535 ? a.R : 65535));
+cudaError_t launch_vec(const VecArgs& a, int64_t rows, int32_t act, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(a.N / kVecWarps), static_cast<unsigned>(rows));
     return launch_rows(act == SPMM_ACT_SILU   ? gated_vec_kernel<T, SPMM_ACT_SILU>
                        : act == SPMM_ACT_GELU ? gated_vec_kernel<T, SPMM_ACT_GELU>
                                               : gated_vec_kernel<T, SPMM_ACT_GELU_TANH>,
@@ -235,10 +231,12 @@ cudaError_t launch_vec(const VecArgs& a, int32_t act, cudaStream_t s) {
 spmm_status launch_experts_gated_vec(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
                                      int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
                                      cudaStream_t s) {
-    const VecArgs a{R->offsets, static_cast<int32_t>(R->n_keys), static_cast<int32_t>(R->T * R->k), xs, W, ldx, ldw, lde,
-                    static_cast<int32_t>(N), static_cast<int32_t>(K), out};
+    const VecArgs a{R->offsets, static_cast<int32_t>(R->n_keys), xs, W, ldx, ldw, lde, static_cast<int32_t>(N),
+                    static_cast<int32_t>(K), out};
+    const int64_t rows = R->T * R->k;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    const cudaError_t e = dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16>(a, act, s) : launch_vec<__half>(a, act, s);
+    const cudaError_t e =
+        dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16>(a, rows, act, s) : launch_vec<__half>(a, rows, act, s);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
 }

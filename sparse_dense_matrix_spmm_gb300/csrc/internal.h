@@ -37,6 +37,10 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base
 bool encode_tmap_4d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const uint64_t dims[4],
                     const uint64_t strides_bytes[3], const uint32_t box[4], CUtensorMapSwizzle swizzle);
 
+// 5-D tiled tensor map: dims[0] contiguous, byte strides of dims 1-4.
+bool encode_tmap_5d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const uint64_t dims[5],
+                    const uint64_t strides_bytes[4], const uint32_t box[5], CUtensorMapSwizzle swizzle);
+
 inline spmm_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SPMM_OK : SPMM_ERR_CUDA; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -61,8 +65,8 @@ void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
 // First of the twelve slots of set_smem_attr_once that the experts' kernels take
-// (0-23 belong to the format kernels).
-enum : int { kSlotExperts = 24 };
+// (0-23 belong to the format kernels), and of the nine that their gated form takes.
+enum : int { kSlotExperts = 24, kSlotGated = 36 };
 
 // Raise a kernel's dynamic shared memory limit once per device.
 bool set_smem_attr_once(const void* kernel, int bytes, int slot);
@@ -199,6 +203,10 @@ struct GatedOut {
     uint8_t* scale;
     int64_t lds;
 };
+spmm_status launch_experts_gated(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
+                                 int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
+                                 cudaStream_t s);
+// The same for a few rows in all, on CUDA cores.
 spmm_status launch_experts_gated_vec(const spmm_route_t* R, const void* xs, int64_t ldx, const void* W, int64_t ldw,
                                      int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
                                      cudaStream_t s);
