@@ -610,7 +610,7 @@ SPMM_API spmm_status spmm_topk(const void *logits, int64_t T, int64_t E, int64_t
  * gradient dw[T][k] (fp32) of w: dlogits[t][e] = sum over j with ids[t][j] = e of
  * w_j dw_j, less p_e sum_i w_i dw_i, where p_e is the softmax over the chosen (renorm
  * = 1: the w_j, zero elsewhere, and logits may be null) or over all E.  Every entry is
- * written; a negative id is a dropped choice, whose w and dw are not read; an id >= E is dropped too and
+ * written; a negative id is a dropped choice, whose w and dw do not count; an id >= E is dropped too and
  * sets SPMM_DEVERR_INDEX.  dlogits has the logits' type. */
 SPMM_API spmm_status spmm_topk_grad(const void *logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
                                     int32_t renorm, const void *ids, int32_t id_bytes, const float *w,

@@ -826,35 +826,49 @@ def spmm_experts_grad(R: Route, dys: torch.Tensor, xs: torch.Tensor, W: torch.Te
 _ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH}
 
 
-@dataclass
 class Rows8:
     """rows x cols values of dtype held in 8 bits: 16 consecutive values of a row share
     a power of two, value = q 2^(scale - 127) (scale 255: NaN).  q is int8, rows x
-    cols, scale uint8, rows x ceil(cols / 16); both may be views of wider rows."""
-    rows: int
-    cols: int
-    dtype: torch.dtype
-    q: torch.Tensor
-    scale: torch.Tensor
+    cols, scale uint8, rows x ceil(cols / 16); both may be views of wider rows.  Like a
+    Route it holds its tensors' addresses, so assigning to a field raises."""
+
+    def __init__(self, rows: int, cols: int, dtype: torch.dtype, q: torch.Tensor, scale: torch.Tensor):
+        groups = -(-cols // 16)
+        for t, what, dt, n in ((q, "q", torch.int8, cols), (scale, "scale", torch.uint8, groups)):
+            if not t.is_cuda or t.device != q.device:
+                raise ValueError("q and scale must be on one CUDA device (this library has no CPU path)")
+            if t.dtype is not dt or t.shape != (rows, n):
+                raise ValueError(f"{what} must be {rows} x {n} of {dt}")
+            if n > 1 and rows > 0 and t.stride(1) != 1:
+                raise ValueError(f"{what} must have contiguous rows")
+        self._hold(rows, cols, dtype, q, q.stride(0) if rows > 1 else groups * 16, scale,
+                   scale.stride(0) if rows > 1 else groups)
+
+    def _hold(self, rows, cols, dtype, q, ldq, scale, lds):
+        self.__dict__.update(rows=rows, cols=cols, dtype=dtype, q=q, scale=scale, device=q.device,
+                             _ref=C.byref(_lib.Rows8T(rows, cols, q.data_ptr(), ldq, scale.data_ptr(), lds)))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"cannot assign to {name}: 8-bit rows hold their tensors' addresses")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"cannot delete {name}: 8-bit rows hold their tensors' addresses")
+
+    def __reduce__(self):
+        return Rows8, (self.rows, self.cols, self.dtype, self.q, self.scale)
 
     def c(self) -> _lib.Rows8T:
-        groups = -(-self.cols // 16)
-        for t, what, dt, n in ((self.q, "q", torch.int8, self.cols), (self.scale, "scale", torch.uint8, groups)):
-            if not t.is_cuda or t.device != self.q.device:
-                raise ValueError("q and scale must be on one CUDA device (this library has no CPU path)")
-            if t.dtype is not dt or t.shape != (self.rows, n):
-                raise ValueError(f"{what} must be {self.rows} x {n} of {dt}")
-            if n > 1 and self.rows > 0 and t.stride(1) != 1:
-                raise ValueError(f"{what} must have contiguous rows")
-        wide = self.rows > 1
-        return _lib.Rows8T(self.rows, self.cols, self.q.data_ptr(), self.q.stride(0) if wide else -(-self.cols // 16) * 16,
-                           self.scale.data_ptr(), self.scale.stride(0) if wide else groups)
+        return self._ref._obj
 
 
 def _rows8(like: torch.Tensor, rows: int, cols: int, dtype, stream) -> Rows8:
     """Unwritten 8-bit rows; the pitch of q is a multiple of 16, so that every row moves in wide pieces."""
-    q = _empty(like, (rows, -(-cols // 16) * 16), torch.int8, stream)[:, :cols]
-    return Rows8(rows, cols, dtype, q, _empty(like, (rows, -(-cols // 16)), torch.uint8, stream))
+    groups = (cols + 15) // 16
+    q = _empty(like, (rows, groups * 16), torch.int8, stream)
+    P = Rows8.__new__(Rows8)
+    P._hold(rows, cols, dtype, q if cols == groups * 16 else q[:, :cols], groups * 16,
+            _empty(like, (rows, groups), torch.uint8, stream), groups)
+    return P
 
 
 def _act(act: str) -> int:
@@ -925,21 +939,20 @@ def spmm_pack_rows(x: torch.Tensor, out: Optional[Rows8] = None, stream=None) ->
     code, ldx = _row_code(x.dtype), _rows(x, "x", rows, cols, x.dtype, x.device)
     if out is None:
         out = _rows8(x, rows, cols, x.dtype, stream)
-    elif (out.rows, out.cols, out.dtype, out.q.device) != (rows, cols, x.dtype, x.device):
+    elif (out.rows, out.cols, out.dtype, out.device) != (rows, cols, x.dtype, x.device):
         raise ValueError(f"out must hold {rows} x {cols} values of {x.dtype} on {x.device}")
-    _lib.call("spmm_pack_rows", x.data_ptr(), ldx, code, C.byref(out.c()), _handle(stream, x.device))
+    _lib.call("spmm_pack_rows", x.data_ptr(), ldx, code, out._ref, _handle(stream, x.device))
     return out
 
 
 def spmm_unpack_rows(P: Rows8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The rows that P holds, of P.dtype (or of out's type)."""
-    dev = P.q.device
-    p = P.c()
+    dev = P.device
     if out is None:
         out, ldo = _empty(P.q, (P.rows, P.cols), P.dtype, stream), P.cols
     else:
         ldo = _rows(out, "out", P.rows, P.cols, out.dtype, dev)
-    _lib.call("spmm_unpack_rows", C.byref(p), out.data_ptr(), ldo, _row_code(out.dtype), _handle(stream, dev))
+    _lib.call("spmm_unpack_rows", P._ref, out.data_ptr(), ldo, _row_code(out.dtype), _handle(stream, dev))
     return out
 
 
@@ -963,7 +976,7 @@ def spmm_experts_gated(R: Route, xs: torch.Tensor, W: torch.Tensor, act: str = "
     gu = _empty(xs, (rows, 2 * N), dt, stream) if save == "rows" else None
     packed = _rows8(xs, rows, 2 * N, dt, stream) if save == "packed" else None
     _lib.call("spmm_experts_gated", R._ref, xs.data_ptr(), ldx, W.data_ptr(), ldw, lde, N, K, code, actc, out.data_ptr(), ldo,
-              None if gu is None else gu.data_ptr(), 2 * N, None if packed is None else C.byref(packed.c()),
+              None if gu is None else gu.data_ptr(), 2 * N, None if packed is None else packed._ref,
               _handle(stream, dev))
     return out if save is None else (out, gu if packed is None else packed)
 
@@ -977,9 +990,9 @@ def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: b
     N = dh.shape[-1]
     code, ldd, actc = _row_code(dt), _rows(dh, "dh", rows, N, dt, dev), _act(act)
     if isinstance(gu, Rows8):
-        if (gu.rows, gu.cols, gu.q.device) != (rows, 2 * N, dev):
+        if (gu.rows, gu.cols, gu.device) != (rows, 2 * N, dev):
             raise ValueError(f"gu must hold {rows} x {2 * N} values on {dev}")
-        gu_ptr, ldgu, packed = None, 2 * N, C.byref(gu.c())
+        gu_ptr, ldgu, packed = None, 2 * N, gu._ref
     else:
         ldgu = _rows(gu, "gu", rows, 2 * N, dt, dev)
         gu_ptr, packed = gu.data_ptr(), None

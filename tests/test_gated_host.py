@@ -1,4 +1,5 @@
 """What the gated experts' wrappers refuse on the host, without a GPU."""
+import copy
 import inspect
 from types import SimpleNamespace
 
@@ -30,7 +31,7 @@ def test_every_wrapper_asks_for_the_handle():
 def test_host_tensors_are_refused():
     x = torch.zeros(4, 16)
     for f in (lambda: spmm.spmm_topk(x, 2), lambda: spmm.spmm_pack_rows(x),
-              lambda: spmm.spmm_unpack_rows(spmm.Rows8(4, 16, x.dtype, x.to(torch.int8), x[:, :1].to(torch.uint8)))):
+              lambda: spmm.Rows8(4, 16, x.dtype, x.to(torch.int8), x[:, :1].to(torch.uint8))):
         with pytest.raises(ValueError, match="no CPU path"):
             f()
 
@@ -63,13 +64,25 @@ def test_rows8_arguments():
     assert (c.rows, c.cols, c.ldq, c.lds) == (4, 40, 40, 3)
     c = spmm.Rows8(1, 40, torch.bfloat16, _cuda((1, 40), torch.int8), _cuda((1, 3), torch.uint8)).c()
     assert (c.ldq, c.lds) == (48, 3)
-    for P in (spmm.Rows8(4, 40, torch.bfloat16, q, _cuda((4, 2), torch.uint8)),
-              spmm.Rows8(4, 41, torch.bfloat16, q, s), spmm.Rows8(4, 40, torch.bfloat16, _cuda((4, 40), torch.uint8), s),
-              spmm.Rows8(4, 40, torch.bfloat16, _cuda((4, 40), torch.int8, (1, 4)), s)):
+    for cols, q1, s1 in ((40, q, _cuda((4, 2), torch.uint8)), (41, q, s), (40, _cuda((4, 40), torch.uint8), s),
+                         (40, _cuda((4, 40), torch.int8, (1, 4)), s), (40, q, _cuda((4, 3), torch.uint8, (1, 4)))):
         with pytest.raises(ValueError, match="must"):
-            P.c()
+            spmm.Rows8(4, cols, torch.bfloat16, q1, s1)
     with pytest.raises(ValueError, match="out must hold"):
         spmm.spmm_pack_rows(_cuda((4, 39)), spmm.Rows8(4, 40, torch.bfloat16, q, s))
+
+
+@pytest.mark.parametrize("name", ["rows", "cols", "dtype", "q", "scale", "device"])
+def test_rows8_fields_cannot_be_replaced(name):
+    """The C struct holds the tensors' addresses: a replaced tensor would leave the kernels on freed memory."""
+    P = spmm.Rows8(4, 40, torch.bfloat16, _cuda((4, 40), torch.int8, (48, 1)), _cuda((4, 3), torch.uint8))
+    before = getattr(P, name)
+    with pytest.raises(AttributeError, match="addresses"):
+        setattr(P, name, before)
+    with pytest.raises(AttributeError, match="addresses"):
+        delattr(P, name)
+    c = copy.copy(P)
+    assert getattr(c, name) is before and c._ref is not P._ref and (c.c().ldq, c.c().lds, c.c().q) == (48, 3, 256)
 
 
 def test_gated_arguments():
