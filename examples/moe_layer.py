@@ -4,8 +4,8 @@ training steps, then one decoding step.
     python examples/moe_layer.py [--tokens T --experts E --top K --width H --hidden F --vocab V --steps N]
 
 The layer is y = x + sum over a token's experts e of w_e W2_e silu(W1_e x) with
-x = embed(token).  Rows are bf16, weights of the experts fp32; the router, the
-activation and the loss are ordinary torch operations.
+x = embed(token).  Rows are bf16, weights of the experts fp32; the router's
+projection, the activation and the loss are ordinary torch operations.
 """
 from __future__ import annotations
 
@@ -42,29 +42,27 @@ class Layer:
 def forward(layer: Layer, tokens: torch.Tensor):
     """y and what the backward pass needs."""
     x = spmm.spmm_embed(layer.table, tokens)
-    scores = torch.topk(x.float() @ layer.router.float().t(), layer.top, dim=1)
-    w = torch.softmax(scores.values, dim=1).contiguous()
-    R = spmm.spmm_build_route(scores.indices, layer.W1.shape[0])
+    logits = x.float() @ layer.router.float().t()
+    chosen, w = spmm.spmm_topk(logits, layer.top)
+    R = spmm.spmm_build_route(chosen, layer.W1.shape[0])
     xs = spmm.spmm_dispatch(R, x)
     h = spmm.spmm_experts(R, xs, layer.W1)
     a = torch.nn.functional.silu(h.float()).to(h.dtype)
     ys = spmm.spmm_experts(R, a, layer.W2)
     y = x + spmm.spmm_combine(R, ys, w)
-    return y, (tokens, x, R, w, scores.indices, xs, h, a, ys)
+    return y, (tokens, x, R, w, chosen, xs, h, a, ys, logits)
 
 
 def backward(layer: Layer, saved, dy: torch.Tensor):
     """Gradients of the table, the router, W1 and W2 for the gradient dy of y."""
-    tokens, x, R, w, chosen, xs, h, a, ys = saved
+    tokens, x, R, w, chosen, xs, h, a, ys, logits = saved
     dys, dw = spmm.spmm_combine_grad(R, dy, ys, w)
     da, dW2 = spmm.spmm_experts_grad(R, dys, a, layer.W2)
     s = torch.sigmoid(h.float())
     dh = (da.float() * s * (1 + h.float() * (1 - s))).to(h.dtype)
     dxs, dW1 = spmm.spmm_experts_grad(R, dh, xs, layer.W1)
     dx = dy.float() + spmm.spmm_dispatch_grad(R, dxs).float()
-    # softmax over the chosen scores, then the scores' product with the router
-    dscore = w * (dw - (dw * w).sum(1, keepdim=True))
-    dlogits = torch.zeros(x.shape[0], layer.router.shape[0], device=x.device).scatter_(1, chosen, dscore)
+    dlogits = spmm.spmm_topk_grad(logits, chosen, w, dw)
     dx += dlogits @ layer.router.float()
     drouter = dlogits.t() @ x.float()
     V = spmm.spmm_build_route(tokens, layer.table.shape[0])

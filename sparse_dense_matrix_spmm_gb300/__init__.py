@@ -54,7 +54,7 @@ __all__ = ["BCSR", "Mat24", "Slide", "TVW", "CSR", "WCSR", "SpmmError", "spmm_bc
            "spmm_combine", "spmm_combine_grad", "spmm_embed", "spmm_embed_grad", "spmm_embed_grad_workspace_size",
            "spmm_experts", "spmm_experts_dx", "spmm_experts_dw", "spmm_experts_grad",
            "Rows8", "spmm_topk", "spmm_topk_grad", "spmm_pack_rows", "spmm_unpack_rows",
-           "spmm_experts_gated", "spmm_gated_grad", "spmm_experts_gated_grad",
+           "spmm_experts_gated", "spmm_gated_grad", "spmm_experts_gated_grad", "spmm_experts_gated_grad_workspace_size",
            "last_device_error", "selftest_timeout", "library_path", "trace_enable", "trace_read"]
 
 _DT = {torch.bfloat16: _lib.SPMM_BF16, torch.float16: _lib.SPMM_F16, torch.int8: _lib.SPMM_I8,
@@ -864,10 +864,14 @@ class Rows8:
 def _rows8(like: torch.Tensor, rows: int, cols: int, dtype, stream) -> Rows8:
     """Unwritten 8-bit rows; the pitch of q is a multiple of 16, so that every row moves in wide pieces."""
     groups = (cols + 15) // 16
-    q = _empty(like, (rows, groups * 16), torch.int8, stream)
+    ldq = groups * 16
+    if stream is None:  # (slicing a wider tensor costs the host twice as much)
+        q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.int8, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.int8, device=like.device)
     P = Rows8.__new__(Rows8)
-    P._hold(rows, cols, dtype, q if cols == groups * 16 else q[:, :cols], groups * 16,
-            _empty(like, (rows, groups), torch.uint8, stream), groups)
+    P._hold(rows, cols, dtype, q, ldq, _empty(like, (rows, groups), torch.uint8, stream), groups)
     return P
 
 
@@ -989,13 +993,7 @@ def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: b
     dev, dt, rows = R.device, dh.dtype, R.n_rows
     N = dh.shape[-1]
     code, ldd, actc = _row_code(dt), _rows(dh, "dh", rows, N, dt, dev), _act(act)
-    if isinstance(gu, Rows8):
-        if (gu.rows, gu.cols, gu.device) != (rows, 2 * N, dev):
-            raise ValueError(f"gu must hold {rows} x {2 * N} values on {dev}")
-        gu_ptr, ldgu, packed = None, 2 * N, gu._ref
-    else:
-        ldgu = _rows(gu, "gu", rows, 2 * N, dt, dev)
-        gu_ptr, packed = gu.data_ptr(), None
+    gu_ptr, ldgu, packed = _kept(gu, rows, N, dt, dev)
     if out is None:
         out, ldo = _empty(dh, (rows, 2 * N), dt, stream), 2 * N
     else:
@@ -1006,11 +1004,41 @@ def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: b
     return (out, h) if with_h else out
 
 
-def spmm_experts_gated_grad(R: Route, dh: torch.Tensor, xs, W: torch.Tensor, gu, act: str = "silu", stream=None):
+def _kept(gu, rows: int, N: int, dtype, device):
+    """(address, pitch, 8-bit struct) of what a forward call kept of [g u]."""
+    if isinstance(gu, Rows8):
+        if (gu.rows, gu.cols, gu.device) != (rows, 2 * N, device):
+            raise ValueError(f"gu must hold {rows} x {2 * N} values on {device}")
+        return None, 2 * N, gu._ref
+    return gu.data_ptr(), _rows(gu, "gu", rows, 2 * N, dtype, device), None
+
+
+def spmm_experts_gated_grad_workspace_size(R: Route, K: int, packed_rows: bool) -> int:
+    n = C.c_size_t(0)
+    _lib.call("spmm_experts_gated_grad_workspace_size", R._ref, K, 1 if packed_rows else 0, C.byref(n))
+    return n.value
+
+
+def spmm_experts_gated_grad(R: Route, dh: torch.Tensor, xs, W: torch.Tensor, gu, act: str = "silu",
+                            workspace: Optional[torch.Tensor] = None, stream=None):
     """The gradients (dgu, dxs, dW) of spmm_experts_gated from the gradient dh of h: xs
-    (rows or their Rows8 checkpoint) and W as in the forward call, gu what it saved."""
-    dgu = spmm_gated_grad(R, dh, gu, act, stream=stream)
-    dxs = spmm_experts_dx(R, dgu, W, stream=stream)
+    (rows, or the Rows8 checkpoint of them) and W as in the forward call, gu what it saved.
+    dxs and dW are products of dgu as it is rounded."""
+    dev, dt, rows = R.device, dh.dtype, R.n_rows
+    N, K = dh.shape[-1], W.shape[-1]
+    code, ldd, actc = _row_code(dt), _rows(dh, "dh", rows, N, dt, dev), _act(act)
+    gu_ptr, ldgu, packed = _kept(gu, rows, N, dt, dev)
+    ldw, lde = _weights(W, "W", R.n_keys, 2 * N, K, dt, dev)
     if isinstance(xs, Rows8):
-        xs = spmm_unpack_rows(xs, _empty(dh, (xs.rows, xs.cols), dh.dtype, stream), stream=stream)
-    return dgu, dxs, spmm_experts_dw(R, dgu, xs, stream=stream)
+        if (xs.rows, xs.cols, xs.device) != (rows, K, dev):
+            raise ValueError(f"xs must hold {rows} x {K} values on {dev}")
+        xs_ptr, ldx, xs8, need = None, K, xs._ref, spmm_experts_gated_grad_workspace_size(R, K, True)
+    else:
+        xs_ptr, ldx, xs8, need = xs.data_ptr(), _rows(xs, "xs", rows, K, dt, dev), None, 0
+    dgu, dxs = _empty(dh, (rows, 2 * N), dt, stream), _empty(dh, (rows, K), dt, stream)
+    dW = _empty(dh, (R.n_keys, 2 * N, K), dt, stream)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dh, stream)
+    _lib.call("spmm_experts_gated_grad", R._ref, dh.data_ptr(), ldd, xs_ptr, ldx, xs8, W.data_ptr(), ldw, lde, gu_ptr, ldgu,
+              packed, N, K, code, actc, dgu.data_ptr(), 2 * N, dxs.data_ptr(), K, dW.data_ptr(), K, 2 * N * K, ws_ptr, ws_bytes,
+              _handle(stream, dev))
+    return dgu, dxs, dW

@@ -822,6 +822,25 @@ spmm_status check_packed(const spmm_rows8_t* P, const spmm_route_t* R, int64_t N
 
 bool bad_act(int32_t act) { return act != SPMM_ACT_SILU && act != SPMM_ACT_GELU && act != SPMM_ACT_GELU_TANH; }
 
+spmm_status check_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                             const spmm_rows8_t* packed, int64_t N, int32_t dtype, int32_t act, const void* dgu,
+                             int64_t lddgu, const void* h, int64_t ldh) {
+    spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (dtype != SPMM_BF16 && dtype != SPMM_F16) return SPMM_ERR_DTYPE;
+    if (N <= 0 || N % 16) return SPMM_ERR_SHAPE;
+    if (N >= kDimLimit / 4 || bad_act(act)) return SPMM_ERR_UNSUPPORTED;
+    if (bad_pitch(lddh, N) || bad_pitch(lddgu, 2 * N) || lddh % 8 || lddgu % 8) return SPMM_ERR_SHAPE;
+    if (h && (bad_pitch(ldh, N) || ldh % 8)) return SPMM_ERR_SHAPE;
+    if (gu && (bad_pitch(ldgu, 2 * N) || ldgu % 8)) return SPMM_ERR_SHAPE;
+    if (packed && (st = check_packed(packed, R, N)) != SPMM_OK) return st;
+    if (gu && packed) return SPMM_ERR_UNSUPPORTED;
+    if (R->T == 0) return SPMM_OK;
+    if (!R->offsets || !dh || !dgu || (!gu && !packed)) return SPMM_ERR_NULL;
+    if (!aligned16(dh) || !aligned16(gu) || !aligned16(dgu) || !aligned16(h)) return SPMM_ERR_SHAPE;
+    return SPMM_OK;
+}
+
 spmm_status check_topk(int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k, int32_t renorm, const void* ids,
                        int32_t id_bytes) {
     if (!dtype_row(dtype) || (id_bytes != 4 && id_bytes != 8)) return SPMM_ERR_DTYPE;
@@ -906,21 +925,55 @@ spmm_status spmm_experts_gated(const spmm_route_t* R, const void* xs, int64_t ld
 spmm_status spmm_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
                             const spmm_rows8_t* packed, int64_t N, int32_t dtype, int32_t act, void* dgu,
                             int64_t lddgu, void* h, int64_t ldh, spmm_stream_t stream) {
-    spmm_status st = check_route(R, false);
-    if (st != SPMM_OK) return st;
-    if (dtype != SPMM_BF16 && dtype != SPMM_F16) return SPMM_ERR_DTYPE;
-    if (N <= 0 || N % 16) return SPMM_ERR_SHAPE;
-    if (N >= kDimLimit / 4 || bad_act(act)) return SPMM_ERR_UNSUPPORTED;
-    if (bad_pitch(lddh, N) || bad_pitch(lddgu, 2 * N) || lddh % 8 || lddgu % 8) return SPMM_ERR_SHAPE;
-    if (h && (bad_pitch(ldh, N) || ldh % 8)) return SPMM_ERR_SHAPE;
-    if (gu && (bad_pitch(ldgu, 2 * N) || ldgu % 8)) return SPMM_ERR_SHAPE;
-    if (packed && (st = check_packed(packed, R, N)) != SPMM_OK) return st;
-    if (R->T == 0) return SPMM_OK;
-    if (!R->offsets || !dh || !dgu || (!gu && !packed)) return SPMM_ERR_NULL;
-    if (gu && packed) return SPMM_ERR_UNSUPPORTED;
-    if (!aligned16(dh) || !aligned16(gu) || !aligned16(dgu) || !aligned16(h)) return SPMM_ERR_SHAPE;
+    const spmm_status st = check_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, h, ldh);
+    if (st != SPMM_OK || R->T == 0) return st;
     return launch_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, h, ldh,
                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t* R, int64_t K, int32_t packed_rows,
+                                                   size_t* bytes) {
+    if (!bytes) return SPMM_ERR_NULL;
+    const spmm_status st = check_route(R, false);
+    if (st != SPMM_OK) return st;
+    if (K <= 0 || K % 8 || (packed_rows & ~1)) return SPMM_ERR_SHAPE;
+    if (K >= kDimLimit / 2) return SPMM_ERR_UNSUPPORTED;
+    *bytes = packed_rows ? static_cast<size_t>(R->T * R->k) * static_cast<size_t>(K) * 2 : 0;
+    return SPMM_OK;
+}
+
+spmm_status spmm_experts_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh, const void* xs, int64_t ldx,
+                                    const spmm_rows8_t* xs8, const void* W, int64_t ldw, int64_t lde, const void* gu,
+                                    int64_t ldgu, const spmm_rows8_t* packed, int64_t N, int64_t K, int32_t dtype,
+                                    int32_t act, void* dgu, int64_t lddgu, void* dxs, int64_t lddx, void* dW,
+                                    int64_t lddw, int64_t ldde, void* workspace, size_t workspace_bytes,
+                                    spmm_stream_t stream) {
+    // every check of the three parts before the first of them is launched
+    spmm_status st = check_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, nullptr, 0);
+    if (st != SPMM_OK) return st;
+    if ((st = check_experts(R, lddgu, 2 * N, lddx, K, ldw, lde, 2 * N, K, dtype)) != SPMM_OK) return st;
+    if ((st = check_experts(R, lddgu, 2 * N, xs8 ? K : ldx, K, lddw, ldde, 2 * N, K, dtype)) != SPMM_OK) return st;
+    if (xs && xs8) return SPMM_ERR_UNSUPPORTED;
+    const int64_t rows = R->T * R->k;
+    if (xs8) {
+        if ((st = check_rows8(xs8)) != SPMM_OK) return st;
+        if (xs8->rows != rows || xs8->cols != K) return SPMM_ERR_SHAPE;
+        if (rows > 0 && (!xs8->q || !xs8->scale)) return SPMM_ERR_NULL;
+    }
+    if (!R->offsets || !dW || (rows > 0 && ((!xs && !xs8) || !W || !dxs))) return SPMM_ERR_NULL;
+    if (!aligned16(xs) || !aligned16(W) || !aligned16(dxs) || !aligned16(dW)) return SPMM_ERR_SHAPE;
+    const size_t need = xs8 ? static_cast<size_t>(rows) * static_cast<size_t>(K) * 2 : 0;
+    if (need && (!workspace || workspace_bytes < need)) return SPMM_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SPMM_ERR_SHAPE;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows > 0) {
+        st = launch_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, nullptr, 0, s);
+        if (st != SPMM_OK) return st;
+        st = launch_experts_rows(R, dgu, lddgu, W, ldw, lde, 2 * N, K, true, dtype, dxs, lddx, s);
+        if (st != SPMM_OK) return st;
+        if (xs8 && (st = launch_unpack_rows(xs8, workspace, K, dtype, s)) != SPMM_OK) return st;
+    }
+    return launch_experts_dw(R, dgu, lddgu, xs8 ? workspace : xs, xs8 ? K : ldx, 2 * N, K, dtype, dW, lddw, ldde, s);
 }
 
 }  // extern "C"

@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(accf_bar(acc), aph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
                 tc_fence_after();
             }
-        // Halves of the tile for dw; of the live columns, in chunks of 32, for a row product, so that both
+            // Halves of the tile for dw; of the live columns, in chunks of 32, for a row product, so that both
             // warps of a quarter have work in a short tile (53 rows per expert, 2 x 528 x 1032: 15.8 us
             // against 18.3 us kept in 8 bits, 11.9 against 12.6 us kept not at all; plain 10.3 either way).
             const int mid = DW ? TILE / 2 : (w.live + 63) / 64 * 32;

@@ -32,3 +32,15 @@ def test_every_kernel_waits_for_its_predecessor(name):
     assert kernels
     for at in kernels:
         assert "grid_dep_wait()" in _block(code, code.index(")", code.index("const", at)))
+
+
+def test_gated_epilogue_reads_tmem_together():
+    """TMEM loads and transposing stores need whole warps, which come from spinning waits and one thread's stores."""
+    from tests.test_warp_convergence import _NEEDS, _body, _unsafe
+    code = _code("experts.cu")
+    body = _body(code, r"void store_gated\(")
+    loop = body[body.index("for (int c = c0"):]
+    assert re.search(_NEEDS, loop) and _unsafe(loop + loop, True) is None
+    assert _unsafe(_body(code, r"void store_plane\("), True) is None
+    for head in (r"void store_plane\(", r"void store_packed\("):
+        assert not re.search(r"\breturn\b[^;]*;\s*__syncwarp", _body(code, head))

@@ -5,7 +5,7 @@ import pytest
 
 from tests.test_onehot_abi import _route
 
-NULL, SHAPE, DTYPE, UNSUPPORTED = 1, 2, 3, 8
+NULL, SHAPE, DTYPE, WORKSPACE, UNSUPPORTED = 1, 2, 3, 5, 8
 BF16, F16, I8, F32 = 0, 1, 2, 5
 
 
@@ -124,3 +124,33 @@ def test_gated_grad(L):
                 dict(gu=None, P=_rows8(ldq=80, q=18))):
         assert call(**bad) == SHAPE, bad
     assert call(act=9) == UNSUPPORTED and call(P=_rows8()) == UNSUPPORTED and call(gu=None, P=_rows8(q=None)) == NULL
+
+
+def test_experts_gated_grad(L):
+    f = L.spmm_experts_gated_grad
+    N, K = 32, 64
+    ok = dict(R=_route(), dh=16, lddh=N, xs=16, ldx=K, xs8=None, W=16, ldw=K, lde=2 * N * K, gu=16, ldgu=2 * N, P=None, N=N, K=K,
+              dt=BF16, act=0, dgu=16, lddgu=2 * N, dxs=16, lddx=K, dW=16, lddw=K, ldde=2 * N * K, ws=None, wsb=0)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return f(*(a[n] for n in ok), None)
+
+    x8 = _rows8(cols=K, ldq=K)
+    for name in ("R", "dh", "xs", "W", "gu", "dgu", "dxs", "dW"):
+        assert call(**{name: None}) == NULL, name
+    assert call(dt=F32) == DTYPE
+    for bad in (dict(N=24), dict(K=60), dict(lddh=24), dict(ldx=56), dict(ldx=68), dict(ldw=56), dict(lde=2 * N * K - 8),
+                dict(ldgu=56), dict(lddgu=56), dict(lddx=60), dict(lddw=60), dict(ldde=2 * N * K - 8), dict(xs=24), dict(W=24),
+                dict(dxs=24), dict(dW=24), dict(gu=24), dict(dh=24), dict(dgu=24), dict(xs=None, xs8=_rows8(rows=19)),
+                dict(xs=None, xs8=_rows8(cols=48)), dict(xs=None, xs8=x8, ws=24, wsb=1 << 20)):
+        assert call(**bad) == SHAPE, bad
+    assert call(xs8=x8) == UNSUPPORTED and call(P=_rows8()) == UNSUPPORTED and call(act=5) == UNSUPPORTED
+    assert call(xs=None, xs8=x8) == WORKSPACE and call(xs=None, xs8=x8, ws=16, wsb=20 * K * 2 - 1) == WORKSPACE
+    assert call(xs=None, xs8=_rows8(cols=K, ldq=K, q=None), ws=16, wsb=1 << 20) == NULL
+    n = ctypes.c_size_t(0)
+    size = L.spmm_experts_gated_grad_workspace_size
+    assert size(_route(), K, 1, ctypes.byref(n)) == 0 and n.value == 20 * K * 2
+    assert size(_route(), K, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert size(_route(), K, 2, ctypes.byref(n)) == SHAPE and size(_route(), 60, 1, ctypes.byref(n)) == SHAPE
+    assert size(_route(), K, 1, None) == NULL and size(None, K, 1, ctypes.byref(n)) == NULL

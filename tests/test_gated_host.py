@@ -24,7 +24,7 @@ def _R(T=5, k=2, E=3):
 
 def test_every_wrapper_asks_for_the_handle():
     for f in (spmm.spmm_topk, spmm.spmm_topk_grad, spmm.spmm_pack_rows, spmm.spmm_unpack_rows, spmm.spmm_experts_gated,
-              spmm.spmm_gated_grad):
+              spmm.spmm_gated_grad, spmm.spmm_experts_gated_grad):
         assert "_handle(stream, " in inspect.getsource(f), f.__name__
 
 
@@ -106,3 +106,13 @@ def test_gated_arguments():
         spmm.spmm_gated_grad(R, dh, spmm.Rows8(10, 48, torch.bfloat16, _cuda((10, 48), torch.int8), _cuda((10, 3), torch.uint8)))
     with pytest.raises(TypeError, match="gu must be"):
         spmm.spmm_gated_grad(R, dh, _cuda((10, 96), torch.float16))
+    gu = _cuda((10, 96))
+    with pytest.raises(ValueError, match="xs must be"):
+        spmm.spmm_experts_gated_grad(R, dh, _cuda((10, 63)), W, gu)
+    with pytest.raises(ValueError, match="xs must hold"):
+        spmm.spmm_experts_gated_grad(R, dh, spmm.Rows8(10, 48, torch.bfloat16, _cuda((10, 48), torch.int8), _cuda((10, 3), torch.uint8)),
+                                     W, gu)
+    with pytest.raises(ValueError, match="W must be"):
+        spmm.spmm_experts_gated_grad(R, dh, xs, _cuda((3, 80, 64)), gu)
+    with pytest.raises(ValueError, match="gu must be"):
+        spmm.spmm_experts_gated_grad(R, dh, xs, W, _cuda((10, 64)))
