@@ -13,7 +13,9 @@
  * ("SlideSparse", abstract) and a Reverse Cuthill-McKee permutation before
  * BCSR ("SMaT", abstract).  SDDMM samples a dense product at a CSR pattern.
  * One-hot matrices (tokens by expert, tokens by vocabulary row) are stored by
- * their sorted rows (spmm_route_t) and multiplied by the one-hot operators.
+ * their sorted rows (spmm_route_t) and multiplied by the one-hot operators; the
+ * gated experts' operators (router, gated feed-forward block, rows in 8 bits) stand
+ * around them.
  *
  * Conventions shared by every entry point
  *   - All matrix pointers are DEVICE pointers owned by the caller.  The library
@@ -75,7 +77,7 @@ typedef enum {
  * E5M2: exponent bias 15, IEEE-style infinities and NaN), the FP8 that the
  * pages pair with 2:4 sparse tensor cores ("Spense", abstract, on the "sparse
  * FP4 GEMM" search page: B200 with FP8 precision). */
-/* SPMM_F32: rows of the one-hot operators only (spmm_dispatch and below). */
+/* SPMM_F32: rows of the one-hot operators and below only (from spmm_dispatch on). */
 typedef enum { SPMM_BF16 = 0, SPMM_F16 = 1, SPMM_I8 = 2, SPMM_E4M3 = 3, SPMM_E5M2 = 4, SPMM_F32 = 5 } spmm_dtype;
 
 /* Bits of the sticky device error word. */
@@ -597,8 +599,9 @@ SPMM_API spmm_status spmm_experts_dw(const spmm_route_t *R, const void *dys, int
 
 /* The router: for each token t the k largest of its E logits (row pitch ldl; bf16,
  * fp16 or fp32), in descending order, equal ones by ascending index.  ids[T][k]
- * (id_bytes 4 or 8 each) are their indices, w[T][k] fp32 their weights: with renorm = 1 the softmax
- * over the chosen logits, with renorm = 0 their entries of the softmax over all E.
+ * (id_bytes 4 or 8 each) are their indices, w[T][k] fp32 their weights: with renorm
+ * = 1 the softmax over the chosen logits, with renorm = 0 their entries of the
+ * softmax over all E.
  * A logit of -infinity is never chosen: a token with fewer than k others gets id -1
  * (a dropped choice of spmm_build_route) and weight 0 in its last places.  NaN ranks
  * above every number and makes the token's weights NaN, as +infinity does.
@@ -609,9 +612,9 @@ SPMM_API spmm_status spmm_topk(const void *logits, int64_t T, int64_t E, int64_t
 /* Gradient of spmm_topk's weights for the logits, from its ids and w and the
  * gradient dw[T][k] (fp32) of w: dlogits[t][e] = sum over j with ids[t][j] = e of
  * w_j dw_j, less p_e sum_i w_i dw_i, where p_e is the softmax over the chosen (renorm
- * = 1: the w_j, zero elsewhere, and logits may be null) or over all E.  Every entry is
- * written; a negative id is a dropped choice, whose w and dw do not count; an id >= E is dropped too and
- * sets SPMM_DEVERR_INDEX.  dlogits has the logits' type. */
+ * = 1: the w_j, zero elsewhere, and logits may be null) or over all E.  Every entry
+ * is written; a negative id is a dropped choice, whose w and dw do not count; an id
+ * >= E is dropped too and sets SPMM_DEVERR_INDEX.  dlogits has the logits' type. */
 SPMM_API spmm_status spmm_topk_grad(const void *logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k,
                                     int32_t renorm, const void *ids, int32_t id_bytes, const float *w,
                                     const float *dw, void *dlogits, int64_t ldd, spmm_stream_t stream);
@@ -629,10 +632,10 @@ SPMM_API spmm_status spmm_unpack_rows(const spmm_rows8_t *P, void *out, int64_t 
  *   [g u] = W[e] xs[p] (fp32 sums),   h[p] = act(g) u,
  * rounded once.  A training step keeps [g u] for the way back: rounded to the rows'
  * type in gu (T k x 2 N, row pitch ldgu; null: not kept), or in 8 bits straight
- * from the sums in *packed (rows = T k, cols = 2 N; null: not kept); not both. Rows
+ * from the sums in *packed (rows = T k, cols = 2 N; null: not kept); not both.  Rows
  * past the kept places are written as zeros (scale 1).  Types, alignment and limits
- * as for spmm_experts with 2 N features; N % 16 == 0; packed->q 16-byte aligned with ldq %
- * 16 == 0. */
+ * as for spmm_experts with 2 N features; N % 16 == 0; packed->q 16-byte aligned,
+ * packed->ldq % 16 == 0.  h does not depend on what is kept. */
 SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, int64_t ldx, const void *W,
                                         int64_t ldw, int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act,
                                         void *h, int64_t ldh, void *gu, int64_t ldgu, const spmm_rows8_t *packed,
@@ -640,10 +643,10 @@ SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, i
 /* Gradient of the activation and the product, from the kept [g u] (gu, or packed;
  * exactly one of them) and the gradient dh of h:
  *   dgu[p] = [dh u act'(g), dh act(g)]  (T k x 2 N),
- * and, where h is not null, h[p] = act(g) u again (T k x N), which the gradient of the projection after
- * it needs.  Rows past the kept places are written as zeros and never read.  bf16 or
- * fp16; N % 16 == 0, pitches multiples of 8 (packed->ldq of 16) and pointers 16-byte
- * aligned. */
+ * and, where h is not null, h[p] = act(g) u again (T k x N), which the gradient of
+ * the projection after it needs.  Rows past the kept places are written as zeros and
+ * never read into a result.  bf16 or fp16; N % 16 == 0, pitches multiples of 8
+ * (packed->ldq of 16) and pointers 16-byte aligned. */
 SPMM_API spmm_status spmm_gated_grad(const spmm_route_t *R, const void *dh, int64_t lddh, const void *gu, int64_t ldgu,
                                      const spmm_rows8_t *packed, int64_t N, int32_t dtype, int32_t act, void *dgu,
                                      int64_t lddgu, void *h, int64_t ldh, spmm_stream_t stream);
@@ -654,9 +657,9 @@ SPMM_API spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t *
 /* The whole way back of spmm_experts_gated: dgu as by spmm_gated_grad, then
  *   dxs[p] = W[e]^T dgu[p] (T k x K),   dW[e] = sum_p dgu[p] xs[p]^T (2 N x K)
  * from dgu as it was rounded.  The rows of the forward pass are given as they were
- * (xs) or as an 8-bit checkpoint of them (xs8, T k x K, read back exactly); exactly one of
- * them.  W and dW have their own pitches.  Requirements as for spmm_experts_dx,
- * spmm_experts_dw and spmm_gated_grad; workspace 16-byte aligned. */
+ * (xs) or as an 8-bit checkpoint of them (xs8, T k x K, read back in the rows' type);
+ * exactly one of them.  W and dW have their own pitches.  Requirements as for
+ * spmm_experts_dx, spmm_experts_dw and spmm_gated_grad; workspace 16-byte aligned. */
 SPMM_API spmm_status spmm_experts_gated_grad(const spmm_route_t *R, const void *dh, int64_t lddh, const void *xs,
                                              int64_t ldx, const spmm_rows8_t *xs8, const void *W, int64_t ldw,
                                              int64_t lde, const void *gu, int64_t ldgu, const spmm_rows8_t *packed,

@@ -965,8 +965,8 @@ def spmm_experts_gated(R: Route, xs: torch.Tensor, W: torch.Tensor, act: str = "
     """h[p] = act(g) u with [g u] = W[e] xs[p] for the rows p of expert e: W is E x 2N x
     K, the gate's N rows before the up projection's; act is silu, gelu or gelu_tanh;
     zero rows past the kept places.  bf16 or fp16, N a multiple of 16.  A training step
-    keeps [g u] (T k x 2N) for spmm_experts_gated_grad: save="rows" returns (h, gu) with gu of xs's
-    type, save="packed" (h, Rows8) with gu in 8 bits."""
+    keeps [g u] (T k x 2N) for spmm_experts_gated_grad: save="rows" returns (h, gu)
+    with gu of xs's type, save="packed" (h, Rows8) with gu in 8 bits."""
     dev, dt, rows = R.device, xs.dtype, R.n_rows
     N, K = W.shape[-2] // 2, W.shape[-1]
     code, ldx, actc = _row_code(dt), _rows(xs, "xs", rows, K, dt, dev), _act(act)
@@ -988,8 +988,8 @@ def spmm_experts_gated(R: Route, xs: torch.Tensor, W: torch.Tensor, act: str = "
 def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: bool = False,
                     out: Optional[torch.Tensor] = None, stream=None):
     """Gradient of h = act(g) u for [g u], from the kept gu (rows or Rows8) and the
-    gradient dh: dgu (T k x 2N), zero rows past the kept places.  with_h returns (dgu, h):
-    h again, which the gradient of the projection after it needs."""
+    gradient dh: dgu (T k x 2N), zero rows past the kept places.  with_h returns (dgu,
+    h): h again, which the gradient of the projection after it needs."""
     dev, dt, rows = R.device, dh.dtype, R.n_rows
     N = dh.shape[-1]
     code, ldd, actc = _row_code(dt), _rows(dh, "dh", rows, N, dt, dev), _act(act)
@@ -1007,8 +1007,8 @@ def spmm_gated_grad(R: Route, dh: torch.Tensor, gu, act: str = "silu", with_h: b
 def _kept(gu, rows: int, N: int, dtype, device):
     """(address, pitch, 8-bit struct) of what a forward call kept of [g u]."""
     if isinstance(gu, Rows8):
-        if (gu.rows, gu.cols, gu.device) != (rows, 2 * N, device):
-            raise ValueError(f"gu must hold {rows} x {2 * N} values on {device}")
+        if (gu.rows, gu.cols, gu.dtype, gu.device) != (rows, 2 * N, dtype, device):
+            raise ValueError(f"gu must hold {rows} x {2 * N} values of {dtype} on {device}")
         return None, 2 * N, gu._ref
     return gu.data_ptr(), _rows(gu, "gu", rows, 2 * N, dtype, device), None
 
@@ -1030,8 +1030,8 @@ def spmm_experts_gated_grad(R: Route, dh: torch.Tensor, xs, W: torch.Tensor, gu,
     gu_ptr, ldgu, packed = _kept(gu, rows, N, dt, dev)
     ldw, lde = _weights(W, "W", R.n_keys, 2 * N, K, dt, dev)
     if isinstance(xs, Rows8):
-        if (xs.rows, xs.cols, xs.device) != (rows, K, dev):
-            raise ValueError(f"xs must hold {rows} x {K} values on {dev}")
+        if (xs.rows, xs.cols, xs.dtype, xs.device) != (rows, K, dt, dev):
+            raise ValueError(f"xs must hold {rows} x {K} values of {dt} on {dev}")
         xs_ptr, ldx, xs8, need = None, K, xs._ref, spmm_experts_gated_grad_workspace_size(R, K, True)
     else:
         xs_ptr, ldx, xs8, need = xs.data_ptr(), _rows(xs, "xs", rows, K, dt, dev), None, 0
