@@ -14,8 +14,13 @@ using namespace gated;
 
 // ---------------------------------------------------------------- forward, very few rows
 // Dot products on CUDA cores: a warp takes one feature, its gate row and its up
-// row, with up to four rows of an expert; 16 warps a group of 16 features.
-constexpr int kVecWarps = 16, kVecRows = 4;
+// row, with up to four rows of an expert, and has both sums in every lane at the
+// end.  Where [g u] is kept in 8 bits a CTA's 16 warps are a group of 16 features
+// and meet in shared memory; else 8 warps that do not wait for one another.  One
+// token with 2 of 8 experts (2 x 2048 x 4096, 67 MB) 13.0 us, with 8 of 64 (2 x 768 x 2048,
+// 50 MB) 10.7 us, with 8 of 128 (2 x 1280 x 4096, 168 MB) 28 us: launch, ramp and the
+// chain of offsets, weights and shuffles, then HBM.
+constexpr int kVecRows = 4;
 
 struct VecArgs {
     const int32_t* offsets;
@@ -26,12 +31,15 @@ struct VecArgs {
     GatedOut out;
 };
 
+// sums[half][row] of the gate row wg and the up row wu with C rows of x.
 template <typename T, int C>
 __device__ __forceinline__ void dot_rows(const VecArgs& a, const T* wg, const T* wu, const T* x, int lane,
-                                         float (*sums)[kVecRows][kVecWarps], int warp) {
+                                         float (&sums)[2][kVecRows]) {
     using V = Vec<T, 8>;
     float acc[2][C] = {};
-    constexpr int kFlight = 2;  // loads per weight row before their sums
+    // Loads per weight row before their sums: four keep a lone row's weights coming
+    // (two: 13.0 -> 14.1, 28 -> 30.5 us), with more rows their registers are sums.
+    constexpr int kFlight = C == 1 ? 4 : 2;
     for (int k0 = lane * 8; k0 < a.K; k0 += 256 * kFlight) {
         uint4 r[2][kFlight];
 #pragma unroll
@@ -66,27 +74,25 @@ __device__ __forceinline__ void dot_rows(const VecArgs& a, const T* wg, const T*
             acc[0][c] += __shfl_xor_sync(0xffffffffu, acc[0][c], s);
             acc[1][c] += __shfl_xor_sync(0xffffffffu, acc[1][c], s);
         }
-        if (lane == 0) {
-            sums[0][c][warp] = acc[0][c];
-            sums[1][c][warp] = acc[1][c];
-        }
+        sums[0][c] = acc[0][c];
+        sums[1][c] = acc[1][c];
     }
 }
 
-// Grid (16 features, sorted place): the CTAs of an expert's first place and of
-// every fourth after it take up to four of its rows, the others leave; places of
-// dropped choices are zeroed.
-// MOST: rows of an expert that a CTA takes, 1 for a single token, whose choices are
-// experts of their own: 42 registers, so that three CTAs are resident instead of two and 384 of
-// them (8 experts of 768 features, 2048 deep) run at once: 10.3 us against 12.4 us.
-template <typename T, int ACT, int MOST>
-__global__ void __launch_bounds__(kVecWarps * 32, MOST == 1 ? 3 : 2) gated_vec_kernel(const VecArgs a) {
-    __shared__ float sums[2][kVecRows][kVecWarps];  // gate and up
+// Grid (features, sorted place): the CTAs of an expert's first place and of every
+// fourth after it take up to four of its rows, the others leave; places of dropped
+// choices are zeroed.
+template <bool PACKED>
+constexpr int kVecWarps = PACKED ? 16 : 8;
+template <typename T, int ACT, bool PACKED>
+__global__ void __launch_bounds__(kVecWarps<PACKED> * 32, 32 / kVecWarps<PACKED>)
+    gated_vec_kernel(const VecArgs a) {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = blockIdx.y, n0 = blockIdx.x * kVecWarps;
+    const int p = blockIdx.y, n = blockIdx.x * kVecWarps<PACKED> + warp;
     int rows = 1;
+    float sums[2][kVecRows] = {};
     const bool live = p < a.offsets[a.E];
     if (live) {
         int lo = 0, hi = a.E;  // the last e with offsets[e] <= p, 32 probes at a time
@@ -96,37 +102,52 @@ __global__ void __launch_bounds__(kVecWarps * 32, MOST == 1 ? 3 : 2) gated_vec_k
             lo += step * (31 - __clz(le));
             hi = min(hi, lo + step);
         }
-        if ((p - a.offsets[lo]) % MOST) return;
-        rows = min(MOST, a.offsets[lo + 1] - p);
+        if ((p - a.offsets[lo]) % kVecRows) return;
+        rows = min(kVecRows, a.offsets[lo + 1] - p);
         const T* x = static_cast<const T*>(a.xs) + p * a.ldx;
-        const T* wg = static_cast<const T*>(a.W) + lo * a.lde + (n0 + warp) * a.ldw;
+        const T* wg = static_cast<const T*>(a.W) + lo * a.lde + n * a.ldw;
         const T* wu = wg + a.N * a.ldw;
-        if (MOST == 1 || rows == 1)
-            dot_rows<T, 1>(a, wg, wu, x, lane, sums, warp);
+        if (rows == 1)
+            dot_rows<T, 1>(a, wg, wu, x, lane, sums);
         else if (rows == 2)
-            dot_rows<T, 2>(a, wg, wu, x, lane, sums, warp);
+            dot_rows<T, 2>(a, wg, wu, x, lane, sums);
         else if (rows == 3)
-            dot_rows<T, 3>(a, wg, wu, x, lane, sums, warp);
+            dot_rows<T, 3>(a, wg, wu, x, lane, sums);
         else
-            dot_rows<T, 4>(a, wg, wu, x, lane, sums, warp);
+            dot_rows<T, 4>(a, wg, wu, x, lane, sums);
     }
-    __syncthreads();
-    if (threadIdx.x >= 2 * kVecRows * 16) return;  // whole warps: half, row, feature
-    const int f = threadIdx.x & 15, c = threadIdx.x >> 4 & 3, half = threadIdx.x >> 6;
-    const bool in = c < rows;
-    const float v = live && in ? sums[half][c][f] : 0.f;
-    const int64_t row = p + c;
-    const int n = n0 + f;
-    if (half == 0 && in)
-        static_cast<T*>(a.out.h)[row * a.out.ldh + n] = from_f32<T>(live ? act<ACT>(v) * sums[1][c][f] : 0.f);
-    if (a.out.gu && in) static_cast<T*>(a.out.gu)[row * a.out.ldgu + half * a.N + n] = from_f32<T>(v);
-    if (a.out.q) {
+    // lane c writes row c
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int c = 0; c < kVecRows; ++c) {
+        g = lane == c ? sums[0][c] : g;
+        u = lane == c ? sums[1][c] : u;
+    }
+    if (lane < rows) {
+        const int64_t row = p + lane;
+        static_cast<T*>(a.out.h)[row * a.out.ldh + n] = from_f32<T>(live ? act<ACT>(g) * u : 0.f);
+        if (!PACKED && a.out.gu) {
+            T* gu = static_cast<T*>(a.out.gu) + row * a.out.ldgu + n;
+            gu[0] = from_f32<T>(g);
+            gu[a.N] = from_f32<T>(u);
+        }
+    }
+    if constexpr (PACKED) {
+        __shared__ float all[2][kVecRows][16];  // gate and up
+        if (lane < kVecRows) {
+            all[0][lane][warp] = g;
+            all[1][lane][warp] = u;
+        }
+        __syncthreads();
+        if (threadIdx.x >= 2 * kVecRows * 16) return;  // whole warps: half, row, feature
+        const int f = threadIdx.x & 15, c = threadIdx.x >> 4 & 3, half = threadIdx.x >> 6;
+        const float v = all[half][c][f];
         uint32_t code = magnitude_code(v);
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, d));
         const uint32_t b = scale_byte(code);
-        const int64_t col = static_cast<int64_t>(half) * a.N + n;
-        if (in) {
+        const int64_t row = p + c, col = static_cast<int64_t>(half) * a.N + blockIdx.x * 16 + f;
+        if (c < rows) {
             uint32_t q[1];
             quantise({v}, b, q);
             a.out.q[row * a.out.ldq + col] = static_cast<int8_t>(q[0]);
@@ -235,13 +256,17 @@ cudaError_t launch_grad(const GradArgs& a, int64_t blocks, int32_t act, cudaStre
     return launch_grad_of<T, SPMM_ACT_GELU_TANH, PACKED>(a, blocks, s);
 }
 
-template <typename T, int MOST>
+template <typename T, bool PACKED>
+cudaError_t launch_vec_of(const VecArgs& a, int64_t rows, int32_t act, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(a.N / kVecWarps<PACKED>), static_cast<unsigned>(rows));
+    return launch_rows(act == SPMM_ACT_SILU   ? gated_vec_kernel<T, SPMM_ACT_SILU, PACKED>
+                       : act == SPMM_ACT_GELU ? gated_vec_kernel<T, SPMM_ACT_GELU, PACKED>
+                                              : gated_vec_kernel<T, SPMM_ACT_GELU_TANH, PACKED>,
+                       grid, kVecWarps<PACKED> * 32, s, a);
+}
+template <typename T>
 cudaError_t launch_vec(const VecArgs& a, int64_t rows, int32_t act, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.N / kVecWarps), static_cast<unsigned>(rows));
-    return launch_rows(act == SPMM_ACT_SILU   ? gated_vec_kernel<T, SPMM_ACT_SILU, MOST>
-                       : act == SPMM_ACT_GELU ? gated_vec_kernel<T, SPMM_ACT_GELU, MOST>
-                                              : gated_vec_kernel<T, SPMM_ACT_GELU_TANH, MOST>,
-                       grid, kVecWarps * 32, s, a);
+    return a.out.q ? launch_vec_of<T, true>(a, rows, act, s) : launch_vec_of<T, false>(a, rows, act, s);
 }
 
 }  // namespace
@@ -253,12 +278,7 @@ spmm_status launch_experts_gated_vec(const spmm_route_t* R, const void* xs, int6
                     static_cast<int32_t>(K), out};
     const int64_t rows = R->T * R->k;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
-    cudaError_t e;
-    if (R->T == 1)
-        e = dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16, 1>(a, rows, act, s) : launch_vec<__half, 1>(a, rows, act, s);
-    else
-        e = dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16, kVecRows>(a, rows, act, s)
-                               : launch_vec<__half, kVecRows>(a, rows, act, s);
+    const cudaError_t e = dtype == SPMM_BF16 ? launch_vec<__nv_bfloat16>(a, rows, act, s) : launch_vec<__half>(a, rows, act, s);
     trace_end(SPMM_KERNEL_EXPERTS, s);
     return cuda_status(e);
 }
