@@ -74,6 +74,11 @@ constexpr uint64_t wait_limit_ns(int64_t most_depth) {
 // instead of six (64 tokens x 8 of 128 experts, 1536 x 4096: 226 us against 240).
 constexpr int kFewRows = 16;
 constexpr int kVecMost = 16;   // rows in all up to which the forward product runs on CUDA cores
+// .. and, for the gated block, where there are no more rows than experts, so that few
+// share one.  CUDA cores against this kernel, us: 32 rows, 32 experts, 2 x 1024 x 4096 55 / 66;
+// 64 rows, 64 experts, 2 x 768 x 2048 42 / 47; 64 of 256, 2 x 512 x 2048 37 / 41; 64 of 128,
+// 2 x 1280 x 4096 157 / 157; with more rows than experts (48, 32) 72 / 69, (48, 16) 55 / 45.
+constexpr int kVecSpread = 64;
 constexpr int kDwFewRows = 4;  // rows per expert up to which dw runs on CUDA cores
 
 struct ExpertArgs {
@@ -1232,7 +1237,8 @@ spmm_status launch_experts_gated(const spmm_route_t* R, const void* xs, int64_t 
                                  int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act, const GatedOut& out,
                                  cudaStream_t s) {
     const int64_t n = R->T * R->k;
-    if (n <= kVecMost) return launch_experts_gated_vec(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, s);
+    if (n <= kVecMost || (n <= kVecSpread && n <= R->n_keys))
+        return launch_experts_gated_vec(R, xs, ldx, W, ldw, lde, N, K, dtype, act, out, s);
     const DeviceInfo* dev = device_info();
     if (!dev) return SPMM_ERR_CUDA;
     const GateArgs g{static_cast<int32_t>(N), act};
