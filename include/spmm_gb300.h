@@ -635,7 +635,7 @@ SPMM_API spmm_status spmm_unpack_rows(const spmm_rows8_t *P, void *out, int64_t 
  * from the sums in *packed (rows = T k, cols = 2 N; null: not kept); not both.  Rows
  * past the kept places are written as zeros (scale 1).  Types, alignment and limits
  * as for spmm_experts with 2 N features; N % 16 == 0; packed->q 16-byte aligned,
- * packed->ldq % 16 == 0.  h does not depend on what is kept. */
+ * packed->ldq % 16 == 0. */
 SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, int64_t ldx, const void *W,
                                         int64_t ldw, int64_t lde, int64_t N, int64_t K, int32_t dtype, int32_t act,
                                         void *h, int64_t ldh, void *gu, int64_t ldgu, const spmm_rows8_t *packed,

@@ -49,8 +49,22 @@ namespace {
 using namespace ptx;
 
 // What a kernel computes: a plain product, or the gated block that keeps nothing, [g
-// u] in the rows' type, or [g u] in 8 bits.
-enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3 };
+// u] in the rows' type, or [g u] in 8 bits, the last for fp16 with its sums in halves.
+// Why halves: what an addition into an accumulator shifts out is cut off, not rounded,
+// which takes 3.3e-6 of their spread off sums of 4096 products (256 additions), always
+// towards zero; and a kept integer is another one where its sum lies that close to a
+// tie.  fp16 results, good to 2^-12, show it: the gradients of a training step (16382
+// rows, 2 x 1792 x 4096, tanh form) were off by 4.1e-4 of their norm where sums in
+// fp32 give 2.6e-4; bf16's, good to 2^-9, do not (1.7e-3 both).  So the halves of the
+// depth are summed in accumulators of their own and added in fp32: 3.2e-4.  Both
+// accumulators then belong to one unit.  The epilogue first folds them, the sum into
+// the second one, and gives the first back, so that the next unit's first half runs
+// beside the rest of it: 320 us against 305 with one sum.  Without the fold 372-418
+// us; three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns
+// takes nearly the time of one of 256).
+enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3, kGatedHalves = 4 };
+// The step at which the second half begins; there is one if that is below the steps.
+__host__ __device__ constexpr int second_half(int steps) { return (steps + 1) / 2; }
 
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half of the columns each
 constexpr int kMoreProducers = 4 + kEpiWarps;  // first warp of the second pair of producers
@@ -133,6 +147,8 @@ struct Gate<kGatedPacked> : GateArgs {
     uint8_t* scale;
     int64_t lds;
 };
+template <>
+struct Gate<kGatedHalves> : Gate<kGatedPacked> {};
 
 // A work unit: D rows m0.. and columns n0.. (row products: rows p0 + n0 ..) of
 // expert e, `nt` columns computed and `live` of them stored, `steps` stages.
@@ -405,11 +421,38 @@ __device__ __forceinline__ void store_gated(const ExpertArgs& a, const Gate<FORM
             store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, f0, in, row, live, g, lane, planes, turn);
             store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, x.features + f0, in, row, live, u, lane, planes, turn);
         }
-        if constexpr (FORM == kGatedPacked) {
+        if constexpr (FORM >= kGatedPacked) {
             store_packed(x, f0, in, row, live, g, lane, planes, turn);
             store_packed(x, x.features + f0, in, row, live, u, lane, planes, turn);
         }
     }
+}
+
+// The sum of both halves' accumulators (t and t2) into the second, for this warp's
+// lanes and columns [c0, c1); one half alone is copied.
+__device__ __forceinline__ void fold_halves(uint32_t t, uint32_t t2, int c0, int c1, bool both) {
+    for (int c = c0; c < c1; c += 32) {
+        uint32_t a[2][16], b[2][16];
+        __syncwarp();  // as in store_rows
+        tmem_ld16(t + c, a[0]);
+        tmem_ld16(t + c + 16, a[1]);
+        if (both) {
+            tmem_ld16(t2 + c, b[0]);
+            tmem_ld16(t2 + c + 16, b[1]);
+        }
+        tmem_ld_wait();
+        if (both) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    a[h][i] = __float_as_uint(__uint_as_float(a[h][i]) + __uint_as_float(b[h][i]));
+        }
+        tmem_st16(t2 + c, a[0]);
+        tmem_st16(t2 + c + 16, a[1]);
+    }
+    __syncwarp();  // a warp without columns comes from its wait
+    tmem_st_wait();
 }
 
 // The kept form of rows past the last expert's: zeros. Called by a warp per row.
@@ -419,7 +462,7 @@ __device__ __forceinline__ void clear_kept(const Gate<FORM>& x, int64_t p, int l
         uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(x.gu) + p * x.ldgu);
         for (int c = lane; c < x.features / 4; c += 32) row[c] = make_uint4(0, 0, 0, 0);
     }
-    if constexpr (FORM == kGatedPacked) {
+    if constexpr (FORM >= kGatedPacked) {
         uint4* row = reinterpret_cast<uint4*>(x.q + p * x.ldq);
         for (int c = lane; c < x.features / 8; c += 32) {
             row[c] = make_uint4(0, 0, 0, 0);
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
                    const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a,
                    const __grid_constant__ Gate<FORM> gate) {
-    constexpr bool DW = BMN;
+    constexpr bool DW = BMN, HALVES = FORM == kGatedHalves;
     using G = Ring<CG, TILE, DW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -698,16 +741,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : mbar_wait(acce_bar(acc), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)))
                 break;
             tc_fence_after();
-            const uint32_t d = tmem + static_cast<uint32_t>(acc * TILE);
+            uint32_t d = tmem + static_cast<uint32_t>(acc * TILE);
             const uint32_t idesc = idesc_f16(128 * CG, w.nt, a.bf16 != 0, AMN, BMN, false);
             // whole stages; the loop stays warp-uniform around the one issuing thread, which keeps the
             // descriptors in uniform registers
             const int whole = DW ? w.cnt / kDepth : w.steps;
+            const int half = HALVES ? second_half(w.steps) : -1;
             bool ready = whole > 0 && mbar_test_wait(full_bar(s), ph);
             for (int k = 0; k < whole; ++k) {
                 if (!ready && !mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
                     ok = false;
                     break;
+                }
+                if (HALVES && k == half) {  // the epilogue of the unit before has read the second accumulator
+                    if (!(CG == 2 ? mbar_wait_cluster(acce_bar(1), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)
+                                  : mbar_wait(acce_bar(1), aph ^ 1u, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT))) {
+                        ok = false;
+                        break;
+                    }
+                    d += TILE;
                 }
                 tc_fence_after();
                 const uint32_t so = static_cast<uint32_t>(s) * (G::kStage >> 4), empty = empty_bar(s);
@@ -720,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t a_lo = static_cast<uint32_t>(adesc0) + so, b_lo = static_cast<uint32_t>(bdesc0) + so;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma<CG>(d, a_lo + kAStep * kk, a_hi, b_lo + kBStep * kk, b_hi, idesc, (k | kk) != 0 ? 1u : 0u, issue);
+                    mma<CG>(d, a_lo + kAStep * kk, a_hi, b_lo + kBStep * kk, b_hi, idesc,
+                            (k | kk) != 0 && !(HALVES && k == half && kk == 0) ? 1u : 0u, issue);
                 if (lane == 0) commit<CG>(empty);
                 __syncwarp();
             }
@@ -754,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) commit<CG>(accf_bar(acc));
             __syncwarp();
-            acc ^= 1;
+            if (!HALVES) acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
         if (lane == 0) commit<CG>(done_bar);
@@ -813,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t aph = 0;
         while (next_unit()) {
             const int row0 = w.m0 + 128 * rank + 32 * q;
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * TILE);
+            uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * TILE);
             if (w.steps > 0) {
                 if (!mbar_wait(accf_bar(acc), aph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
                 tc_fence_after();
@@ -823,16 +876,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // against 18.3 us kept in 8 bits, 11.9 against 12.6 us kept not at all; plain 10.3 either way).
             const int mid = DW ? TILE / 2 : (w.live + 63) / 64 * 32;
             const int c0 = half ? mid : 0, c1 = half ? w.live : min(w.live, mid);
+            // this warp has read the accumulator
+            auto give_back = [&](int b) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive(acce_bar(b));
+                    else
+                        mbar_arrive_remote(map_shared(acce_bar(b), 0));
+                }
+                __syncwarp();
+            };
+            if constexpr (HALVES) {
+                fold_halves(t, t + TILE, c0, c1, second_half(w.steps) < w.steps);
+                give_back(0);
+                t += TILE;
+            }
             if constexpr (FORM != kPlain) {
                 auto store = [&](auto type, auto act) {
                     using T = decltype(type);
                     store_gated<T, decltype(act)::value, FORM>(a, gate, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
                 };
-                auto typed = [&](auto act) {
-                    if (a.bf16)
-                        store(__nv_bfloat16(), act);
+                auto typed = [&](auto act) {  // 8 bits: bf16 in one sum, fp16 in halves
+                    if (FORM == kGatedPacked || (FORM != kGatedHalves && a.bf16))
+                        store(std::conditional_t<FORM == kGatedHalves, __half, __nv_bfloat16>(), act);
                     else
-                        store(__half(), act);
+                        store(std::conditional_t<FORM == kGatedPacked, __nv_bfloat16, __half>(), act);
                 };
                 if (gate.act == SPMM_ACT_SILU)
                     typed(std::integral_constant<int, SPMM_ACT_SILU>());
@@ -851,16 +921,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_rows<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
             }
             if (w.steps == 0) continue;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (rank == 0)
-                    mbar_arrive(acce_bar(acc));
-                else
-                    mbar_arrive_remote(map_shared(acce_bar(acc), 0));
-            }
-            __syncwarp();
-            acc ^= 1;
+            give_back(HALVES ? 1 : acc);
+            if (!HALVES) acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
         if (lane == 0) bulk_wait<0>();  // this warp's stores have completed
@@ -1255,6 +1317,8 @@ spmm_status launch_experts_gated(const spmm_route_t* R, const void* xs, int64_t 
         if (!encode_tmap_2d(&x.tmKept, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.q, cols, rows, static_cast<uint64_t>(out.ldq), 16,
                             32, CU_TENSOR_MAP_SWIZZLE_NONE))
             return SPMM_ERR_CUDA;
+        if (dtype == SPMM_F16)
+            return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, Gate<kGatedHalves>{x}, dev, s);
         return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, x, dev, s);
     }
     return launch_gated(R, xs, ldx, W, ldw, lde, N, K, dtype, out.h, out.ldh, Gate<kGated>{g}, dev, s);

@@ -65,7 +65,7 @@ void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
 // First of the twelve slots of set_smem_attr_once that the experts' kernels take
-// (0-23 belong to the format kernels), and of the nine that their gated form takes.
+// (0-23 belong to the format kernels), and of the twelve that their gated form takes.
 enum : int { kSlotExperts = 24, kSlotGated = 36 };
 
 // Raise a kernel's dynamic shared memory limit once per device.

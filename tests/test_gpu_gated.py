@@ -86,7 +86,9 @@ def test_forward(dtype, pad, i):
     check(kept16, gu, mag, K, dtype, "gu")
     h8, kept8 = spmm.spmm_experts_gated(R, xs, W, act=name, save="packed")
     _check_packed(kept8, gu, mag, K)
-    assert torch.equal(h16, h) and torch.equal(h8, h)
+    assert torch.equal(h16, h)
+    _check_h(h8, gu, mag, K, N, name, dtype)
+    assert dtype == "f16" or torch.equal(h8, h)  # fp16 sums kept in 8 bits are formed in halves
     assert not kept16[kept:].any() and not kept8.q[kept:].any() and (kept8.scale[kept:] == 1).all()
     torch.cuda.synchronize()
     assert spmm.last_device_error() == 0
