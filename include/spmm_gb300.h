@@ -650,16 +650,18 @@ SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, i
 SPMM_API spmm_status spmm_gated_grad(const spmm_route_t *R, const void *dh, int64_t lddh, const void *gu, int64_t ldgu,
                                      const spmm_rows8_t *packed, int64_t N, int32_t dtype, int32_t act, void *dgu,
                                      int64_t lddgu, void *h, int64_t ldh, spmm_stream_t stream);
-/* Workspace bytes spmm_experts_gated_grad needs for rows kept in 8 bits: one row of
- * the rows' type per choice (0 for rows given as they are, packed_rows = 0). */
-SPMM_API spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t *R, int64_t K, int32_t packed_rows,
-                                                            size_t *bytes);
+/* Workspace bytes spmm_experts_gated_grad needs: for rows kept in 8 bits (packed_rows
+ * = 1) one row of the rows' type per choice, and where an expert has many rows and dW
+ * few tiles, fp32 sums of it (20 MB at most). */
+SPMM_API spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t *R, int64_t N, int64_t K,
+                                                            int32_t packed_rows, size_t *bytes);
 /* The whole way back of spmm_experts_gated: dgu as by spmm_gated_grad, then
  *   dxs[p] = W[e]^T dgu[p] (T k x K),   dW[e] = sum_p dgu[p] xs[p]^T (2 N x K)
  * from dgu as it was rounded.  The rows of the forward pass are given as they were
  * (xs) or as an 8-bit checkpoint of them (xs8, T k x K, read back in the rows' type);
- * exactly one of them.  W and dW have their own pitches.  Requirements as for
- * spmm_experts_dx, spmm_experts_dw and spmm_gated_grad; workspace 16-byte aligned. */
+ * exactly one of them.  W and dW have their own pitches.  Where dW has few tiles an
+ * expert's rows are summed in parts, joined in fp32 in a fixed order.  Requirements as
+ * for spmm_experts_dx, spmm_experts_dw and spmm_gated_grad; workspace 16-byte aligned. */
 SPMM_API spmm_status spmm_experts_gated_grad(const spmm_route_t *R, const void *dh, int64_t lddh, const void *xs,
                                              int64_t ldx, const spmm_rows8_t *xs8, const void *W, int64_t ldw,
                                              int64_t lde, const void *gu, int64_t ldgu, const spmm_rows8_t *packed,

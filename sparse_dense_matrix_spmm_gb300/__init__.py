@@ -1013,9 +1013,9 @@ def _kept(gu, rows: int, N: int, dtype, device):
     return gu.data_ptr(), _rows(gu, "gu", rows, 2 * N, dtype, device), None
 
 
-def spmm_experts_gated_grad_workspace_size(R: Route, K: int, packed_rows: bool) -> int:
+def spmm_experts_gated_grad_workspace_size(R: Route, N: int, K: int, packed_rows: bool) -> int:
     n = C.c_size_t(0)
-    _lib.call("spmm_experts_gated_grad_workspace_size", R._ref, K, 1 if packed_rows else 0, C.byref(n))
+    _lib.call("spmm_experts_gated_grad_workspace_size", R._ref, N, K, 1 if packed_rows else 0, C.byref(n))
     return n.value
 
 
@@ -1032,9 +1032,10 @@ def spmm_experts_gated_grad(R: Route, dh: torch.Tensor, xs, W: torch.Tensor, gu,
     if isinstance(xs, Rows8):
         if (xs.rows, xs.cols, xs.dtype, xs.device) != (rows, K, dt, dev):
             raise ValueError(f"xs must hold {rows} x {K} values of {dt} on {dev}")
-        xs_ptr, ldx, xs8, need = None, K, xs._ref, spmm_experts_gated_grad_workspace_size(R, K, True)
+        xs_ptr, ldx, xs8 = None, K, xs._ref
     else:
-        xs_ptr, ldx, xs8, need = xs.data_ptr(), _rows(xs, "xs", rows, K, dt, dev), None, 0
+        xs_ptr, ldx, xs8 = xs.data_ptr(), _rows(xs, "xs", rows, K, dt, dev), None
+    need = spmm_experts_gated_grad_workspace_size(R, N, K, xs8 is not None)
     dgu, dxs = _empty(dh, (rows, 2 * N), dt, stream), _empty(dh, (rows, K), dt, stream)
     dW = _empty(dh, (R.n_keys, 2 * N, K), dt, stream)
     ws, ws_ptr, ws_bytes = _workspace(workspace, need, dh, stream)

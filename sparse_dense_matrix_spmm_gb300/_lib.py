@@ -115,7 +115,7 @@ SIGNATURES = {
     "spmm_experts_gated": (I32, [C.POINTER(RouteT), P, I64, P, I64, I64, I64, I64, I32, I32, P, I64, P, I64,
                                  C.POINTER(Rows8T), P]),
     "spmm_gated_grad": (I32, [C.POINTER(RouteT), P, I64, P, I64, C.POINTER(Rows8T), I64, I32, I32, P, I64, P, I64, P]),
-    "spmm_experts_gated_grad_workspace_size": (I32, [C.POINTER(RouteT), I64, I32, C.POINTER(SZ)]),
+    "spmm_experts_gated_grad_workspace_size": (I32, [C.POINTER(RouteT), I64, I64, I32, C.POINTER(SZ)]),
     "spmm_experts_gated_grad": (I32, [C.POINTER(RouteT), P, I64, P, I64, C.POINTER(Rows8T), P, I64, I64, P, I64,
                                       C.POINTER(Rows8T), I64, I64, I32, I32, P, I64, P, I64, P, I64, I64, P, SZ, P]),
 }

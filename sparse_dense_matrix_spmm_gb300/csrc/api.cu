@@ -15,7 +15,7 @@ __device__ int g_device_error;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxKernelSlots = 48;
+constexpr int kMaxKernelSlots = 56;
 DeviceInfo g_info[kMaxDevices];
 bool g_info_ok[kMaxDevices];
 bool g_attr_done[kMaxDevices][kMaxKernelSlots];
@@ -931,14 +931,28 @@ spmm_status spmm_gated_grad(const spmm_route_t* R, const void* dh, int64_t lddh,
                              reinterpret_cast<cudaStream_t>(stream));
 }
 
-spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t* R, int64_t K, int32_t packed_rows,
+namespace {
+// What spmm_experts_gated_grad keeps for the duration of the call: the fp32 sums of
+// dW's parts, and the rows read back from 8 bits.
+struct GradSpace {
+    size_t sums, rows;  // bytes
+};
+GradSpace grad_space(const spmm_route_t* R, int64_t N, int64_t K, bool packed_rows) {
+    const int64_t n = R->T * R->k, parts = experts_dw_parts(n, R->n_keys, 2 * N, K);
+    return {parts > 1 ? static_cast<size_t>(parts * R->n_keys) * static_cast<size_t>(2 * N * K) * 4 : 0,
+            packed_rows ? static_cast<size_t>(n) * static_cast<size_t>(K) * 2 : 0};
+}
+}  // namespace
+
+spmm_status spmm_experts_gated_grad_workspace_size(const spmm_route_t* R, int64_t N, int64_t K, int32_t packed_rows,
                                                    size_t* bytes) {
     if (!bytes) return SPMM_ERR_NULL;
     const spmm_status st = check_route(R, false);
     if (st != SPMM_OK) return st;
-    if (K <= 0 || K % 8 || (packed_rows & ~1)) return SPMM_ERR_SHAPE;
-    if (K >= kDimLimit / 2) return SPMM_ERR_UNSUPPORTED;
-    *bytes = packed_rows ? static_cast<size_t>(R->T * R->k) * static_cast<size_t>(K) * 2 : 0;
+    if (N <= 0 || N % 16 || K <= 0 || K % 8 || (packed_rows & ~1)) return SPMM_ERR_SHAPE;
+    if (N >= kDimLimit / 4 || K >= kDimLimit / 2 || R->n_keys > 65535) return SPMM_ERR_UNSUPPORTED;
+    const GradSpace g = grad_space(R, N, K, packed_rows != 0);
+    *bytes = g.sums + g.rows;
     return SPMM_OK;
 }
 
@@ -962,18 +976,20 @@ spmm_status spmm_experts_gated_grad(const spmm_route_t* R, const void* dh, int64
     }
     if (!R->offsets || !dW || (rows > 0 && ((!xs && !xs8) || !W || !dxs))) return SPMM_ERR_NULL;
     if (!aligned16(xs) || !aligned16(W) || !aligned16(dxs) || !aligned16(dW)) return SPMM_ERR_SHAPE;
-    const size_t need = xs8 ? static_cast<size_t>(rows) * static_cast<size_t>(K) * 2 : 0;
-    if (need && (!workspace || workspace_bytes < need)) return SPMM_ERR_WORKSPACE;
+    const GradSpace need = grad_space(R, N, K, xs8 != nullptr);
+    if (need.sums + need.rows && (!workspace || workspace_bytes < need.sums + need.rows)) return SPMM_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPMM_ERR_SHAPE;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    float* sums = need.sums ? static_cast<float*>(workspace) : nullptr;
+    void* read = static_cast<char*>(workspace) + need.sums;  // a multiple of 16 bytes: K % 8 == 0
     if (rows > 0) {
         st = launch_gated_grad(R, dh, lddh, gu, ldgu, packed, N, dtype, act, dgu, lddgu, nullptr, 0, s);
         if (st != SPMM_OK) return st;
         st = launch_experts_rows(R, dgu, lddgu, W, ldw, lde, 2 * N, K, true, dtype, dxs, lddx, s);
         if (st != SPMM_OK) return st;
-        if (xs8 && (st = launch_unpack_rows(xs8, workspace, K, dtype, s)) != SPMM_OK) return st;
+        if (xs8 && (st = launch_unpack_rows(xs8, read, K, dtype, s)) != SPMM_OK) return st;
     }
-    return launch_experts_dw(R, dgu, lddgu, xs8 ? workspace : xs, xs8 ? K : ldx, 2 * N, K, dtype, dW, lddw, ldde, s);
+    return launch_experts_dw(R, dgu, lddgu, xs8 ? read : xs, xs8 ? K : ldx, 2 * N, K, dtype, dW, lddw, ldde, s, sums);
 }
 
 }  // extern "C"

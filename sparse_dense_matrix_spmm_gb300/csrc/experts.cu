@@ -62,7 +62,11 @@ using namespace ptx;
 // beside the rest of it: 320 us against 305 with one sum.  Without the fold 372-418
 // us; three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns
 // takes nearly the time of one of 256).
-enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3, kGatedHalves = 4 };
+// Beside these, dw in parts: an expert's rows in several units, whose fp32 sums a second
+// kernel joins.
+enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3, kGatedHalves = 4, kDwParts = 5 };
+__host__ __device__ constexpr bool is_gated(int form) { return form >= kGated && form <= kGatedHalves; }
+__host__ __device__ constexpr bool is_packed(int form) { return form == kGatedPacked || form == kGatedHalves; }
 // The step at which the second half begins; there is one if that is below the steps.
 __host__ __device__ constexpr int second_half(int steps) { return (steps + 1) / 2; }
 
@@ -149,6 +153,11 @@ struct Gate<kGatedPacked> : GateArgs {
 };
 template <>
 struct Gate<kGatedHalves> : Gate<kGatedPacked> {};
+template <>
+struct Gate<kDwParts> {
+    float* sums;  // parts x E x m x n
+    int32_t parts;
+};
 
 // A work unit: D rows m0.. and columns n0.. (row products: rows p0 + n0 ..) of
 // expert e, `nt` columns computed and `live` of them stored, `steps` stages.
@@ -176,11 +185,13 @@ __device__ __forceinline__ void tile_of(int i, int m_tiles, int n_tiles, int& mt
     nt = g * kGroup + rest - mt * width;
 }
 
+// With parts > 1 a dw unit is one of that many consecutive pieces of an expert's
+// rows, all but the last of whole stages, and Unit::e counts experts part by part.
 template <int CG, int TILE, bool DW>
 struct Walk {
     const ExpertArgs& a;
-    int lane, e0 = 0, base = 0, start = 0, cnt = 0, incl = 0;
-    __device__ Walk(const ExpertArgs& args, int l) : a(args), lane(l) {
+    int parts, lane, e0 = 0, base = 0, start = 0, cnt = 0, incl = 0;
+    __device__ Walk(const ExpertArgs& args, int n, int l) : a(args), parts(n), lane(l) {
         if (!DW) window();
     }
     __device__ void window() {
@@ -197,12 +208,19 @@ struct Walk {
     __device__ bool find(int u, Unit& w) {
         if (DW) {
             const int per = a.m_tiles * a.n_tiles;
-            if (u >= a.E * per) return false;
+            if (u >= parts * a.E * per) return false;
             w.e = u / per;
             int mt, nt;
             tile_of(u - w.e * per, a.m_tiles, a.n_tiles, mt, nt);
-            w.p0 = a.offsets[w.e];
-            w.cnt = a.offsets[w.e + 1] - w.p0;
+            const int part = parts > 1 ? w.e / a.E : 0, e = w.e - part * a.E;
+            w.p0 = a.offsets[e];
+            w.cnt = a.offsets[e + 1] - w.p0;
+            if (parts > 1) {
+                const int size = (w.cnt + parts * kDepth - 1) / (parts * kDepth) * kDepth;
+                const int skip = min(part * size, w.cnt);
+                w.p0 += skip;
+                w.cnt = min(size, w.cnt - skip);
+            }
             w.m0 = mt * 128 * CG;
             w.n0 = nt * TILE;
             w.live = min(TILE, a.n - w.n0);
@@ -421,7 +439,7 @@ __device__ __forceinline__ void store_gated(const ExpertArgs& a, const Gate<FORM
             store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, f0, in, row, live, g, lane, planes, turn);
             store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, x.features + f0, in, row, live, u, lane, planes, turn);
         }
-        if constexpr (FORM >= kGatedPacked) {
+        if constexpr (is_packed(FORM)) {
             store_packed(x, f0, in, row, live, g, lane, planes, turn);
             store_packed(x, x.features + f0, in, row, live, u, lane, planes, turn);
         }
@@ -462,7 +480,7 @@ __device__ __forceinline__ void clear_kept(const Gate<FORM>& x, int64_t p, int l
         uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(x.gu) + p * x.ldgu);
         for (int c = lane; c < x.features / 4; c += 32) row[c] = make_uint4(0, 0, 0, 0);
     }
-    if constexpr (FORM >= kGatedPacked) {
+    if constexpr (is_packed(FORM)) {
         uint4* row = reinterpret_cast<uint4*>(x.q + p * x.ldq);
         for (int c = lane; c < x.features / 8; c += 32) {
             row[c] = make_uint4(0, 0, 0, 0);
@@ -505,6 +523,31 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap*
         if (lane == 0) {
             if (row0 < a.m) tma_store_3d(tmOut, stage, w.n0 + c, row0, w.e);
             bulk_commit();
+        }
+    }
+}
+
+// dw in parts: fp32 sums as they are, a lane's row by 16 bytes.
+__device__ __forceinline__ void store_part(const ExpertArgs& a, float* sums, const Unit& w, uint32_t t, int c0, int c1,
+                                           int row0, int lane) {
+    const bool in = row0 + lane < a.m;
+    float* out = sums + (static_cast<int64_t>(w.e) * a.m + row0 + lane) * a.n + w.n0;
+    for (int c = c0; c < c1; c += 32) {
+        uint32_t v[2][16];
+        __syncwarp();  // as in store_rows
+        if (w.steps == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
+        } else {
+            tmem_ld16(t + c, v[0]);
+            tmem_ld16(t + c + 16, v[1]);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t* f = &v[i >> 2][4 * (i & 3)];
+            if (in && c + 4 * i < c1)  // n % 8 == 0: four are stored or none
+                *reinterpret_cast<uint4*>(out + c + 4 * i) = make_uint4(f[0], f[1], f[2], f[3]);
         }
     }
 }
@@ -685,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (AMN) {
                             load_3d<CG>(st, &tmA, bar, m0, d0, w.e);
                             load_3d<CG>(st + kABytes / 2, &tmA, bar, m0 + 64, d0, w.e);
-                        } else if (FORM != kPlain) {
+                        } else if constexpr (is_gated(FORM)) {
                             load_5d<CG>(st, &tmA, bar, d0, 0, 0, m0 / 32, w.e);  // 32 rows of D: 16 gate, 16 up
                         } else {
                             load_3d<CG>(st, &tmA, bar, d0, m0, w.e);
@@ -834,7 +877,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
     } else if (warp == 3) {
         // ------------------------------------------------ work units, and the zero rows of dropped choices
-        Walk<CG, TILE, DW> walk(a, lane);
+        int parts = 1;
+        if constexpr (FORM == kDwParts) parts = gate.parts;
+        Walk<CG, TILE, DW> walk(a, parts, lane);
         bool more = true;
         for (int u = group; more; u += groups) {
             more = walk.find(u, w);
@@ -853,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!DW) {
             for (int64_t p = a.offsets[a.E] + static_cast<int64_t>(blockIdx.x); p < a.R; p += gridDim.x) {
                 uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + p * a.ldo);
-                for (int c = lane; c < (FORM == kPlain ? a.m / 8 : a.m / 16); c += 32) row[c] = make_uint4(0, 0, 0, 0);
+                for (int c = lane; c < (is_gated(FORM) ? a.m / 16 : a.m / 8); c += 32) row[c] = make_uint4(0, 0, 0, 0);
                 clear_kept(gate, p, lane);
             }
         }
@@ -893,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 give_back(0);
                 t += TILE;
             }
-            if constexpr (FORM != kPlain) {
+            if constexpr (is_gated(FORM)) {
                 auto store = [&](auto type, auto act) {
                     using T = decltype(type);
                     store_gated<T, decltype(act)::value, FORM>(a, gate, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
@@ -910,6 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     typed(std::integral_constant<int, SPMM_ACT_GELU>());
                 else
                     typed(std::integral_constant<int, SPMM_ACT_GELU_TANH>());
+            } else if constexpr (FORM == kDwParts) {
+                store_part(a, gate.sums, w, t, c0, c1, row0, lane);
             } else if (DW) {
                 if (a.bf16)
                     store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
@@ -1126,6 +1173,38 @@ __global__ void __launch_bounds__(kDwThreads, 4) experts_dw_vec_kernel(const DwA
     }
 }
 
+// Parts of dw joined, in their order.
+struct JoinArgs {
+    const float* sums;
+    int32_t parts;
+    int64_t E;
+    int32_t N, K;
+    void* dW;
+    int64_t ldw, lde;
+};
+constexpr int kJoinThreads = 64;
+
+// Grid (8 columns per thread, row, expert).
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) experts_join_kernel(const JoinArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int k = (blockIdx.x * kJoinThreads + threadIdx.x) * 8;
+    if (k >= a.K) return;
+    const int64_t row = static_cast<int64_t>(blockIdx.z) * a.N + blockIdx.y, part = a.E * a.N * a.K;
+    const float* in = a.sums + row * a.K + k;
+    float f[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.parts; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(in + s * part);
+        const float4 y = *reinterpret_cast<const float4*>(in + s * part + 4);
+        f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
+        f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+    }
+    using V = rows::Vec<T, 8>;
+    V::store(static_cast<T*>(a.dW) + blockIdx.z * a.lde + blockIdx.y * a.ldw + k, V::pack(f));
+}
+
 bool weights_map(CUtensorMap* map, int32_t dtype, const void* W, int64_t ldw, int64_t lde, int64_t N, int64_t K,
                  int64_t E, uint32_t box_rows) {
     const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
@@ -1145,9 +1224,9 @@ spmm_status launch(const CUtensorMap& tmA, const BMaps& tmB, const CUtensorMap& 
     if (units >= (int64_t(1) << 31) - dev->sms) return SPMM_ERR_UNSUPPORTED;
     const auto kern = experts_kernel<CG, TILE, AMN, BMN, FORM>;
     constexpr int smem = Ring<CG, TILE, BMN>::kSmem;
-    constexpr int slot = FORM == kPlain
+    constexpr int slot = !is_gated(FORM) && FORM != kDwParts
                              ? kSlotExperts + (TILE < 256 ? 6 : 0) + (CG - 1) * 3 + (BMN ? 2 : AMN ? 1 : 0)
-                             : kSlotGated + 3 * (FORM - 1) + (TILE < 256 ? 2 : CG - 1);
+                             : kSlotGated + 3 * (FORM - 1) + (TILE < 256 ? 2 : CG - 1);  // twelve, and two for dw in parts
     if (!set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, slot)) return SPMM_ERR_CUDA;
     const int64_t groups = units < dev->sms / CG ? units : dev->sms / CG;
     trace_begin(SPMM_KERNEL_EXPERTS, s);
@@ -1212,11 +1291,31 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
                       : launch<1, 256, false, false>(tmA, tmB, tmOut, a, units, dev, s);
 }
 
+// dw never splits an expert's rows by itself, so few experts with small matrices
+// leave most SMs idle.  With room for the sums (E N K fp32 per part) the rows are cut
+// into as many parts as fill the CTA pairs once, of 256 rows or more on average, where
+// experts have 4096 rows or more on average: the join and the fp32 stores cost 6-8 us, a
+// step of 64 rows 0.28.  The whole way back of 65536 rows over 2 experts, 2 x 128 x 256:
+// 61 us in 38 parts, 172 us in one; 32768 over 2, 2 x 256 x 512: 63 us in 9, 107 in one; 4096
+// over 2, 2 x 128 x 256: 24 us in 8, 25 in one; 16384 over 8, 2 x 256 x 512: 40 us in 2, 36
+// in one.  By sizes alone, so that the bits do not depend on how the ids are spread.
+int experts_dw_parts(int64_t n, int64_t E, int64_t N, int64_t K) {
+    constexpr int64_t kSms = 152, kLeast = 256, kLong = 4096;
+    if (n < E * kLong) return 1;
+    const int64_t group = N > 128 ? 2 : 1, rows = 128 * group;
+    const int64_t units = E * ((N + rows - 1) / rows) * ((K + 255) / 256);
+    const int64_t fill = kSms / group / units, most = n / (E * kLeast);
+    const int64_t parts = fill < most ? fill : most;
+    return parts > 1 ? static_cast<int>(parts) : 1;
+}
+
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
-                              int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s) {
+                              int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s,
+                              float* sums) {
     const DeviceInfo* dev = device_info();
     if (!dev) return SPMM_ERR_CUDA;
     const int64_t n = R->T * R->k;
+    const int parts = sums ? experts_dw_parts(n, R->n_keys, N, K) : 1;
     if (n <= R->n_keys * kDwFewRows) {
         const DwArgs v{R->offsets, dys, xs, ldd, ldx, ldw, lde, static_cast<int32_t>(N), static_cast<int32_t>(K), dW};
         const dim3 grid(static_cast<unsigned>(N / kDwRows), static_cast<unsigned>(R->n_keys));
@@ -1248,6 +1347,21 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     if (!rows_map(&tmA, dtype, dys, ldd, n, N, kDepth) || !rows_map(&tmB.m[0], dtype, xs, ldx, n, K, kDepth))
         return SPMM_ERR_CUDA;
     const int64_t units = static_cast<int64_t>(a.E) * a.m_tiles * a.n_tiles;
+    if (parts > 1) {
+        const Gate<kDwParts> gate{sums, parts};
+        const spmm_status st = pair ? launch<2, 256, true, true, kDwParts>(tmA, tmB, tmOut, a, units * parts, dev, s, gate)
+                                    : launch<1, 256, true, true, kDwParts>(tmA, tmB, tmOut, a, units * parts, dev, s, gate);
+        if (st != SPMM_OK) return st;
+        const JoinArgs j{sums, parts, R->n_keys, static_cast<int32_t>(N), static_cast<int32_t>(K), dW, ldw, lde};
+        const dim3 grid(static_cast<unsigned>((K / 8 + kJoinThreads - 1) / kJoinThreads), static_cast<unsigned>(N),
+                        static_cast<unsigned>(R->n_keys));
+        trace_begin(SPMM_KERNEL_EXPERTS, s);
+        const cudaError_t e = dtype == SPMM_BF16
+                                  ? launch_chained(experts_join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, s, j)
+                                  : launch_chained(experts_join_kernel<__half>, grid, kJoinThreads, 0, 1, s, j);
+        trace_end(SPMM_KERNEL_EXPERTS, s);
+        return cuda_status(e);
+    }
     return pair ? launch<2, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s)
                 : launch<1, 256, true, true>(tmA, tmB, tmOut, a, units, dev, s);
 }

@@ -65,8 +65,8 @@ void trace_begin(int kernel, cudaStream_t s);
 void trace_end(int kernel, cudaStream_t s);
 
 // First of the twelve slots of set_smem_attr_once that the experts' kernels take
-// (0-23 belong to the format kernels), and of the twelve that their gated form takes.
-enum : int { kSlotExperts = 24, kSlotGated = 36 };
+// (0-23 belong to the format kernels), and of the fourteen that their gated forms and dw in parts take.
+enum : int { kSlotExperts = 24, kSlotGated = 36 };  // the last is 49
 
 // Raise a kernel's dynamic shared memory limit once per device.
 bool set_smem_attr_once(const void* kernel, int bytes, int slot);
@@ -182,7 +182,11 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
                                 int64_t lde, int64_t N, int64_t K, bool transposed, int32_t dtype, void* out,
                                 int64_t ldo, cudaStream_t s);
 spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ldd, const void* xs, int64_t ldx,
-                              int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s);
+                              int64_t N, int64_t K, int32_t dtype, void* dW, int64_t ldw, int64_t lde, cudaStream_t s,
+                              float* sums = nullptr);
+// Parts that launch_experts_dw cuts the rows into where it is given `sums`, room
+// for E N K fp32 per part; n rows in all.
+int experts_dw_parts(int64_t n, int64_t E, int64_t N, int64_t K);
 
 // The router; rows in 8 bits; the gated block and the gradient of its activation.
 spmm_status launch_topk(const void* logits, int64_t T, int64_t E, int64_t ldl, int32_t dtype, int32_t k, int32_t renorm,

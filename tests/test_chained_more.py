@@ -38,7 +38,7 @@ def test_gated_epilogue_reads_tmem_together():
     """TMEM loads and transposing stores need whole warps, which come from spinning waits and one thread's stores."""
     from tests.test_warp_convergence import _NEEDS, _body, _unsafe
     code = _code("experts.cu")
-    for head in (r"void store_gated\(", r"void fold_halves\("):
+    for head in (r"void store_gated\(", r"void fold_halves\(", r"void store_part\("):
         body = _body(code, head)
         loop = body[body.index("for (int c = c0"):]
         assert re.search(_NEEDS, loop) and _unsafe(loop + loop, True) is None, head

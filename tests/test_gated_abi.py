@@ -150,7 +150,31 @@ def test_experts_gated_grad(L):
     assert call(xs=None, xs8=_rows8(cols=K, ldq=K, q=None), ws=16, wsb=1 << 20) == NULL
     n = ctypes.c_size_t(0)
     size = L.spmm_experts_gated_grad_workspace_size
-    assert size(_route(), K, 1, ctypes.byref(n)) == 0 and n.value == 20 * K * 2
-    assert size(_route(), K, 0, ctypes.byref(n)) == 0 and n.value == 0
-    assert size(_route(), K, 2, ctypes.byref(n)) == SHAPE and size(_route(), 60, 1, ctypes.byref(n)) == SHAPE
-    assert size(_route(), K, 1, None) == NULL and size(None, K, 1, ctypes.byref(n)) == NULL
+    assert size(_route(), N, K, 1, ctypes.byref(n)) == 0 and n.value == 20 * K * 2
+    assert size(_route(), N, K, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert size(_route(), N, K, 2, ctypes.byref(n)) == SHAPE and size(_route(), N, 60, 1, ctypes.byref(n)) == SHAPE
+    assert size(_route(), 24, K, 1, ctypes.byref(n)) == SHAPE and size(_route(E=70000), N, K, 1, ctypes.byref(n)) == UNSUPPORTED
+    assert size(_route(), N, K, 1, None) == NULL and size(None, N, K, 1, ctypes.byref(n)) == NULL
+
+
+@pytest.mark.parametrize("rows,E,N,K", [(65536, 2, 128, 256), (16384, 2, 256, 512), (5000, 1, 64, 64), (50000, 12, 80, 248),
+                                        (1 << 20, 3, 16, 8)])
+def test_room_for_the_parts_of_dw(L, rows, E, N, K):
+    """Parts fill the 76 CTA pairs (or 152 CTAs, up to 128 rows of dW) once at most, with 256 rows each on average; experts
+    have 4096 on average."""
+    n = ctypes.c_size_t(0)
+    assert L.spmm_experts_gated_grad_workspace_size(_route(T=rows, k=1, E=E), N, K, 0, ctypes.byref(n)) == 0
+    parts, rest = divmod(n.value, E * 2 * N * K * 4)
+    side = 256 if 2 * N > 128 else 128
+    units = E * -(-2 * N // side) * -(-K // 256)
+    assert rest == 0 and parts == min((76 if side == 256 else 152) // units, rows // (256 * E)) and parts > 1
+    assert n.value <= 20 << 20
+    assert L.spmm_experts_gated_grad_workspace_size(_route(T=rows, k=1, E=E), N, K, 1, ctypes.byref(n)) == 0
+    assert n.value == parts * E * 2 * N * K * 4 + rows * K * 2
+
+
+def test_no_room_where_dw_is_large(L):
+    n = ctypes.c_size_t(0)
+    for rows, E, N, K in ((65536, 16, 1280, 3584), (900, 2, 64, 64), (65536, 64, 128, 512), (8, 2, 16, 64), (16384, 8, 256, 512)):
+        assert L.spmm_experts_gated_grad_workspace_size(_route(T=rows, k=1, E=E), N, K, 0, ctypes.byref(n)) == 0
+        assert n.value == 0

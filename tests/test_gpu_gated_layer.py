@@ -84,7 +84,7 @@ def test_the_whole_way_back_is_its_parts(xs_packed, gu_packed):
     dgu = spmm.spmm_gated_grad(R, dh, gu, act="gelu")
     rows = spmm.spmm_unpack_rows(P) if xs_packed else xs
     want = dgu, spmm.spmm_experts_dx(R, dgu, W), spmm.spmm_experts_dw(R, dgu, rows)
-    need = spmm.spmm_experts_gated_grad_workspace_size(R, 136, xs_packed)
+    need = spmm.spmm_experts_gated_grad_workspace_size(R, 80, 136, xs_packed)
     assert need == (180 * 136 * 2 if xs_packed else 0)
     ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
     for a, b, c in zip(got, want, spmm.spmm_experts_gated_grad(R, dh, P, W, gu, act="gelu", workspace=ws)):
@@ -92,3 +92,40 @@ def test_the_whole_way_back_is_its_parts(xs_packed, gu_packed):
     if xs_packed:
         with pytest.raises(spmm.SpmmError, match="WORKSPACE"):
             spmm.spmm_experts_gated_grad(R, dh, P, W, gu, act="gelu", workspace=ws[:need - 16])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("xs_packed", [False, True])
+@pytest.mark.parametrize("counts,dropped,N,K", [([5000, 0, 9000], 40, 128, 248), ([8000, 400], 0, 64, 64), ([1, 9000], 5, 80, 520),
+                                                ([4500], 0, 16, 8), ([64 * 69, 64 * 67 + 1, 0, 0, 12000], 3, 144, 136)])
+def test_dw_in_parts(dtype, xs_packed, counts, dropped, N, K):
+    """Few experts with small matrices: dW's rows are summed in parts.  Experts of unequal length, one with fewer rows
+    than there are parts, one without any; NaN behind the kept rows; the same bits on every run."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    from tests.gated_util import held
+    from tests.onehot_util import DT, check, f64, matrix
+    ids = np.concatenate([np.full(c, e) for e, c in enumerate(counts)] + [np.full(dropped, -1)])
+    R = spmm.spmm_build_route(torch.from_numpy(np.random.default_rng(2).permutation(ids)).cuda(), len(counts))
+    n, kept, E = R.n_rows, sum(counts), len(counts)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    xs, W, dh = matrix((n, K), dtype, 1), matrix((E, 2 * N, K), dtype, 2, K ** -0.5), matrix((n, N), dtype, 3)
+    gu = matrix((n, 2 * N), dtype, 4)
+    xs[kept:], dh[kept:], gu[kept:] = float("nan"), float("nan"), float("nan")
+    P = spmm.spmm_pack_rows(xs) if xs_packed else xs
+    X = held(P.q.cpu().numpy(), P.scale.cpu().numpy()) if xs_packed else f64(xs)
+    need = spmm.spmm_experts_gated_grad_workspace_size(R, N, K, xs_packed) - (n * K * 2 if xs_packed else 0)
+    assert need >= 2 * E * 2 * N * K * 4
+    ws = torch.full((need + n * K * 2,), 255, dtype=torch.uint8, device="cuda")  # NaN everywhere
+    dgu, dxs, dW = spmm.spmm_experts_gated_grad(R, dh, P, W, gu, workspace=ws)
+    D = f64(dgu)
+    dw, dwm = np.zeros((E, 2 * N, K)), np.zeros((E, 2 * N, K))
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        dw[e], dwm[e] = D[a:b].T @ X[a:b], np.abs(D[a:b]).T @ np.abs(X[a:b])
+    check(dW, dw, dwm, max(counts), dtype, "dW")
+    assert torch.equal(dxs, spmm.spmm_experts_dx(R, dgu, W))
+    for _ in range(2):
+        assert torch.equal(spmm.spmm_experts_gated_grad(R, dh, P, W, gu)[2], dW)
+    torch.cuda.synchronize()
+    assert spmm.last_device_error() == 0

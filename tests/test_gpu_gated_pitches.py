@@ -17,7 +17,7 @@ def _wide(torch, rows, cols, pad, dtype, fill=7):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("tokens,experts", [(3, 4), (200, 4), (90, 40)])
+@pytest.mark.parametrize("tokens,experts", [(3, 4), (200, 4), (90, 40), (4200, 2)])
 def test_wider_rows(dtype, tokens, experts):
     torch = need_gpu()
     import sparse_dense_matrix_spmm_gb300 as spmm
@@ -31,6 +31,7 @@ def test_wider_rows(dtype, tokens, experts):
     h, gu = spmm.spmm_experts_gated(R, xs, W, act="gelu", save="rows")
     h8, P = spmm.spmm_experts_gated(R, xs, W, act="gelu", save="packed")
     stream = spmm._handle(None, xs.device)
+    room = torch.empty(spmm.spmm_experts_gated_grad_workspace_size(R, N, K, False) + 16, dtype=torch.uint8, device="cuda")
     fh, wh = _wide(torch, n, N, 24, t)
     fg, wg = _wide(torch, n, 2 * N, 40, t)
     _lib.call("spmm_experts_gated", R._ref, xs.data_ptr(), K, W.data_ptr(), K, 2 * N * K, N, K, code, _lib.ACT_GELU, wh.data_ptr(),
@@ -56,7 +57,7 @@ def test_wider_rows(dtype, tokens, experts):
         fw = torch.full((experts, 2 * N + 3, K + 16), 7, dtype=t, device="cuda")
         _lib.call("spmm_experts_gated_grad", R._ref, dh.data_ptr(), N, xs.data_ptr(), K, None, W.data_ptr(), K, 2 * N * K, rows,
                   pitch or 2 * N, None if pitch else wide._ref, N, K, code, _lib.ACT_GELU, wd.data_ptr(), 2 * N + 8, wx.data_ptr(),
-                  K + 8, fw.data_ptr(), K + 16, (2 * N + 3) * (K + 16), None, C.c_size_t(0), stream)
+                  K + 8, fw.data_ptr(), K + 16, (2 * N + 3) * (K + 16), room.data_ptr(), C.c_size_t(room.numel()), stream)
         assert torch.equal(wd, want[0]) and torch.equal(wx, want[1]) and torch.equal(fw[:, :2 * N, :K], want[2])
         assert (fx[:, K:] == 7).all() and (fw[:, 2 * N:] == 7).all() and (fw[:, :, K:] == 7).all()
     torch.cuda.synchronize()
