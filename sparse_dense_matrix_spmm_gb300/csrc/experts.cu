@@ -374,26 +374,61 @@ __device__ __forceinline__ void store_packed(const Gate<kGatedPacked>& x, int co
     const uint32_t plane = planes + turn * kPlaneBytes;
     turn = (turn + 1) % kPlanes;
     if (lane == 0) bulk_wait_read<kPlanes - 1>();
-    uint32_t mine = 0;  // the scale of row 8 (lane / 8) + 2 (lane % 4) + lane / 4 % 2
     __syncwarp();
+    // The upper halves of the magnitudes order as they do and hold what the scale goes by;
+    // two rows side by side.
+    uint32_t m[4], most = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        // codes of two rows side by side, 16 bits each
-        uint32_t code = max(magnitude_code(v[4 * b]), magnitude_code(v[4 * b + 2])) |
-                        max(magnitude_code(v[4 * b + 1]), magnitude_code(v[4 * b + 3])) << 16;
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) code = __vmaxu2(code, __shfl_xor_sync(0xffffffffu, code, d));
-        const uint32_t s0 = scale_byte(code & 0xFFFFu), s1 = scale_byte(code >> 16);
-        const uint32_t at = plane + (8 * b + 2 * (lane & 3)) * 16 + (lane >> 2);
-        uint32_t q0[2], q1[2];
-        quantise({v[4 * b], v[4 * b + 2]}, s0, q0);
-        quantise({v[4 * b + 1], v[4 * b + 3]}, s1, q1);
-        st_shared_u8(at, q0[0]);
-        st_shared_u8(at + 8, q0[1]);
-        st_shared_u8(at + 16, q1[0]);
-        st_shared_u8(at + 24, q1[1]);
-        if (lane >> 3 == b) mine = lane & 4 ? s1 : s0;
+        const uint32_t x = __byte_perm(__float_as_uint(v[4 * b]), __float_as_uint(v[4 * b + 1]), 0x7632);
+        const uint32_t y = __byte_perm(__float_as_uint(v[4 * b + 2]), __float_as_uint(v[4 * b + 3]), 0x7632);
+        m[b] = __vmaxu2(x & 0x7FFF7FFFu, y & 0x7FFF7FFFu);
     }
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) m[b] = __vmaxu2(m[b], __shfl_xor_sync(0xffffffffu, m[b], d));
+    uint32_t mine = 0;  // m of rows 8 (lane / 8) + 2 (lane % 4) and the next
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        most = __vmaxu2(most, m[b]);
+        mine = lane >> 3 == b ? m[b] : mine;
+    }
+    const uint32_t at = plane + 2 * (lane & 3) * 16 + (lane >> 2);
+    if (!__any_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16) >= 0x7EFFu)) {
+        // codes below 254: no cut at 127, nothing infinite
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t s = __vmaxu2((m[b] + 0x00010001u) >> 7 & 0x01FF01FFu, 0x00070007u) - 0x00060006u;
+            const float i0 = __uint_as_float(0x7F000000u - (s << 23)), i1 = __uint_as_float(0x7F000000u - (s >> 16 << 23));
+            st_shared_u8(at + 128 * b, __float_as_uint(fmaf(v[4 * b], i0, kRoundUnits)));
+            st_shared_u8(at + 128 * b + 8, __float_as_uint(fmaf(v[4 * b + 2], i0, kRoundUnits)));
+            st_shared_u8(at + 128 * b + 16, __float_as_uint(fmaf(v[4 * b + 1], i1, kRoundUnits)));
+            st_shared_u8(at + 128 * b + 24, __float_as_uint(fmaf(v[4 * b + 3], i1, kRoundUnits)));
+        }
+    } else {
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+            uint32_t q0[2], q1[2], mb = m[0];
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+#pragma unroll
+            for (int c = 1; c < 4; ++c)
+                if (b == c) {
+                    mb = m[c];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = v[4 * c + i];
+                }
+            quantise({w[0], w[2]}, scale_byte(code_of_upper(mb & 0xFFFFu)), q0);
+            quantise({w[1], w[3]}, scale_byte(code_of_upper(mb >> 16)), q1);
+            st_shared_u8(at + 128 * b, q0[0]);
+            st_shared_u8(at + 128 * b + 8, q0[1]);
+            st_shared_u8(at + 128 * b + 16, q1[0]);
+            st_shared_u8(at + 128 * b + 24, q1[1]);
+        }
+    }
+    mine = scale_byte(code_of_upper(lane & 4 ? mine >> 16 : mine & 0xFFFFu));
     const int mine_row = 8 * (lane >> 3) + 2 * (lane & 3) + (lane >> 2 & 1);
     if (in && mine_row < live)
         x.scale[(static_cast<int64_t>(row) + mine_row) * x.lds + column / gated::kGroup] = static_cast<uint8_t>(mine);
