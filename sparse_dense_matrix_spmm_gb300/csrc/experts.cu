@@ -59,7 +59,7 @@ using namespace ptx;
 // depth are summed in accumulators of their own and added in fp32: 3.2e-4.  Both
 // accumulators then belong to one unit.  The epilogue first folds them, the sum into
 // the second one, and gives the first back, so that the next unit's first half runs
-// beside the rest of it: 320 us against 305 with one sum.  Without the fold 372-418
+// beside the rest of it: 320 us against 305 with one sum (306 with the epilogue as it is).  Without the fold 372-418
 // us; three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns
 // takes nearly the time of one of 256).
 // Beside these, dw in parts: an expert's rows in several units, whose fp32 sums a second
@@ -265,7 +265,7 @@ struct Ring {
     static constexpr int kBox = DW ? 4096 : 2048;  // one staging buffer
     static constexpr int kOut = 2 * kBox;
     static constexpr int kStages = (kSmemMax - 1024 - kEpiWarps * kOut - 1536) / kStage;
-    static constexpr int kBars = 4 * kStages + 5 + 2 * kUnits;
+    static constexpr int kBars = 4 * kStages + 5 + 2 * kUnits + 2;
     static constexpr int kBarOff = kStages * kStage + kEpiWarps * kOut;
     static constexpr int kUnitOff = kBarOff + kBars * 8 + 16;
     static constexpr int kSmem = 1024 + kUnitOff + kUnits * static_cast<int>(sizeof(Unit));
@@ -324,59 +324,50 @@ __device__ __forceinline__ void store_rows(const ExpertArgs& a, const CUtensorMa
 }
 
 // Gated block: TMEM lanes 0-15 of the warp's quarter are g, 16-31 u of the same 16
-// features.  Results leave in planes of 32 rows x 16 features, four of which a warp
-// uses in turn: as a TMA box of 32 live rows (32 bytes a row, 16-byte units swizzled
-// by row / 4), the last rows of a tile in 16-byte pieces.
-constexpr int kPlanes = 4, kPlaneBytes = 1024;
+// features.  Results of 32 rows are put into shared memory as planes of 32 rows x 16
+// features (h, and what is kept of g and u) and leave together: as TMA boxes where
+// all 32 rows are live (32 bytes a row in 16 bits, 16-byte units swizzled by row / 4),
+// the last rows of a tile in 16-byte pieces.  (A fence, a barrier and a store for each
+// plane: 22.9 us where this takes 21.2, kept in 16 bits, 8192 rows, 2 x 1024 x 256.)
+constexpr int kPlaneBytes = 1024, kBytePlane = 512;
+// What a warp's staging bytes hold: so many chunks of planes in turn, and for 8 bits,
+// in the first warp of each half of the columns, two buffers of scale bytes.
+template <int FORM>
+constexpr int kChunkBytes = FORM == kGated ? kPlaneBytes : FORM == kGatedRows ? 3 * kPlaneBytes : 2 * kPlaneBytes;
+template <int FORM>
+constexpr int kChunks = FORM == kGated ? 4 : 1;
+constexpr int kScalesAt = 2048, kScaleBytes = 1024;  // 128 rows x 8: four groups of g, four of u
 
 // One plane in 16 bits.  v[4 b] .. v[4 b + 3]: rows 8 b + 2 (lane % 4) and the next of
 // feature lane / 4, and the same of feature lane / 4 + 8.
 template <typename T>
-__device__ __forceinline__ void store_plane(const CUtensorMap* tm, T* out, int64_t ld, int column, bool in, int row,
-                                            int live, const float (&v)[16], int lane, uint32_t planes, int& turn) {
-    const uint32_t plane = planes + turn * kPlaneBytes;
-    turn = (turn + 1) % kPlanes;
-    if (lane == 0) bulk_wait_read<kPlanes - 1>();  // the store before the last three has read this plane
-    __syncwarp();
+__device__ __forceinline__ void put_plane(uint32_t plane, const float (&v)[16], int lane) {
     const uint32_t put = plane + ((lane >> 4) * 8 + (lane & 7)) * 32 + (((lane >> 3 & 1) ^ (lane >> 2 & 1)) << 4);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // rows 16 j .. 16 j + 15
         const float* f = v + 8 * j;
         using P = rows::Pair<T>;
-        stmatrix_x4_trans(put + j * 512, P::pack(f[0], f[1]), P::pack(f[2], f[3]), P::pack(f[4], f[5]), P::pack(f[6], f[7]));
+        stmatrix_x4_trans(put + j * 512, P::pack(f[0], f[1]), P::pack(f[2], f[3]), P::pack(f[4], f[5]),
+                          P::pack(f[6], f[7]));
     }
-    if (live >= 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (in) tma_store_2d(tm, plane, column, row);
-            bulk_commit();
-        }
-        return;
-    }
-    __syncwarp();
+}
+// Its first `live` rows to rows of pitch ld, 16 bytes at a time.
+template <typename T>
+__device__ __forceinline__ void copy_plane(uint32_t plane, T* out, int64_t ld, int live, int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = 16 * i + (lane >> 1), unit = lane & 1;
         const uint4 p = ld_shared_v4(plane + r * 32 + ((unit ^ (r >> 2 & 1)) << 4));
-        if (in && r < live)
-            __stcs(reinterpret_cast<uint4*>(out + (static_cast<int64_t>(row) + r) * ld + column + 8 * unit), p);
+        if (r < live) __stcs(reinterpret_cast<uint4*>(out + r * ld + 8 * unit), p);
     }
-    if (lane == 0) bulk_commit();  // an empty group: one per use of a plane
-    __syncwarp();
 }
 
-// One plane in 8 bits, and its 32 scale bytes.  A row's 16 features are in the 8
-// lanes of the same lane % 4, two each.
-__device__ __forceinline__ void store_packed(const Gate<kGatedPacked>& x, int column, bool in, int row, int live,
-                                             const float (&v)[16], int lane, uint32_t planes, int& turn) {
+// One plane in 8 bits, and its 32 scale bytes, eight bytes apart.  A row's 16 features
+// are in the 8 lanes of the same lane % 4, two each.
+__device__ __forceinline__ void put_packed(uint32_t plane, uint32_t scales, const float (&v)[16], int lane) {
     using namespace gated;
-    const uint32_t plane = planes + turn * kPlaneBytes;
-    turn = (turn + 1) % kPlanes;
-    if (lane == 0) bulk_wait_read<kPlanes - 1>();
-    __syncwarp();
-    // The upper halves of the magnitudes order as they do and hold what the scale goes by;
-    // two rows side by side.
+    // The upper halves of the magnitudes order as they do and hold what the scale goes
+    // by; two rows side by side, and the four blocks of rows interleaved.
     uint32_t m[4], most = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -428,31 +419,15 @@ __device__ __forceinline__ void store_packed(const Gate<kGatedPacked>& x, int co
             st_shared_u8(at + 128 * b + 24, q1[1]);
         }
     }
-    mine = scale_byte(code_of_upper(lane & 4 ? mine >> 16 : mine & 0xFFFFu));
-    const int mine_row = 8 * (lane >> 3) + 2 * (lane & 3) + (lane >> 2 & 1);
-    if (in && mine_row < live)
-        x.scale[(static_cast<int64_t>(row) + mine_row) * x.lds + column / gated::kGroup] = static_cast<uint8_t>(mine);
-    if (live >= 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (in) tma_store_2d(&x.tmKept, plane, column, row);
-            bulk_commit();
-        }
-        return;
-    }
-    __syncwarp();
-    const uint4 p = ld_shared_v4(plane + lane * 16);
-    if (in && lane < live)
-        __stcs(reinterpret_cast<uint4*>(x.q + (static_cast<int64_t>(row) + lane) * x.ldq + column), p);
-    if (lane == 0) bulk_commit();
-    __syncwarp();
+    st_shared_u8(scales + 8 * (8 * (lane >> 3) + 2 * (lane & 3) + (lane >> 2 & 1)),
+                 scale_byte(code_of_upper(lane & 4 ? mine >> 16 : mine & 0xFFFFu)));
 }
 
+// scales: this warp's byte of row c0 in shared memory (8 bits).
 template <typename T, int ACT, int FORM>
 __device__ __forceinline__ void store_gated(const ExpertArgs& a, const Gate<FORM>& x, const CUtensorMap* tmOut,
                                             const Unit& w, uint32_t t, int c0, int c1, int row0, int lane,
-                                            uint32_t planes, int& turn) {
+                                            uint32_t buffers, int& turn, uint32_t scales) {
     const int f0 = row0 / 2;  // the warp's first feature: features come in groups of 16 (N % 16 == 0)
     const bool in = row0 < a.m;
     for (int c = c0; c < c1; c += 32) {
@@ -468,17 +443,72 @@ __device__ __forceinline__ void store_gated(const ExpertArgs& a, const Gate<FORM
             u[i] = __uint_as_float(hi[i]);
             h[i] = gated::act<ACT>(g[i]) * u[i];
         }
-        const int row = w.p0 + w.n0 + c, live = c1 - c;
-        store_plane<T>(tmOut, static_cast<T*>(a.out), a.ldo, f0, in, row, live, h, lane, planes, turn);
+        const uint32_t plane = buffers + turn * kChunkBytes<FORM>;
+        turn = (turn + 1) % kChunks<FORM>;
+        if (lane == 0) bulk_wait_read<kChunks<FORM> - 1>();  // the store that used this buffer has read it
+        __syncwarp();
+        put_plane<T>(plane, h, lane);
         if constexpr (FORM == kGatedRows) {
-            store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, f0, in, row, live, g, lane, planes, turn);
-            store_plane<T>(&x.tmKept, static_cast<T*>(x.gu), x.ldgu, x.features + f0, in, row, live, u, lane, planes, turn);
+            put_plane<T>(plane + kPlaneBytes, g, lane);
+            put_plane<T>(plane + 2 * kPlaneBytes, u, lane);
         }
         if constexpr (is_packed(FORM)) {
-            store_packed(x, f0, in, row, live, g, lane, planes, turn);
-            store_packed(x, x.features + f0, in, row, live, u, lane, planes, turn);
+            put_packed(plane + kPlaneBytes, scales + 8 * (c - c0), g, lane);
+            put_packed(plane + kPlaneBytes + kBytePlane, scales + 8 * (c - c0) + 4, u, lane);
         }
+        const int row = w.p0 + w.n0 + c, live = c1 - c;
+        if (live >= 32) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (in) {
+                    tma_store_2d(tmOut, plane, f0, row);
+                    if constexpr (FORM != kGated) {
+                        constexpr int kSize = FORM == kGatedRows ? kPlaneBytes : kBytePlane;
+                        tma_store_2d(&x.tmKept, plane + kPlaneBytes, f0, row);
+                        tma_store_2d(&x.tmKept, plane + kPlaneBytes + kSize, x.features + f0, row);
+                    }
+                }
+                bulk_commit();
+            }
+            continue;
+        }
+        __syncwarp();
+        if (in) {
+            copy_plane(plane, static_cast<T*>(a.out) + row * a.ldo + f0, a.ldo, live, lane);
+            if constexpr (FORM == kGatedRows) {
+                T* gu = static_cast<T*>(x.gu) + row * x.ldgu + f0;
+                copy_plane(plane + kPlaneBytes, gu, x.ldgu, live, lane);
+                copy_plane(plane + 2 * kPlaneBytes, gu + x.features, x.ldgu, live, lane);
+            }
+            if constexpr (is_packed(FORM)) {
+                const uint4 g8 = ld_shared_v4(plane + kPlaneBytes + lane * 16);
+                const uint4 u8 = ld_shared_v4(plane + kPlaneBytes + kBytePlane + lane * 16);
+                if (lane < live) {
+                    int8_t* q = x.q + (row + lane) * x.ldq + f0;
+                    __stcs(reinterpret_cast<uint4*>(q), g8);
+                    __stcs(reinterpret_cast<uint4*>(q + x.features), u8);
+                }
+            }
+        }
+        if (lane == 0) bulk_commit();  // an empty group: one per use of a buffer
+        __syncwarp();
     }
+}
+
+// The scale bytes of the rows [c0, c1) that the four warps of a half of the columns have
+// put together, eight a row: a warp's quarter q of those rows, a row's four bytes of g
+// or u by neighbouring lanes.  (From each warp a byte per row, 32 sectors a store, and
+// each plane by itself: 143 us where this takes 115, 23670 rows, 2 x 1488 x 328.)
+__device__ __forceinline__ void store_scales(const Gate<kGatedPacked>& x, const Unit& w, int c0, int c1, int first,
+                                             int q, int lane, uint32_t scales) {
+    const int r0 = c0 + 32 * q, r1 = min(c1, r0 + 32), byte = lane & 7;
+    const int group = first + (byte & 3);  // of g
+    const int64_t column = byte < 4 ? group : x.features / gated::kGroup + group;
+    if (group >= x.features / gated::kGroup) return;
+    for (int r = r0 + (lane >> 3); r < r1; r += 4)
+        x.scale[(w.p0 + w.n0 + static_cast<int64_t>(r)) * x.lds + column] =
+            static_cast<uint8_t>(ld_shared_u8(scales + 8 * (r - c0) + byte));
 }
 
 // The sum of both halves' accumulators (t and t2) into the second, for this warp's
@@ -667,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto zeroed_bar = [&](int s) { return done_bar + 8u + 8u * (G::kStages + s); };
     auto unitf_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + i); };
     auto unite_bar = [&](int i) { return done_bar + 8u + 8u * (2 * G::kStages + kUnits + i); };
+    auto scale_bar = [&](int half) { return done_bar + 8u + 8u * (2 * G::kStages + 2 * kUnits + half); };
     Unit* ring = reinterpret_cast<Unit*>(smem + G::kUnitOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
@@ -687,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(unitf_bar(i), 1);
             mbar_init(unite_bar(i), kThreads / 32 - 1);  // every warp but the walking one
         }
+        for (int h = 0; h < 2; ++h) mbar_init(scale_bar(h), kEpiWarps / 2);
         mbar_init(done_bar, 1);
         fence_mbar_init();
     }
@@ -943,9 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stage = out0 + (warp - 4) * G::kOut;
         int acc = 0;
         int odd = 0;  // the staging buffers alternate across units too: only the newest store may be unread
-        uint32_t aph = 0;
+        uint32_t aph = 0, sph = 0;
         while (next_unit()) {
             const int row0 = w.m0 + 128 * rank + 32 * q;
+            const uint32_t scales = out0 + half * (kEpiWarps / 2) * G::kOut + kScalesAt + sph * kScaleBytes;  // 8 bits
             uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * TILE);
             if (w.steps > 0) {
                 if (!mbar_wait(accf_bar(acc), aph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
@@ -976,7 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (is_gated(FORM)) {
                 auto store = [&](auto type, auto act) {
                     using T = decltype(type);
-                    store_gated<T, decltype(act)::value, FORM>(a, gate, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
+                    store_gated<T, decltype(act)::value, FORM>(a, gate, &tmOut, w, t, c0, c1, row0, lane, stage, odd,
+                                                               scales + q);
                 };
                 auto typed = [&](auto act) {  // 8 bits: bf16 in one sum, fp16 in halves
                     if (FORM == kGatedPacked || (FORM != kGatedHalves && a.bf16))
@@ -1004,6 +1038,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (w.steps == 0) continue;
             give_back(HALVES ? 1 : acc);
+            if constexpr (is_packed(FORM)) {
+                if (c0 < c1) {  // alike in the four warps of a half
+                    if (lane == 0) mbar_arrive(scale_bar(half));
+                    __syncwarp();
+                    if (!mbar_wait(scale_bar(half), sph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) break;
+                    __syncwarp();
+                    store_scales(gate, w, c0, c1, (w.m0 + 128 * rank) / 32, q, lane, scales);
+                    sph ^= 1u;
+                }
+            }
             if (!HALVES) acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }

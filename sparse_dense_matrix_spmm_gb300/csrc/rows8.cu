@@ -27,7 +27,7 @@ struct Rows8Args {
     int64_t ldq;
     uint8_t* scale;
     int64_t lds;
-    int32_t tx;  // threads along a row, a power of two of at least 16; kThreads / tx rows per CTA
+    int32_t tx;  // threads along a row, a power of two; kThreads / tx rows per CTA
     bool wide;   // packing: integers leave 4 (fp32) or 8 at a time
 };
 
@@ -109,8 +109,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
             }
             memcpy(r[i], part, sizeof(r[i]));
         }
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
+        auto one = [&](int i) {
             uint32_t m = largest<T>(r[i]);
 #pragma unroll
             for (int d = 1; d < kGroup / V; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
             X::unpack(raw, f);
             uint32_t v[V];
             quantise(f, b, v);
-            if (at >= cols) continue;
+            if (at >= cols) return;
             if (a.wide && at + V <= cols) {
                 store_q<V>(q + at, v);
             } else {
@@ -131,6 +130,16 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
                     if (at + j < cols) q[at + j] = static_cast<int8_t>(v[j]);
             }
             if (at % kGroup == 0) scale[at / kGroup] = static_cast<uint8_t>(b);
+        };
+        if (P == V && c0 + (kVecs - 1) * step < a.cols) {  // all four vectors, without a test each
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) one(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                if (c0 + i * step >= a.cols) break;  // alike for all threads
+                one(i);
+            }
         }
     }
 }
@@ -177,9 +186,11 @@ bool moves(const spmm_rows8_t* P, int n) {
     return reinterpret_cast<uintptr_t>(P->q) % static_cast<unsigned>(n) == 0 && P->ldq % n == 0;
 }
 
-// `per`: values of a thread per turn.
-Rows8Args arguments(void* x, int64_t ldx, const spmm_rows8_t* P, int per, dim3& grid) {
-    Rows8Args a{x, ldx, P->rows, P->cols, P->q, P->ldq, P->scale, P->lds, 16, false};
+// `per`: values of a thread per turn; `least`: threads of a group.  No more threads to a row than
+// have work: short rows share a CTA (61657 x 87 bf16 to 8 bits: 24 us at 16 threads and
+// four vectors, 8 us so).
+Rows8Args arguments(void* x, int64_t ldx, const spmm_rows8_t* P, int per, int least, dim3& grid) {
+    Rows8Args a{x, ldx, P->rows, P->cols, P->q, P->ldq, P->scale, P->lds, least, false};
     while (a.tx < kThreads && a.tx * per < P->cols) a.tx *= 2;
     const int64_t rows = kThreads / a.tx;
     grid = dim3(static_cast<unsigned>((P->rows + rows - 1) / rows));
@@ -191,7 +202,7 @@ Rows8Args arguments(void* x, int64_t ldx, const spmm_rows8_t* P, int per, dim3& 
 spmm_status launch_pack_rows(const void* x, int64_t ldx, int32_t dtype, const spmm_rows8_t* P, cudaStream_t s) {
     const int es = row_elem_bytes(dtype), p = row_width({Operand{x, ldx, es}}, P->cols);
     dim3 grid;
-    Rows8Args a = arguments(const_cast<void*>(x), ldx, P, 4 * 16 / es, grid);
+    Rows8Args a = arguments(const_cast<void*>(x), ldx, P, 4 * 16 / es, es, grid);
     a.wide = moves(P, 16 / es);
     cudaError_t e;
     trace_begin(SPMM_KERNEL_ROWS8, s);
@@ -204,7 +215,7 @@ spmm_status launch_unpack_rows(const spmm_rows8_t* P, void* out, int64_t ldo, in
     int v = row_width({Operand{out, ldo, row_elem_bytes(dtype)}}, P->cols);
     while (v > 1 && !moves(P, v)) v /= 2;
     dim3 grid;
-    const Rows8Args a = arguments(out, ldo, P, v * (v >= 4 ? kFlight<4> : kFlight<1>), grid);
+    const Rows8Args a = arguments(out, ldo, P, v * (v >= 4 ? kFlight<4> : kFlight<1>), 1, grid);
     cudaError_t e;
     trace_begin(SPMM_KERNEL_ROWS8, s);
     SPMM_ROWS_TYPED(e, dtype, v, unpack_kernel, grid, kThreads, s, a);

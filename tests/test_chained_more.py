@@ -43,6 +43,3 @@ def test_gated_epilogue_reads_tmem_together():
         loop = body[body.index("for (int c = c0"):]
         assert re.search(_NEEDS, loop) and _unsafe(loop + loop, True) is None, head
     assert re.search(r"__syncwarp\(\);\s*tmem_st_wait\(\)", _body(code, r"void fold_halves\("))
-    assert _unsafe(_body(code, r"void store_plane\("), True) is None
-    for head in (r"void store_plane\(", r"void store_packed\("):
-        assert not re.search(r"\breturn\b[^;]*;\s*__syncwarp", _body(code, head))
