@@ -93,23 +93,28 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
     const int x = threadIdx.x % a.tx, step = a.tx * V;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / a.tx) + threadIdx.x / a.tx;
     const int64_t cols = row < a.rows ? a.cols : 0;
+    const bool all_rows = (static_cast<int64_t>(blockIdx.x) + 1) * (kThreads / a.tx) <= a.rows;
     const T* in = static_cast<const T*>(a.x) + row * a.ldx;
     int8_t* q = a.q + row * a.ldq;
     uint8_t* scale = a.scale + row * a.lds;
-    for (int64_t c0 = 0; c0 < a.cols; c0 += kVecs * step) {  // whole warps stay together for the shuffles
+    // Four vectors of each thread; `whole`: all of them lie in their rows.
+    auto turn = [&](int64_t c0, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
         const int64_t c = c0 + x * V;
-        uint32_t r[kVecs][4] = {};
+        uint32_t r[kVecs][4];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             typename Piece::Raw part[V / P];
 #pragma unroll
             for (int j = 0; j < V / P; ++j) {
                 const int64_t at = c + i * step + j * P;
-                part[j] = at < cols ? Piece::load(in + at) : Piece::zero();  // cols % P == 0
+                part[j] = kWhole || at < cols ? Piece::load(in + at) : Piece::zero();  // cols % P == 0
             }
             memcpy(r[i], part, sizeof(r[i]));
         }
-        auto one = [&](int i) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (!kWhole && c0 + i * step >= a.cols) break;  // alike for all threads
             uint32_t m = largest<T>(r[i]);
 #pragma unroll
             for (int d = 1; d < kGroup / V; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -121,26 +126,22 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
             X::unpack(raw, f);
             uint32_t v[V];
             quantise(f, b, v);
-            if (at >= cols) return;
-            if (a.wide && at + V <= cols) {
+            if (!kWhole && at >= cols) continue;
+            if (a.wide && (kWhole || at + V <= cols)) {
                 store_q<V>(q + at, v);
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (at + j < cols) q[at + j] = static_cast<int8_t>(v[j]);
+                    if (kWhole || at + j < cols) q[at + j] = static_cast<int8_t>(v[j]);
             }
             if (at % kGroup == 0) scale[at / kGroup] = static_cast<uint8_t>(b);
-        };
-        if (P == V && c0 + (kVecs - 1) * step < a.cols) {  // all four vectors, without a test each
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) one(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                if (c0 + i * step >= a.cols) break;  // alike for all threads
-                one(i);
-            }
         }
+    };
+    for (int64_t c0 = 0; c0 < a.cols; c0 += kVecs * step) {  // whole warps stay together for the shuffles
+        if (P == V && all_rows && c0 + kVecs * step <= a.cols)
+            turn(c0, std::true_type());
+        else
+            turn(c0, std::false_type());
     }
 }
 
