@@ -222,3 +222,31 @@ def test_no_tokens():
     assert h.shape == (0, 32) and gu.q.shape == (0, 64)
     dgu, dxs, dW = spmm.spmm_experts_gated_grad(R, h, xs, W, gu)
     assert dgu.shape == (0, 64) and dxs.shape == (0, 64) and not dW.any()
+
+
+@pytest.mark.parametrize("dtype,powers", [("bf16", (-100, -30, 0, 60, 119, 120, 121, 122, 126, 127)), ("f16", (-14, -7, 0, 3, 9, 15))])
+@pytest.mark.parametrize("n", [10, 80, 300])
+def test_packed_sums_exactly(dtype, powers, n):
+    """Sums that are exact (one product each): the kept integers are the definition's bit for bit, ties, sums next to the
+    largest fp32 and infinite ones among them, on CUDA cores and on the tensor cores."""
+    torch = need_gpu()
+    import sparse_dense_matrix_spmm_gb300 as spmm
+    from tests.gated_util import packed
+    rng = np.random.default_rng(n)
+    N, K = 80, 16
+    R = spmm.spmm_build_route(torch.zeros(n, dtype=torch.int64, device="cuda"), 1)
+    xs, W = torch.zeros(n, K, dtype=torch.float64), torch.zeros(1, 2 * N, K, dtype=torch.float64)
+    xs[:, 3] = torch.from_numpy(2.0 ** rng.choice(powers, n))
+    W[0, :, 3] = torch.from_numpy(rng.integers(-255, 256, 2 * N) * rng.choice([0.5, 0.25, 1.0], 2 * N))
+    W[0, 16:32] = 0
+    W[0, 48:64, 3] = torch.arange(16) + 0.5
+    W[0, 63, 3] = 127.0  # the unit is 1 at power 0: the others are ties
+    with np.errstate(over="ignore"):
+        g = (f64(xs) @ f64(W[0]).T).astype(np.float32).astype(np.float64)
+    xs, W = xs.to(DT[dtype]).cuda(), W.to(DT[dtype]).cuda()
+    q, scale = packed(g)
+    _, P = spmm.spmm_experts_gated(R, xs, W, save="packed")
+    assert np.array_equal(P.scale.cpu().numpy(), scale) and np.array_equal(P.q.cpu().numpy(), q)
+    if dtype == "bf16":
+        assert (scale == 255).any() and (scale == 248).any()
+    assert spmm.last_device_error() == 0
