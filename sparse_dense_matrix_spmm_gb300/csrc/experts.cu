@@ -25,11 +25,13 @@
 //   gated     [g u] = W[e] xs[p], h[p] = act(g) u     (W[e]: N gate rows, N up rows)
 // is the forward product with another order of the weights' rows and another
 // epilogue.  A tile's 128 rows are loaded as 16 gate rows, the 16 up rows of the same
-// features, the next 16 gate rows and so on (one 5-D TMA box), so that TMEM lanes 0-15 of a
-// warp's quarter hold g and lanes 16-31 hold u: the two 16-lane loads of the epilogue
-// leave g and u of one feature and row in the same thread, and neither shuffles nor
-// shared memory stand between the sums and act(g) u.  [g u] itself never leaves the SM
-// unless it is kept, rounded or as 8-bit integers whose groups of 16 are the warp's 16 features.
+// features, the next 16 gate rows and so on (one 5-D TMA box), so that TMEM lanes 0-15
+// of a warp's quarter hold g and lanes 16-31 hold u: the two 16-lane loads of the
+// epilogue leave g and u of one feature and row in the same thread, and neither
+// shuffles nor shared memory stand between the sums and act(g) u.  [g u] itself never
+// leaves the SM unless it is kept, rounded or as 8-bit integers whose groups of 16 are
+// the warp's 16 features.  It takes the time of the plain product of 2 N features (1818
+// TFLOP/s with 1024 rows per expert, 2 x 2048 x 4096).
 //
 // Roles per CTA: warps 0, 1, 12 and 13 load A and B (TMA, 128-byte swizzle, one
 // ring of stages of 64 depth), one thread of warp 2 issues the MMAs, warps 4-11
@@ -59,11 +61,11 @@ using namespace ptx;
 // depth are summed in accumulators of their own and added in fp32: 3.2e-4.  Both
 // accumulators then belong to one unit.  The epilogue first folds them, the sum into
 // the second one, and gives the first back, so that the next unit's first half runs
-// beside the rest of it: 320 us against 305 with one sum (306 with the epilogue as it is).  Without the fold 372-418
-// us; three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns
-// takes nearly the time of one of 256).
-// Beside these, dw in parts: an expert's rows in several units, whose fp32 sums a second
-// kernel joins.
+// beside the rest of it: 5% over one sum (320 us, 305).  Without the fold 372-418 us;
+// three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns takes
+// nearly the time of one of 256).
+// Beside these, dw in parts: an expert's rows in several units, whose fp32 sums a
+// second kernel joins.
 enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3, kGatedHalves = 4, kDwParts = 5 };
 __host__ __device__ constexpr bool is_gated(int form) { return form >= kGated && form <= kGatedHalves; }
 __host__ __device__ constexpr bool is_packed(int form) { return form == kGatedPacked || form == kGatedHalves; }
@@ -92,10 +94,11 @@ constexpr uint64_t wait_limit_ns(int64_t most_depth) {
 // instead of six (64 tokens x 8 of 128 experts, 1536 x 4096: 226 us against 240).
 constexpr int kFewRows = 16;
 constexpr int kVecMost = 16;   // rows in all up to which the forward product runs on CUDA cores
-// .. and, for the gated block, where there are no more rows than experts, so that few
-// share one.  CUDA cores against this kernel, us: 32 rows, 32 experts, 2 x 1024 x 4096 55 / 66;
-// 64 rows, 64 experts, 2 x 768 x 2048 42 / 47; 64 of 256, 2 x 512 x 2048 37 / 41; 64 of 128,
-// 2 x 1280 x 4096 157 / 157; with more rows than experts (48, 32) 72 / 69, (48, 16) 55 / 45.
+// .. and, for the gated block, up to this many where there are no more rows than
+// experts, so that few share one.  CUDA cores against this kernel, us: 32 rows, 32
+// experts, 2 x 1024 x 4096 55 / 66; 64 rows, 64 experts, 2 x 768 x 2048 42 / 47; 64 of
+// 256, 2 x 512 x 2048 37 / 41; 64 of 128, 2 x 1280 x 4096 157 / 157; with more rows
+// than experts (48 of 32) 72 / 69, (48 of 16) 55 / 45.
 constexpr int kVecSpread = 64;
 constexpr int kDwFewRows = 4;  // rows per expert up to which dw runs on CUDA cores
 
@@ -216,10 +219,10 @@ struct Walk {
             w.p0 = a.offsets[e];
             w.cnt = a.offsets[e + 1] - w.p0;
             if (parts > 1) {
-                const int size = (w.cnt + parts * kDepth - 1) / (parts * kDepth) * kDepth;
-                const int skip = min(part * size, w.cnt);
-                w.p0 += skip;
-                w.cnt = min(size, w.cnt - skip);
+                const int64_t size = (static_cast<int64_t>(w.cnt) + parts * kDepth - 1) / (parts * kDepth) * kDepth;
+                const int64_t skip = min(part * size, static_cast<int64_t>(w.cnt));
+                w.p0 += static_cast<int>(skip);
+                w.cnt = static_cast<int>(min(size, w.cnt - skip));
             }
             w.m0 = mt * 128 * CG;
             w.n0 = nt * TILE;
@@ -257,7 +260,7 @@ struct Walk {
 
 // Shared memory: the ring of stages, as deep as fits, two staging buffers per
 // epilogue warp (32 x 32 results of a row product, 32 x 64 of dw; the gated block uses
-// the same bytes as four planes of 32 x 16), barriers, units.
+// the same bytes as kChunkBytes says), barriers, units.
 template <int CG, int TILE, bool DW>
 struct Ring {
     static constexpr int kBBytes = TILE / CG * 128;

@@ -17,9 +17,9 @@ using namespace gated;
 // row, with up to four rows of an expert, and has both sums in every lane at the
 // end.  Where [g u] is kept in 8 bits a CTA's 16 warps are a group of 16 features
 // and meet in shared memory; else 8 warps that do not wait for one another.  One
-// token with 2 of 8 experts (2 x 2048 x 4096, 67 MB) 13.0 us, with 8 of 64 (2 x 768 x 2048,
-// 50 MB) 10.7 us, with 8 of 128 (2 x 1280 x 4096, 168 MB) 28 us: launch, ramp and the
-// chain of offsets, weights and shuffles, then HBM.
+// token with 2 of 8 experts (2 x 2048 x 4096, 67 MB) 13.0 us, with 8 of 64 (2 x 768 x
+// 2048, 50 MB) 10.7 us, with 8 of 128 (2 x 1280 x 4096, 168 MB) 28 us: launch, ramp
+// and the chain of offsets, weights and shuffles, then HBM.
 constexpr int kVecRows = 4;
 
 struct VecArgs {
@@ -157,8 +157,9 @@ __global__ void __launch_bounds__(kVecWarps<PACKED> * 32, 32 / kVecWarps<PACKED>
 }
 
 // ---------------------------------------------------------------- gradient of the activation
-// Bound by HBM: a thread takes 8 features of a place, reads dh, g and u and writes
-// both gradients (and h).
+// A thread takes 8 features of a place, reads dh, g and u and writes both gradients (and
+// h).  From rows bound by HBM (16372 x 1280 bf16, silu, 210 MB: 31 us), from 8 bits by
+// instructions (170 MB: 31 us; tanh form, fp16, 16382 x 1792: 44 and 46-50 us).
 constexpr int kGradThreads = 256;
 
 struct GradArgs {
