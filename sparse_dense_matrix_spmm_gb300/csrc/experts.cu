@@ -101,14 +101,6 @@ constexpr int kVecMost = 16;   // rows in all up to which the forward product ru
 // than experts (48 of 32) 72 / 69, (48 of 16) 55 / 45.
 constexpr int kVecSpread = 64;
 constexpr int kDwFewRows = 4;  // rows per expert up to which dw runs on CUDA cores
-// Above this many rows per expert, and where dW's rows lie on 32 bytes, dw is stored by the
-// epilogue's threads (store_wide) instead of by TMA, whose engine the loads then have to
-// themselves.  us, threads / TMA: 16 experts of 2560 x 3584 with 512 rows each 120-127 /
-// 117-122, 768 rows 149-151 / 158-162, 1024 rows 173-179 / 189-204, 2048 rows 313-323 /
-// 328-333; 8 of 3584 x 4096 with 1024 rows 144 / 162-165.  With fewer rows the stores set
-// the pace, and TMA writes the faster.  In pieces of 16 bytes, half a sector, 224 us with
-// 1024 rows.
-constexpr int kDwWideRows = 512;
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -119,7 +111,6 @@ struct ExpertArgs {
     void* out;
     int64_t ldo, lde;
     int32_t bf16;
-    int32_t wide;  // dw: store_wide instead of store_dw
     int* err;
     uint64_t timeout_ns;
 };
@@ -604,40 +595,6 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& a, const CUtensorMap*
     }
 }
 
-// dw where dW's rows lie on 32 bytes and the depth is long: a lane's row by 32 bytes.
-template <typename T>
-__device__ __forceinline__ void store_wide(const ExpertArgs& a, const Unit& w, uint32_t t, int c0, int c1, int row0,
-                                           int lane) {
-    T* out = static_cast<T*>(a.out) + w.e * a.lde + (row0 + lane) * a.ldo + w.n0;
-    for (int c = c0; c < c1; c += 64) {
-        uint32_t v[4][16];
-        __syncwarp();  // as in store_rows
-        if (w.steps == 0) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[h][i] = 0u;
-        } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) tmem_ld16(t + c + 16 * h, v[h]);
-            tmem_ld_wait();
-        }
-        if (row0 + lane < a.m) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t p[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = pack2<T>(v[h][2 * i], v[h][2 * i + 1]);
-                const int k = c + 16 * h;
-                if (k + 16 <= c1)
-                    st_global_v8(out + k, p);
-                else if (k < c1)  // K % 8 == 0: 8 columns are left
-                    *reinterpret_cast<uint4*>(out + k) = make_uint4(p[0], p[1], p[2], p[3]);
-            }
-        }
-    }
-}
-
 // dw in parts: fp32 sums as they are, a lane's row by 16 bytes.
 __device__ __forceinline__ void store_part(const ExpertArgs& a, float* sums, const Unit& w, uint32_t t, int c0, int c1,
                                            int row0, int lane) {
@@ -1073,11 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if constexpr (FORM == kDwParts) {
                 store_part(a, gate.sums, w, t, c0, c1, row0, lane);
             } else if (DW) {
-                if (a.wide && a.bf16)
-                    store_wide<__nv_bfloat16>(a, w, t, c0, c1, row0, lane);
-                else if (a.wide)
-                    store_wide<__half>(a, w, t, c0, c1, row0, lane);
-                else if (a.bf16)
+                if (a.bf16)
                     store_dw<__nv_bfloat16>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
                 else
                     store_dw<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
@@ -1465,8 +1418,6 @@ spmm_status launch_experts_dw(const spmm_route_t* R, const void* dys, int64_t ld
     a.ldo = ldw;
     a.lde = lde;
     a.bf16 = dtype == SPMM_BF16;
-    a.wide = n > a.E * static_cast<int64_t>(kDwWideRows) &&
-             (reinterpret_cast<uintptr_t>(dW) | static_cast<uintptr_t>(ldw * 2) | static_cast<uintptr_t>(lde * 2)) % 32 == 0;
     a.err = dev->err;
     a.timeout_ns = wait_limit_ns(n);
     const bool pair = a.m > 128;
