@@ -1175,13 +1175,13 @@ __global__ void __launch_bounds__(kVecWarps * 32, 4) experts_vec_kernel(const Ve
 }
 
 // dw of few rows per expert is a write: E N K values from a handful of rows. The
-// kernel above stores tiles at 4.8 TB/s at best (an SM's loads and stores cost
-// nearly their sum: 185 us with 64 rows per expert, 122 us for the same stores
-// alone); here short-lived CTAs write the gradient in address order, 8 of its
-// rows at a time, from sums on CUDA cores (two products per instruction).
-// Measured (64 experts, 1536 x 4096, 805 MB): 107 us with a row per expert
-// (7.5 TB/s) against 139 us, 134 us against 154 us with four, 184 us against
-// 167 us with eight, hence the limit of four per expert on average.
+// kernel above stores tiles at 7.0 TB/s at best (152 us with 64 rows per expert);
+// here short-lived CTAs write the gradient in address order, 8 of its rows at a
+// time, from sums on CUDA cores (two products per instruction).  Measured (64
+// experts, 1536 x 4096, 805 MB): 107 us with a row per expert (7.5 TB/s) against
+// 116 us, 113 us against 128 us with four, 141 us against 129 us with five, 169 us
+// against 134 us with eight; 128 experts, 768 x 2048: 55 / 61, 62 / 67, 77 / 68 and
+// 94 / 70 us.  Hence the limit of four per expert on average.
 struct DwArgs {
     const int32_t* offsets;
     const void *dys, *xs;
@@ -1377,8 +1377,8 @@ spmm_status launch_experts_rows(const spmm_route_t* R, const void* rows, int64_t
 // into as many parts as fill the CTA pairs once, of 256 rows or more on average, where
 // experts have 4096 rows or more on average: the join and the fp32 stores cost 6-8 us, a
 // step of 64 rows 0.28.  The whole way back of 65536 rows over 2 experts, 2 x 128 x 256:
-// 61 us in 38 parts, 172 us in one; 32768 over 2, 2 x 256 x 512: 63 us in 9, 107 in one; 4096
-// over 2, 2 x 128 x 256: 24 us in 8, 25 in one; 16384 over 8, 2 x 256 x 512: 40 us in 2, 36
+// 59 us in 38 parts, 167 us in one; 32768 over 2, 2 x 256 x 512: 61 us in 9, 103 in one; 4096
+// over 2, 2 x 128 x 256: 24 us in 8, 25 in one; 16384 over 8, 2 x 256 x 512: 40 us in 2, 35
 // in one.  By sizes alone, so that the bits do not depend on how the ids are spread.
 int experts_dw_parts(int64_t n, int64_t E, int64_t N, int64_t K) {
     constexpr int64_t kSms = 152, kLeast = 256, kLong = 4096;
