@@ -158,8 +158,10 @@ __global__ void __launch_bounds__(kVecWarps<PACKED> * 32, 32 / kVecWarps<PACKED>
 
 // ---------------------------------------------------------------- gradient of the activation
 // A thread takes 8 features of a place, reads dh, g and u and writes both gradients (and
-// h).  From rows bound by HBM (16372 x 1280 bf16, silu, 210 MB: 31 us), from 8 bits by
-// instructions (170 MB: 31 us; tanh form, fp16, 16382 x 1792: 44 and 46-50 us).
+// h).  Bound by HBM from rows (16372 x 1280 bf16, 210 MB: 31 us; 16382 x 1792, 294 MB: 43
+// us) and, but for gelu, from 8 bits (silu 170 MB: 26 us, 238 MB: 35 us; tanh form 28 and
+// 38 us, gelu 30 and 41 us, by instructions).  A thread's row by one multiplication:
+// with divisions 26.6, 36, 28.2, 38.4, 31.3 and 43 us from 8 bits.
 constexpr int kGradThreads = 256;
 
 struct GradArgs {
@@ -167,6 +169,7 @@ struct GradArgs {
     int32_t E;
     int64_t R;
     int32_t N;
+    uint64_t per_row;  // 2^64 over the threads of a row, rounded up
     const void* dh;
     int64_t lddh;
     const void* gu;
@@ -196,12 +199,10 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GradArgs
     using V = Vec<T, 8>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const uint32_t per = static_cast<uint32_t>(a.N) / 8;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGradThreads;
-    const int64_t row0 = first / per;
-    const uint32_t rest = static_cast<uint32_t>(first - row0 * per) + threadIdx.x, down = rest / per;
-    const int64_t p = row0 + down;
-    const int c = static_cast<int>(rest - down * per) * 8;
+    // exact while threads x threads of a row stay below 2^64: dgu, 32 bytes a thread, is far smaller
+    const uint64_t thread = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+    const int64_t p = static_cast<int64_t>(__umul64hi(thread, a.per_row));
+    const int c = (static_cast<int>(thread) - static_cast<int>(p) * (a.N / 8)) * 8;
     if (p >= a.R) return;
     const typename V::Raw rd = V::load(static_cast<const T*>(a.dh) + p * a.lddh + c);
     typename V::Raw rg, ru;
@@ -292,6 +293,7 @@ spmm_status launch_gated_grad(const spmm_route_t* R, const void* dh, int64_t ldd
     a.E = static_cast<int32_t>(R->n_keys);
     a.R = R->T * R->k;
     a.N = static_cast<int32_t>(N);
+    a.per_row = UINT64_MAX / static_cast<uint64_t>(N / 8) + 1;  // N % 16 == 0
     a.dh = dh;
     a.lddh = lddh;
     a.gu = gu;
