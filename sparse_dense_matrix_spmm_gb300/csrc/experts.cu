@@ -63,13 +63,17 @@ using namespace ptx;
 // the second one, and gives the first back, so that the next unit's first half runs
 // beside the rest of it: 5% over one sum (320 us, 305).  Without the fold 372-418 us;
 // three accumulators of 160 columns in turn 415-439 us (an MMA of 160 columns takes
-// nearly the time of one of 256).
+// nearly the time of one of 256).  A depth of one step has one half: its accumulators
+// alternate from unit to unit as in the other forms.  (It must not be copied into the
+// second one: nothing would hold the next unit's fold back while this unit's sums are
+// still read there, by the other warp of a quarter, as the warps' columns differ from unit
+// to unit.)
 // Beside these, dw in parts: an expert's rows in several units, whose fp32 sums a
 // second kernel joins.
 enum : int { kPlain = 0, kGated = 1, kGatedRows = 2, kGatedPacked = 3, kGatedHalves = 4, kDwParts = 5 };
 __host__ __device__ constexpr bool is_gated(int form) { return form >= kGated && form <= kGatedHalves; }
 __host__ __device__ constexpr bool is_packed(int form) { return form == kGatedPacked || form == kGatedHalves; }
-// The step at which the second half begins; there is one if that is below the steps.
+// The step at which the second half begins, with two steps or more.
 __host__ __device__ constexpr int second_half(int steps) { return (steps + 1) / 2; }
 
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half of the columns each
@@ -515,25 +519,21 @@ __device__ __forceinline__ void store_scales(const Gate<kGatedPacked>& x, const 
 }
 
 // The sum of both halves' accumulators (t and t2) into the second, for this warp's
-// lanes and columns [c0, c1); one half alone is copied.
-__device__ __forceinline__ void fold_halves(uint32_t t, uint32_t t2, int c0, int c1, bool both) {
+// lanes and columns [c0, c1).
+__device__ __forceinline__ void fold_halves(uint32_t t, uint32_t t2, int c0, int c1) {
     for (int c = c0; c < c1; c += 32) {
         uint32_t a[2][16], b[2][16];
         __syncwarp();  // as in store_rows
         tmem_ld16(t + c, a[0]);
         tmem_ld16(t + c + 16, a[1]);
-        if (both) {
-            tmem_ld16(t2 + c, b[0]);
-            tmem_ld16(t2 + c + 16, b[1]);
-        }
+        tmem_ld16(t2 + c, b[0]);
+        tmem_ld16(t2 + c + 16, b[1]);
         tmem_ld_wait();
-        if (both) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    a[h][i] = __float_as_uint(__uint_as_float(a[h][i]) + __uint_as_float(b[h][i]));
-        }
+            for (int i = 0; i < 16; ++i)
+                a[h][i] = __float_as_uint(__uint_as_float(a[h][i]) + __uint_as_float(b[h][i]));
         tmem_st16(t2 + c, a[0]);
         tmem_st16(t2 + c + 16, a[1]);
     }
@@ -683,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmOut, const ExpertArgs a,
                    const __grid_constant__ Gate<FORM> gate) {
     constexpr bool DW = BMN, HALVES = FORM == kGatedHalves;
+    const bool halves = HALVES && a.depth > kDepth;  // both accumulators belong to one unit
     using G = Ring<CG, TILE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // whole stages; the loop stays warp-uniform around the one issuing thread, which keeps the
             // descriptors in uniform registers
             const int whole = DW ? w.cnt / kDepth : w.steps;
-            const int half = HALVES ? second_half(w.steps) : -1;
+            const int half = halves ? second_half(w.steps) : -1;
             bool ready = whole > 0 && mbar_test_wait(full_bar(s), ph);
             for (int k = 0; k < whole; ++k) {
                 if (!ready && !mbar_wait(full_bar(s), ph, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT)) {
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) commit<CG>(accf_bar(acc));
             __syncwarp();
-            if (!HALVES) acc ^= 1;
+            if (!halves) acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
         if (lane == 0) commit<CG>(done_bar);
@@ -1004,9 +1005,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             if constexpr (HALVES) {
-                fold_halves(t, t + TILE, c0, c1, second_half(w.steps) < w.steps);
-                give_back(0);
-                t += TILE;
+                if (halves) {
+                    fold_halves(t, t + TILE, c0, c1);
+                    give_back(0);
+                    t += TILE;
+                }
             }
             if constexpr (is_gated(FORM)) {
                 auto store = [&](auto type, auto act) {
@@ -1039,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_rows<__half>(a, &tmOut, w, t, c0, c1, row0, lane, stage, odd);
             }
             if (w.steps == 0) continue;
-            give_back(HALVES ? 1 : acc);
+            give_back(halves ? 1 : acc);
             if constexpr (is_packed(FORM)) {
                 if (c0 < c1) {  // alike in the four warps of a half
                     if (lane == 0) mbar_arrive(scale_bar(half));
@@ -1050,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sph ^= 1u;
                 }
             }
-            if (!HALVES) acc ^= 1;
+            if (!halves) acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
         if (lane == 0) bulk_wait<0>();  // this warp's stores have completed
