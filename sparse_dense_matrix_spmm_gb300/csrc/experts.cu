@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (rank == 0)
                         mbar_arrive(acce_bar(b));
                     else
-                        mbar_arrive_remote(map_shared(acce_bar(b), 0));
+                        mbar_hand_back_remote(map_shared(acce_bar(b), 0));
                 }
                 __syncwarp();
             };

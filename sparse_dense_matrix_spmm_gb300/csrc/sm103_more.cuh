@@ -133,18 +133,22 @@ __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive on a barrier of another CTA (address from map_shared).  Released at the scope of
-// this CTA, because what arrivals here hand over lies in it: TMEM that has been read, shared
-// memory cleared and fenced for the async proxy, which a pair's MMA reads where it lies.
-// Not for data that threads of the other CTA read.  A release at cluster scope waits for
-// memory operations of the whole SM: it cost the weight gradient of the experts 0.5 us per
-// unit of work (16 experts of 2560 x 3584, 600 rows each: 166 us against 136, 512 rows 122
-// against 107).
+// Arrive on a barrier of another CTA (address from map_shared).  Released at the scope of the
+// cluster, which holds the thread that waits (mbar_wait_cluster): what was written before, shared
+// memory cleared and fenced for the async proxy among it, comes before what follows the wait.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// mbar_wait for a phase completed by threads of the other CTA: the waiting
-// thread sees their writes (acquire at cluster scope).
+// The same for an accumulator that has been read: it hands over no memory, only the turn, between
+// the fences of tcgen05 on both sides (tcgen05.wait::ld and fence::before_thread_sync here,
+// fence::after_thread_sync there).  A release waits for memory operations of the whole SM, the
+// results' stores among them, once per unit of work: the weight gradient of 16 experts of 2560 x
+// 3584 with 512 rows each took 122 us with it.
+__device__ __forceinline__ void mbar_hand_back_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait for a phase completed by threads of the other CTA: acquired at cluster
+// scope, so the waiting thread sees what an mbar_arrive_remote released.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t timeout_ns, int* err,
                                                   int code) {
     uint64_t t0 = 0;
