@@ -202,7 +202,9 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GradArgs
     // exact while threads x threads of a row stay below 2^64: dgu, 32 bytes a thread, is far smaller
     const uint64_t thread = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
     const int64_t p = static_cast<int64_t>(__umul64hi(thread, a.per_row));
-    const int c = (static_cast<int>(thread) - static_cast<int>(p) * (a.N / 8)) * 8;
+    // modulo 2^32, which the place in a row lies below: rows x features may be more
+    const uint32_t before = static_cast<uint32_t>(p) * static_cast<uint32_t>(a.N / 8);
+    const int c = static_cast<int>(static_cast<uint32_t>(thread) - before) * 8;
     if (p >= a.R) return;
     const typename V::Raw rd = V::load(static_cast<const T*>(a.dh) + p * a.lddh + c);
     typename V::Raw rg, ru;
