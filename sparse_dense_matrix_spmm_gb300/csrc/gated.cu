@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GradArgs
     using V = Vec<T, 8>;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    // exact while threads x threads of a row stay below 2^64: dgu, 32 bytes a thread, is far smaller
+    // exact while threads x threads of a row stay below 2^64 (the launcher refuses more)
     const uint64_t thread = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
     const int64_t p = static_cast<int64_t>(__umul64hi(thread, a.per_row));
     // modulo 2^32, which the place in a row lies below: rows x features may be more
@@ -311,7 +311,8 @@ spmm_status launch_gated_grad(const spmm_route_t* R, const void* dh, int64_t ldd
     a.h = h;
     a.ldh = ldh;
     const int64_t blocks = (a.R * (N / 8) + kGradThreads - 1) / kGradThreads;
-    if (blocks >= int64_t(1) << 31) return SPMM_ERR_UNSUPPORTED;
+    if (blocks >= int64_t(1) << 31 || static_cast<uint64_t>(blocks) * kGradThreads > UINT64_MAX / static_cast<uint64_t>(N / 8))
+        return SPMM_ERR_UNSUPPORTED;  // 8 TB of dgu and more
     cudaError_t e;
     trace_begin(SPMM_KERNEL_GATED_GRAD, s);
     if (dtype == SPMM_BF16)
