@@ -222,7 +222,10 @@ typedef struct {
  * smallest with e in [-126, 121] for which all of them round to integers of at
  * most 127 in magnitude; x is held as q 2^e, q = x 2^-e rounded half to even (at e =
  * 121, next to the largest fp32, cut off at 127).  The error is at most 2^(e - 1), and
- * q 2^e is exact in bf16 and fp32 (fp16 rounds it where it leaves fp16's range).
+ * q 2^e is exact in bf16 and fp32.  Read back as fp16 it is rounded below fp16's normal
+ * range; 65536, as which the largest fp16 values are held, reads as 65504, so that finite
+ * fp16 values stay finite, and what is larger (from fp32, or the sums of a gated block)
+ * becomes infinity.
  *   q[rows][ldq]      the integers
  *   scale[rows][lds]  e + 127 per group; 255: the group held an infinity or a NaN
  *                     (q = 0) and reads back as NaN

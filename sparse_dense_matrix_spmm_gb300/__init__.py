@@ -950,7 +950,8 @@ def spmm_pack_rows(x: torch.Tensor, out: Optional[Rows8] = None, stream=None) ->
 
 
 def spmm_unpack_rows(P: Rows8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The rows that P holds, of P.dtype (or of out's type)."""
+    """The rows that P holds, of P.dtype (or of out's type).  fp16: 65536, as which the largest
+    values are held, reads as 65504; larger ones become infinity."""
     dev = P.device
     if out is None:
         out, ldo = _empty(P.q, (P.rows, P.cols), P.dtype, stream), P.cols

@@ -145,9 +145,15 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Rows8Args a) {
     }
 }
 
+// fp16: 65536, as which its largest values are held (65024 and more beside one of 65280
+// or more), reads back as 65504; what is larger was no fp16 value and becomes infinity.  No
+// other multiple of a unit lies between the two.
+constexpr uint32_t kHalfTop = 127 + 10;  // scale bytes below have less
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const Rows8Args a) {
     using X = Vec<T, V>;
+    constexpr bool kHalf = std::is_same<T, __half>::value;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int x = threadIdx.x % a.tx, step = a.tx * V;
@@ -177,6 +183,11 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const Rows8Args a) {
             float f[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) f[j] = byte_of(w[j >> 2] ^ 0x80808080u, j & 3) * unit;
+            if (kHalf && b[i] >= kHalfTop) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (fabsf(f[j]) == 65536.f) f[j] = copysignf(65504.f, f[j]);
+            }
             X::store(out + at, X::pack(f));
         }
     }
