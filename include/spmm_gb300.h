@@ -636,7 +636,9 @@ SPMM_API spmm_status spmm_unpack_rows(const spmm_rows8_t *P, void *out, int64_t 
  * rounded once.  A training step keeps [g u] for the way back: rounded to the rows'
  * type in gu (T k x 2 N, row pitch ldgu; null: not kept), or in 8 bits straight
  * from the sums in *packed (rows = T k, cols = 2 N; null: not kept); not both.  Rows
- * past the kept places are written as zeros (scale 1).  Types, alignment and limits
+ * past the kept places are written as zeros (scale 1).  h has the same bits whatever is
+ * kept, but for fp16 with *packed: there the depth may be summed in two halves, so that
+ * h can differ from the other forms' in its last bits.  Types, alignment and limits
  * as for spmm_experts with 2 N features; N % 16 == 0; packed->q 16-byte aligned,
  * packed->ldq % 16 == 0. */
 SPMM_API spmm_status spmm_experts_gated(const spmm_route_t *R, const void *xs, int64_t ldx, const void *W,

@@ -967,7 +967,9 @@ def spmm_experts_gated(R: Route, xs: torch.Tensor, W: torch.Tensor, act: str = "
     K, the gate's N rows before the up projection's; act is silu, gelu or gelu_tanh;
     zero rows past the kept places.  bf16 or fp16, N a multiple of 16.  A training step
     keeps [g u] (T k x 2N) for spmm_experts_gated_grad: save="rows" returns (h, gu)
-    with gu of xs's type, save="packed" (h, Rows8) with gu in 8 bits."""
+    with gu of xs's type, save="packed" (h, Rows8) with gu in 8 bits.  h has the same bits
+    whatever is saved, but for fp16 with save="packed", whose last bits can differ (the
+    depth is summed in two halves)."""
     dev, dt, rows = R.device, xs.dtype, R.n_rows
     N, K = W.shape[-2] // 2, W.shape[-1]
     code, ldx, actc = _row_code(dt), _rows(xs, "xs", rows, K, dt, dev), _act(act)
