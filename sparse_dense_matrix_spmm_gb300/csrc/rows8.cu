@@ -36,14 +36,11 @@ using Bytes = typename Word<(V < 2 ? 2 : V)>::type;  // V integers as they move 
 
 template <int V>
 __device__ __forceinline__ void store_q(int8_t* p, const uint32_t (&q)[V]) {
+    static_assert(V == 8 || V == 4, "16 bytes of a row");
     if constexpr (V == 8)
         *reinterpret_cast<uint2*>(p) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
-    else if constexpr (V == 4)
-        *reinterpret_cast<uint32_t*>(p) = pack4(q[0], q[1], q[2], q[3]);
-    else if constexpr (V == 2)
-        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(pack4(q[0], q[1], 0u, 0u));
     else
-        *p = static_cast<int8_t>(q[0]);
+        *reinterpret_cast<uint32_t*>(p) = pack4(q[0], q[1], q[2], q[3]);
 }
 template <int V>
 __device__ __forceinline__ Bytes<V> load_q(const int8_t* p) {
