@@ -102,7 +102,10 @@ constexpr int kVecMost = 16;   // rows in all up to which the forward product ru
 // experts, so that few share one.  CUDA cores against this kernel, us: 32 rows, 32
 // experts, 2 x 1024 x 4096 55 / 66; 64 rows, 64 experts, 2 x 768 x 2048 42 / 47; 64 of
 // 256, 2 x 512 x 2048 37 / 41; 64 of 128, 2 x 1280 x 4096 157 / 157; with more rows
-// than experts (48 of 32) 72 / 69, (48 of 16) 55 / 45.
+// than experts (48 of 32) 72 / 69, (48 of 16) 55 / 45.  The rule goes by the sizes that
+// the host knows, for ids that are spread: 64 rows of one expert of 64 read its weights sixteen times,
+// 27 us against 11.5 (2 x 768 x 2048), 68 against 19 (2 x 1280 x 4096), where rows of
+// 64 experts take 60 and 206.
 constexpr int kVecSpread = 64;
 constexpr int kDwFewRows = 4;  // rows per expert up to which dw runs on CUDA cores
 

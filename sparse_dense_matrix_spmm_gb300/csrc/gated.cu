@@ -1,5 +1,5 @@
-// gated.cu -- the experts' gated block on CUDA cores (a token or two), and the
-// gradient of its activation.
+// gated.cu -- the experts' gated block on CUDA cores (up to 16 rows in all, or 64
+// spread over as many experts), and the gradient of its activation.
 //   forward   [g u] = W[e] xs[p],  h[p] = act(g) u
 //   gradient  dgu[p] = [dh u act'(g), dh act(g)]
 #include "gated.cuh"
