@@ -931,7 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(done_bar, 0, a.timeout_ns, a.err, SPMM_DEVERR_TIMEOUT);
     } else if (warp == 2) {
         // ------------------------------------------------ rank 1 of a pair: dw clears its own tails.
-        // Tails of short units may be in flight together, so each slot has its own barriers.
+        // Tails of short units may be in flight together, so each slot has its own barriers.  The release
+        // that hands the zeros to rank 0's MMA waits for the SM's memory operations (16 experts of 2560 x
+        // 3584: 600 rows each 143-152 us, 608, without tails, 116 us).
         int s = 0;
         uint32_t ph = 0;
         while (next_unit()) {

@@ -143,7 +143,7 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
 // the fences of tcgen05 on both sides (tcgen05.wait::ld and fence::before_thread_sync here,
 // fence::after_thread_sync there).  A release waits for memory operations of the whole SM, the
 // results' stores among them, once per unit of work: the weight gradient of 16 experts of 2560 x
-// 3584 with 512 rows each took 122 us with it.
+// 3584 with 512 rows each took 122 us with it, 98 us so.
 __device__ __forceinline__ void mbar_hand_back_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
